@@ -31,7 +31,8 @@
  *     streams and allocates no memory; the only device memory it holds is
  *     scratch for two paths (serq_linear's K split, chunked activation
  *     quantization) in file-scope device arrays, described at those calls:
- *     calls that take them must not overlap on one device.
+ *     calls that take them must not overlap on one device. The attention
+ *     calls take a workspace from the caller instead.
  *   - Argument errors are detected on the host and returned before anything
  *     is launched; the output buffers are then untouched.
  *   - Online calls only enqueue work on `stream` (a hipStream_t; NULL is the
@@ -453,6 +454,181 @@ int serq_linear_mx(const uint8_t* Xq, const uint8_t* Xsc,
                    void* Y, serq_dtype y_dtype,
                    float* acc_main_dbg, float* acc_res_dbg,
                    void* stream);
+
+/*
+ * The attention half of a decoder layer, between the q/k/v linear and the
+ * output linear: rotating and storing keys, causal attention of new tokens,
+ * and single-token attention of a batch that may share a prefix.
+ *
+ * The paged cache. Keys and values of all sequences live in two device
+ * buffers of n_pages pages each, a page holding page_size tokens of every
+ * key/value head:
+ *     Kc[page][kv head][token in page][D],  Vc likewise,
+ * of one dtype (the calls' `dtype`: SERQ_F32 or SERQ_BF16). page_size is a
+ * power of two from 16 to 1024. A slot is page * page_size + token in page.
+ * A sequence is a row of page ids in order: its token t lies in page
+ * row[t / page_size] at t % page_size. What lies in a page past a sequence's
+ * length is never used (it may hold NaN). Page ids outside [0, n_pages) read
+ * some page inside the cache: wrong values, no access outside.
+ *
+ * Heads. Hq query heads share Hkv key/value heads (Hq a multiple of Hkv);
+ * query head h reads key/value head h / (Hq / Hkv). D is 64 or 128 (others
+ * SERQ_EUNSUPPORTED). Bounds: 16384 heads, rows * Hq and the keys of a
+ * sequence at most 2^30, n_pages * page_size below 2^31.
+ */
+
+typedef enum { SERQ_ROPE_HALF = 0, SERQ_ROPE_INTERLEAVED = 1 } serq_rope_layout;
+typedef enum {
+  SERQ_ROPE_PLAIN = 0,  /* f_i                                              */
+  SERQ_ROPE_LINEAR = 1, /* f_i / factor: positions interpolated             */
+  SERQ_ROPE_BASE = 2,   /* theta * factor^(rot / (rot - 2)) in place of theta */
+  SERQ_ROPE_BANDS = 3   /* low frequencies interpolated, high ones kept     */
+} serq_rope_scaling;
+
+/*
+ * serq_rope_table -- offline, host memory, synchronous.
+ *
+ * Cosines and sines of the rotary position embedding (Su et al. 2021): for
+ * position p and pair i < rot_dim / 2 the angle p * f_i, f_i =
+ * theta^(-2 i / rot_dim), in double, rounded once. For contexts longer than
+ * the trained one the frequencies are scaled: SERQ_ROPE_LINEAR (position
+ * interpolation, Chen et al. 2023), SERQ_ROPE_BASE (a larger base), or
+ * SERQ_ROPE_BANDS (by parts, Peng et al. 2023): with n_i = orig_len f_i / 2 pi
+ * turns over the trained length and g = clamp((n_i - low) / (high - low), 0,
+ * 1) the frequency is (1 - g) f_i / factor + g f_i. Every entry is multiplied
+ * by mscale (1, or that method's temperature 0.1 ln(factor) + 1).
+ *   rot_dim  even, 2..65536;  max_pos >= 1;  theta > 0;  factor >= 1;
+ *            orig_len >= 1 and low < high for SERQ_ROPE_BANDS.
+ *   table    max_pos x rot_dim floats: row p holds its rot_dim / 2 cosines,
+ *            then its sines.
+ * Errors: SERQ_EINVAL (NULL table, a value outside these ranges or not
+ * finite; rot_dim 2 with SERQ_ROPE_BASE).
+ */
+int serq_rope_table(int rot_dim, int max_pos, double theta, serq_rope_scaling scaling,
+                    double factor, int orig_len, double low, double high, double mscale,
+                    float* table);
+
+/*
+ * serq_rope_append -- online, device memory, asynchronous on `stream`.
+ *
+ * From the q/k/v linear's output to queries and a filled cache in one pass:
+ * for token t, every query and key head x (D values) becomes
+ *     y = x * w / sqrt(mean(x^2) + eps)          (only where w is given)
+ *     (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s)
+ * over the pairs of its first rot_dim values, c and s from row pos[t] of the
+ * table: pair i is (i, i + rot_dim / 2) for SERQ_ROPE_HALF and (2 i, 2 i + 1)
+ * for SERQ_ROPE_INTERLEAVED; values from rot_dim on are not rotated. All in
+ * fp32, rounded once at the end. Keys and the unchanged values then go to
+ * slot[t] of the cache.
+ *   QKV      M rows of Hq + 2 Hkv heads of D (queries, keys, values), row t
+ *            at QKV + t * ld elements, ld >= (Hq + 2 Hkv) D. It need only be
+ *            aligned to its element; rows that are all 16-byte aligned take
+ *            the vector path, others a scalar one.
+ *   q_norm, k_norm  D floats each, or NULL for no norm of that kind.
+ *   table    max_pos x rot_dim floats (serq_rope_table); rot_dim even,
+ *            0 <= rot_dim <= D; NULL when rot_dim == 0.
+ *   pos      M int32. A token whose position is outside [0, max_pos) gets
+ *            NaN queries and is not stored (rot_dim > 0 only).
+ *   slot     M int32, distinct where they are stored. A token whose slot is
+ *            outside [0, n_pages * page_size) gets its queries but is not
+ *            stored (-1: padding).
+ *   Q        device, M x Hq x D, row stride ldq >= Hq D elements; must not
+ *            overlap QKV unless it is its query part (Q == QKV, ldq == ld).
+ * M == 0 is a no-op (QKV, pos, slot and Q may then be NULL). Hq may be 0 (Q
+ * is then not used). Errors: SERQ_EINVAL (NULL pointer, bad size, eps
+ * negative or not finite), SERQ_EUNSUPPORTED (D or page_size),
+ * SERQ_EALIGN (QKV or Q not aligned to its element, Kc, Vc, the table or a
+ * norm not 16-byte aligned), SERQ_EHIP. Uses no scratch memory.
+ */
+int serq_rope_append(const void* QKV, serq_dtype dtype, int64_t ld, int M, int Hq, int Hkv, int D,
+                     const float* q_norm, const float* k_norm, float eps,
+                     const float* table, int rot_dim, int max_pos, serq_rope_layout layout,
+                     const int32_t* pos, const int32_t* slot,
+                     void* Q, int64_t ldq, void* Kc, void* Vc, int n_pages, int page_size,
+                     void* stream);
+
+/*
+ * serq_attn_prefill -- online, device memory, asynchronous on `stream`.
+ *
+ * Causal attention of the new tokens of B sequences, packed one after
+ * another, over the cache that already holds their keys and values: with
+ * n_b = cu_q[b + 1] - cu_q[b] new tokens of sequence b and kv_len[b] tokens
+ * in the cache (the new ones the last of them), new token i sees the keys
+ * j <= kv_len[b] - n_b + i:
+ *     O_i = sum_j softmax_j(scale q_i . k_j) v_j .
+ * A token that sees no key (kv_len[b] < n_b) gets zeros, and so does one all
+ * of whose scores are -inf. A key or value that a token does not see has no
+ * influence on it, NaN and infinities included. Scores, softmax statistics
+ * and sums are fp32; with SERQ_BF16 each softmax weight is rounded to bf16
+ * for the product with the values.
+ *   Q        T rows of Hq heads of D, row stride ldq >= Hq D elements; 16-byte
+ *            aligned rows.
+ *   cu_q     B + 1 int32, cu_q[0] = 0, not decreasing, cu_q[B] = T (values
+ *            outside [0, T] are taken as the nearest inside; rows that no
+ *            sequence holds are left untouched).
+ *   page_table  B rows of max_pages page ids;  kv_len  B int32 (taken as at
+ *            most min(max_len, max_pages * page_size)).
+ *   max_len  bound of kv_len, known to the host; sizes the workspace and
+ *            the split of the keys.
+ *   O        T rows of Hq heads of D, row stride ldo >= Hq D, 16-byte
+ *            aligned rows; must not overlap Q unless it is Q (same stride).
+ *   workspace  serq_attn_prefill_workspace(...) bytes, 16-byte aligned, or
+ *            NULL if that is 0. Its contents need no preparation and are
+ *            free again when the call's work is done; calls that may overlap
+ *            need one each.
+ * T == 0 or B == 0 is a no-op. Errors: SERQ_EINVAL (NULL pointer, bad size,
+ * scale not finite, workspace too small), SERQ_EUNSUPPORTED (D or
+ * page_size), SERQ_EALIGN, SERQ_EHIP.
+ */
+int serq_attn_prefill(const void* Q, serq_dtype dtype, int64_t ldq, const int32_t* cu_q, int B, int T,
+                      int Hq, int Hkv, int D, const void* Kc, const void* Vc, int n_pages, int page_size,
+                      const int32_t* page_table, int max_pages, const int32_t* kv_len, int max_len,
+                      float scale, void* O, int64_t ldo, void* workspace, int64_t workspace_bytes,
+                      void* stream);
+
+/* Bytes of workspace serq_attn_prefill needs for these sizes (may be 0), or
+ * -1 for invalid ones. Host only. */
+int64_t serq_attn_prefill_workspace(serq_dtype dtype, int B, int T, int Hq, int Hkv, int D, int max_len);
+
+/*
+ * serq_attn_decode -- online, device memory, asynchronous on `stream`.
+ *
+ * One new token of each of B sequences over the cache. The sequences may
+ * share a prefix of prefix_len tokens, whose pages are given once; sequence
+ * b then continues with kv_len[b] tokens of its own (the new one among
+ * them), which begin in pages of its own whatever prefix_len is. Token b
+ * attends to the prefix and to its own tokens:
+ *     O_b = sum_j softmax_j(scale q_b . k_j) v_j .
+ * The prefix is read once for all sequences: their queries form the rows of
+ * one matrix product per key/value head. Both parts are cut along the keys,
+ * and the parts are joined by their running maxima and sums, in a fixed
+ * order. Zeros where there is no key at all; arithmetic as for
+ * serq_attn_prefill.
+ *   Q, O     B rows of Hq heads of D, strides and alignment as for
+ *            serq_attn_prefill.
+ *   prefix_table  ceil(prefix_len / page_size) page ids; NULL when
+ *            prefix_len == 0.
+ *   page_table  B rows of max_pages page ids (may be NULL when max_pages or
+ *            max_len is 0: no sequence then has tokens of its own);
+ *            kv_len  B int32, taken as at most min(max_len, max_pages *
+ *            page_size), negative as 0.
+ *   max_len  bound of kv_len, known to the host: sizes the workspace and the
+ *            split of the keys.
+ *   workspace  serq_attn_decode_workspace(...) bytes, as for
+ *            serq_attn_prefill.
+ * B == 0 is a no-op. Errors as for serq_attn_prefill.
+ */
+int serq_attn_decode(const void* Q, serq_dtype dtype, int64_t ldq, int B, int Hq, int Hkv, int D,
+                     const void* Kc, const void* Vc, int n_pages, int page_size,
+                     const int32_t* prefix_table, int prefix_len,
+                     const int32_t* page_table, int max_pages, const int32_t* kv_len, int max_len,
+                     float scale, void* O, int64_t ldo, void* workspace, int64_t workspace_bytes,
+                     void* stream);
+
+/* Bytes of workspace serq_attn_decode needs for these sizes (may be 0), or
+ * -1 for invalid ones. Host only. */
+int64_t serq_attn_decode_workspace(serq_dtype dtype, int B, int Hq, int Hkv, int D, int prefix_len,
+                                   int max_len);
 
 #ifdef __cplusplus
 }

@@ -21,7 +21,9 @@ SERQ_F32, SERQ_BF16 = 0, 1
 EXPORTS = ("serq_strerror", "serq_abi_version", "serq_calibrate", "serq_calibrate_gptq", "serq_permute_outputs",
            "serq_quant_act", "serq_silu_mul_quant_act", "serq_linear", "serq_linear_kernel_name",
            "serq_rq_row_bytes", "serq_bf6_bytes", "serq_prepack_bf6", "serq_act_bf6", "serq_linear_bf6",
-           "serq_linear_bf6_kernel_name", "serq_calibrate_mx", "serq_quant_act_mx", "serq_linear_mx")
+           "serq_linear_bf6_kernel_name", "serq_calibrate_mx", "serq_quant_act_mx", "serq_linear_mx",
+           "serq_rope_table", "serq_rope_append", "serq_attn_prefill", "serq_attn_prefill_workspace",
+           "serq_attn_decode", "serq_attn_decode_workspace")
 
 
 class SerqError(RuntimeError):
@@ -80,6 +82,22 @@ def _load() -> ctypes.CDLL:
     lib.serq_quant_act_mx.restype = ip
     lib.serq_linear_mx.argtypes = [vp, vp, vp, vp, vp, vp, ip, ip, ip, ip, vp, i32, vp, vp, vp]
     lib.serq_linear_mx.restype = ip
+    i64, f64 = ctypes.c_int64, ctypes.c_double
+    lib.serq_rope_table.argtypes = [ip, ip, f64, i32, f64, ip, f64, f64, f64, vp]
+    lib.serq_rope_table.restype = ip
+    lib.serq_rope_append.argtypes = [vp, i32, i64, ip, ip, ip, ip, vp, vp, fp, vp, ip, ip, i32, vp, vp, vp, i64, vp, vp,
+                                     ip, ip, vp]
+    lib.serq_rope_append.restype = ip
+    lib.serq_attn_prefill.argtypes = [vp, i32, i64, vp, ip, ip, ip, ip, ip, vp, vp, ip, ip, vp, ip, vp, ip, fp, vp, i64,
+                                      vp, i64, vp]
+    lib.serq_attn_prefill.restype = ip
+    lib.serq_attn_prefill_workspace.argtypes = [i32, ip, ip, ip, ip, ip, ip]
+    lib.serq_attn_prefill_workspace.restype = i64
+    lib.serq_attn_decode.argtypes = [vp, i32, i64, ip, ip, ip, ip, vp, vp, ip, ip, vp, ip, vp, ip, vp, ip, fp, vp, i64,
+                                     vp, i64, vp]
+    lib.serq_attn_decode.restype = ip
+    lib.serq_attn_decode_workspace.argtypes = [i32, ip, ip, ip, ip, ip, ip]
+    lib.serq_attn_decode_workspace.restype = i64
     return lib
 
 

@@ -1,0 +1,224 @@
+"""The attention half of a decoder layer (include/serq.h): argument
+marshalling only. Every online call enqueues the library's HIP kernels on the
+current torch stream.
+
+    cache = KvCache.empty(n_pages, n_kv_heads, page_size, head_dim)
+    table = torch.from_numpy(rope_table(head_dim, max_pos, theta=5e5)).cuda()
+    q = rope_append(qkv, n_heads, cache, pos, slot, table)           # queries; keys and values stored
+    o = attn_prefill(q, cu_q, cache, pages, kv_len, max_len=...)     # new tokens, packed
+    o = attn_decode(q, cache, pages, kv_len, max_len=...)            # one token per sequence
+"""
+
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import numpy as np
+
+from . import _lib
+from ._lib import SERQ_BF16, SERQ_EINVAL, SERQ_F32, SerqError, check
+
+lib = _lib.lib
+
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
+
+
+def _dtype(t, what):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return SERQ_BF16
+    if t.dtype == torch.float32:
+        return SERQ_F32
+    raise ValueError(f"{what} must be float32 or bfloat16")
+
+
+@dataclass
+class KvCache:
+    """Paged keys and values: two contiguous device tensors, each (pages, kv
+    heads, page size, head dim), of one dtype. Slot s is token s % page size
+    of page s // page size."""
+
+    k: "object"
+    v: "object"
+
+    def __post_init__(self):
+        k, v = self.k, self.v
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must be (pages, kv heads, page size, head dim) tensors alike")
+        if not k.is_cuda or not k.is_contiguous() or not v.is_contiguous():
+            raise ValueError("device tensors must be contiguous CUDA tensors")
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        self.dtype = _dtype(k, "the cache")
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, *, dtype=None, device="cuda"):
+        """A cache of uninitialised pages (bfloat16 unless ``dtype`` says otherwise)."""
+        import torch
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        dtype = torch.bfloat16 if dtype is None else dtype
+        return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
+
+
+def rope_table(rot_dim: int, max_pos: int, *, theta: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+               orig_len: int = 0, low: float = 1.0, high: float = 4.0, mscale: float = 1.0) -> np.ndarray:
+    """Cosines and sines of the rotary embedding (serq_rope_table), host:
+    (max_pos, rot_dim) float32, each row its cosines, then its sines.
+    ``scaling`` is "plain", "linear", "base" or "bands"."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
+    if rot_dim < 0 or max_pos < 0:
+        raise SerqError("serq_rope_table", SERQ_EINVAL, "sizes must be positive")
+    t = np.empty((max_pos, rot_dim), np.float32)
+    check("serq_rope_table", lib.serq_rope_table(rot_dim, max_pos, theta, _SCALINGS[scaling], factor, orig_len, low,
+                                                 high, mscale, t.ctypes.data if t.size else None))
+    return t
+
+
+def _stream(t):
+    import torch
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _ints(t, shape, what):
+    import torch
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be a contiguous CUDA int32 tensor of shape {shape}")
+    return t.data_ptr()
+
+
+def _rows(t, cache, what):
+    """Row stride of a (rows, heads, head dim) tensor whose rows are whole."""
+    if t.dim() != 3 or t.shape[2] != cache.head_dim or not t.is_cuda or t.dtype != cache.k.dtype:
+        raise ValueError(f"{what} must be a CUDA (rows, heads, {cache.head_dim}) tensor of the cache's dtype")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
+        raise ValueError(f"{what}: heads must lie one after another in a row")
+    return s0 if n > 1 else h * d
+
+
+def _out(out, q, cache):
+    import torch
+    if out is None:
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if out.shape != q.shape:
+        raise ValueError(f"out must be of shape {tuple(q.shape)}")
+    return out
+
+
+def _space(workspace, need, q):
+    import torch
+    if need < 0:
+        raise ValueError("sizes that the library does not take")
+    if need == 0:
+        return None, 0
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must be a contiguous CUDA tensor of {need} bytes or more")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def rope_append(qkv, n_heads: int, cache: KvCache, pos, slot, table, *, layout: str = "half", q_norm=None, k_norm=None,
+                eps: float = 1e-6, out=None):
+    """Queries of the q/k/v linear's output, with keys and values stored in
+    the cache (serq_rope_append), on the current stream. ``qkv`` is M x
+    (n_heads + 2 kv heads) * head dim (unit column stride), ``pos`` and
+    ``slot`` M int32, ``table`` (max_pos, rot_dim) float32 on the device or
+    None for no rotation. Returns M x n_heads x head dim."""
+    import torch
+    if qkv.dim() != 2 or not qkv.is_cuda or qkv.dtype != cache.k.dtype:
+        raise ValueError("qkv must be a two-dimensional CUDA tensor of the cache's dtype")
+    M, width = qkv.shape
+    D, Hkv = cache.head_dim, cache.n_kv_heads
+    if width != (n_heads + 2 * Hkv) * D or (M > 0 and qkv.stride(1) != 1):
+        raise ValueError(f"qkv must have {(n_heads + 2 * Hkv) * D} columns of unit stride")
+    ld = qkv.stride(0) if M > 1 else width
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}")
+    rot = max_pos = 0
+    if table is not None:
+        if table.dim() != 2 or table.dtype != torch.float32 or not table.is_cuda or not table.is_contiguous():
+            raise ValueError("table must be a contiguous CUDA (max_pos, rot_dim) float32 tensor")
+        max_pos, rot = table.shape
+    for w in (q_norm, k_norm):
+        if w is not None and (w.dtype != torch.float32 or not w.is_cuda or not w.is_contiguous() or w.numel() != D):
+            raise ValueError(f"norms must be contiguous CUDA float32 tensors of {D}")
+    pp = _ints(pos, (M,), "pos") if rot else None
+    sp = _ints(slot, (M,), "slot")
+    q = torch.empty((M, n_heads, D), dtype=qkv.dtype, device=qkv.device) if out is None else out
+    if out is not None and tuple(out.shape) != (M, n_heads, D):
+        raise ValueError(f"out must be of shape {(M, n_heads, D)}")
+    ldq = _rows(q, cache, "out")
+    check("serq_rope_append", lib.serq_rope_append(
+        qkv.data_ptr(), cache.dtype, ld, M, n_heads, Hkv, D, q_norm.data_ptr() if q_norm is not None else None,
+        k_norm.data_ptr() if k_norm is not None else None, eps, table.data_ptr() if rot else None, rot, max_pos,
+        _LAYOUTS[layout], pp, sp, q.data_ptr(), ldq, cache.k.data_ptr(), cache.v.data_ptr(), cache.n_pages,
+        cache.page_size, _stream(qkv)))
+    return q
+
+
+def attn_prefill_workspace(cache: KvCache, B: int, T: int, n_heads: int, max_len: int) -> int:
+    """Bytes of workspace attn_prefill needs (serq_attn_prefill_workspace)."""
+    return lib.serq_attn_prefill_workspace(cache.dtype, B, T, n_heads, cache.n_kv_heads, cache.head_dim, max_len)
+
+
+def attn_prefill(q, cu_q, cache: KvCache, page_table, kv_len, *, max_len: int, scale: float | None = None, out=None,
+                 workspace=None):
+    """Causal attention of packed new tokens over the cache
+    (serq_attn_prefill) on the current stream. ``q`` is T x heads x head dim,
+    ``cu_q`` B + 1, ``page_table`` B x pages and ``kv_len`` B int32 on the
+    device; ``max_len`` bounds kv_len; ``scale`` is head_dim ** -0.5 unless
+    given. A workspace is taken from torch's allocator unless given. Returns
+    T x heads x head dim."""
+    ldq = _rows(q, cache, "q")
+    T, Hq, D = q.shape
+    B, wide = page_table.shape
+    cp = _ints(cu_q, (B + 1,), "cu_q")
+    tp = _ints(page_table, (B, wide), "page_table")
+    kp = _ints(kv_len, (B,), "kv_len")
+    o = _out(out, q, cache)
+    ldo = _rows(o, cache, "out")
+    ws, size = _space(workspace, attn_prefill_workspace(cache, B, T, Hq, max_len), q)
+    check("serq_attn_prefill", lib.serq_attn_prefill(
+        q.data_ptr(), cache.dtype, ldq, cp, B, T, Hq, cache.n_kv_heads, D, cache.k.data_ptr(), cache.v.data_ptr(),
+        cache.n_pages, cache.page_size, tp, wide, kp, max_len, D ** -0.5 if scale is None else scale, o.data_ptr(),
+        ldo, ws.data_ptr() if size else None, size, _stream(q)))
+    return o
+
+
+def attn_decode_workspace(cache: KvCache, B: int, n_heads: int, prefix_len: int, max_len: int) -> int:
+    """Bytes of workspace attn_decode needs (serq_attn_decode_workspace)."""
+    return lib.serq_attn_decode_workspace(cache.dtype, B, n_heads, cache.n_kv_heads, cache.head_dim, prefix_len,
+                                          max_len)
+
+
+def attn_decode(q, cache: KvCache, page_table, kv_len, *, max_len: int, prefix=None, prefix_len: int = 0,
+                scale: float | None = None, out=None, workspace=None):
+    """One new token per sequence over the cache (serq_attn_decode) on the
+    current stream. ``q`` is B x heads x head dim; ``page_table`` B x pages
+    and ``kv_len`` B int32 give each sequence's own tokens, ``prefix`` (int32
+    page ids) and ``prefix_len`` the tokens that all of them share before
+    those. Returns B x heads x head dim."""
+    ldq = _rows(q, cache, "q")
+    B, Hq, D = q.shape
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be {B} x pages")
+    wide = page_table.shape[1]
+    tp = _ints(page_table, (B, wide), "page_table")
+    kp = _ints(kv_len, (B,), "kv_len")
+    pp = None
+    if prefix_len > 0:
+        pages = -(-prefix_len // cache.page_size)
+        if prefix is None or prefix.numel() < pages:
+            raise ValueError(f"prefix must hold {pages} page ids")
+        pp = _ints(prefix, (prefix.numel(),), "prefix")
+    o = _out(out, q, cache)
+    ldo = _rows(o, cache, "out")
+    ws, size = _space(workspace, attn_decode_workspace(cache, B, Hq, prefix_len, max_len), q)
+    check("serq_attn_decode", lib.serq_attn_decode(
+        q.data_ptr(), cache.dtype, ldq, B, Hq, cache.n_kv_heads, D, cache.k.data_ptr(), cache.v.data_ptr(),
+        cache.n_pages, cache.page_size, pp, prefix_len, tp, wide, kp, max_len, D ** -0.5 if scale is None else scale,
+        o.data_ptr(), ldo, ws.data_ptr() if size else None, size, _stream(q)))
+    return o

@@ -28,7 +28,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libserq.so")
 ARCH = os.environ.get("SERQ_OFFLOAD_ARCH", "gfx950")
 
-SOURCES = ["serq_abi.cpp", "calibrate.cpp", "quant_act.hip", "serq_gemm.hip", "serq_mx.hip"]
+SOURCES = ["serq_abi.cpp", "calibrate.cpp", "quant_act.hip", "serq_gemm.hip", "serq_mx.hip",
+           "attn_abi.cpp", "rope_table.cpp", "rope_append.hip", "attention.hip"]
 
 
 def hipcc() -> str:

@@ -1,0 +1,673 @@
+// Attention over the paged cache (gfx950): serq_attn_prefill and
+// serq_attn_decode.
+//
+// Softmax over keys in one pass: with z_j = scale log2(e) q.k_j, the running
+// maximum m, sum l = sum 2^(z_j - m) and o = sum 2^(z_j - m) v_j are kept in
+// fp32; a larger maximum scales l and o by 2^(m_old - m_new). Parts of the
+// keys are joined the same way.
+//
+// Both products are taken transposed. S^T = K Q^T leaves each lane with
+// scores of one query (column = lane % 16) and four keys per 16 x 16 tile,
+// so the statistics of a query are one value per lane; and as the index that
+// a matrix instruction sums over may be renamed on both operands alike,
+// those registers, converted, are the second operand of O^T = V^T P^T as
+// they are: the lane group g = lane / 16 takes the keys it already holds
+// (4 g .. 4 g + 3 of each tile) as its summation slots, and the values are
+// loaded to match. Scores never pass through LDS.
+
+#include "serq_attn.h"
+
+namespace serq {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kNone = -__builtin_inff();
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const bf16x2 p = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
+  return __builtin_bit_cast(uint32_t, p);
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Maximum (sum) over the four lane groups that share a query.
+__device__ __forceinline__ float max_groups(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16, 64));
+  return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+__device__ __forceinline__ float sum_groups(float v) {
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+// The reference of the exponentials: the running maximum, or 0 while no
+// score but -inf has been seen (2^(-inf - 0) = 0).
+__device__ __forceinline__ float ref(float m) { return m == kNone ? 0.0f : m; }
+
+// One sequence's pages of one key/value head, for one wave.
+template <typename T, int D>
+struct Pages {
+  const T* k;
+  const T* v;
+  const int32_t* table;
+  int last;            // last page index in use (keys exist)
+  int shift, n_pages, Hkv, h;
+
+  // Element offset of key `key` (a multiple of 16, wave-uniform); keys past
+  // the last page give that page again.
+  __device__ __forceinline__ int64_t at(int key) const {
+    int i = key >> shift;
+    i = uniform(i < last ? i : last);
+    int page = table[i];
+    page = page < 0 ? 0 : page >= n_pages ? n_pages - 1 : page;
+    page = uniform(page);
+    return (((static_cast<int64_t>(page) * Hkv + h) << shift) + (key & ((1 << shift) - 1))) * D;
+  }
+};
+
+// Sixteen query rows of one wave: operands, running statistics, O^T.
+template <typename T, int D>
+struct Rows;
+
+// bf16: 32 keys a step, v_mfma_f32_16x16x32_bf16. Lane (n = lane % 16, g =
+// lane / 16). Q and K operand c of D / 32: values 32 c + 8 g .. + 7 of row n.
+// V: lane n holds W = D / 16 values W n .. of each of its eight keys; product
+// c takes value W n + c of them as row n of V^T, so O^T register (c, j) is
+// value W (4 g + j) + c of query n.
+template <int D>
+struct Rows<__bf16, D> {
+  static constexpr int kStep = 32, C = D / 32, W = D / 16;
+  u32x4 q[C];
+  f32x4 o[W];
+  float m, l;
+
+  __device__ __forceinline__ void init() {
+    m = kNone;
+    l = 0.0f;
+#pragma unroll
+    for (int c = 0; c < W; ++c) o[c] = f32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void load_q(const __bf16* row, int g) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) q[c] = *reinterpret_cast<const u32x4*>(row + 32 * c + 8 * g);
+  }
+
+  template <bool CAUSAL>
+  __device__ __forceinline__ void step(const Pages<__bf16, D>& pg, int key0, int limit, int mine, float scale, int n,
+                                       int g) {
+    const int64_t at0 = pg.at(key0), at1 = pg.at(key0 + 16);
+    u32x4 k[2][C];
+    uint32_t v[8][W / 2];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      k[0][c] = *reinterpret_cast<const u32x4*>(pg.k + at0 + n * D + 32 * c + 8 * g);
+      k[1][c] = *reinterpret_cast<const u32x4*>(pg.k + at1 + n * D + 32 * c + 8 * g);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const __bf16* p = pg.v + (j < 4 ? at0 : at1) + (4 * g + (j & 3)) * D + W * n;
+      if constexpr (W == 8) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = x[i];
+      } else {
+        const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+        v[j][0] = x[0];
+        v[j][1] = x[1];
+      }
+    }
+    if (key0 + 32 > limit) {        // what lies past the end may be anything
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool in = key0 + 16 * (j / 4) + 4 * g + (j & 3) < limit;
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) v[j][i] = in ? v[j][i] : 0;
+      }
+    }
+    f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[t][c]),
+                                                       __builtin_bit_cast(bf16x8, q[c]), s[t], 0, 0, 0);
+    }
+    float z[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = s[j / 4][j & 3] * scale;
+    if (CAUSAL || key0 + 32 > limit) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = key0 + 16 * (j / 4) + 4 * g + (j & 3) < mine ? z[j] : kNone;
+    }
+    float top = z[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) top = fmaxf(top, z[j]);
+    const float mn = fmaxf(m, max_groups(top));
+    const float r = ref(mn), f = exp2_(m - r);
+    m = mn;
+    l *= f;
+    uint32_t p[4];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float a = exp2_(z[j] - r), b = exp2_(z[j + 1] - r);
+      l += a + b;
+      p[j / 2] = pack2(a, b);       // weights in [0, 1]; 8 bits each, as the values they multiply
+    }
+    const bf16x8 pb = __builtin_bit_cast(bf16x8, u32x4{p[0], p[1], p[2], p[3]});
+#pragma unroll
+    for (int c = 0; c < W; ++c) o[c] *= f;
+    bool odd = false;
+    if constexpr (CAUSAL) odd = __any(key0 + 32 > mine) && __any(!finite(v));
+    if (!odd) {
+      product(v, pb, o);
+    } else {
+      // A value that is not finite lies where some of these queries do not
+      // look, and 0 * inf is not 0: each query takes the product over its own
+      // keys with the others' values cleared.
+      for (int i = 0; i < 16; ++i) {
+        const int lim = __shfl(mine, i, 64);
+        uint32_t u[8][W / 2];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int c = 0; c < W / 2; ++c)
+            u[j][c] = key0 + 16 * (j / 4) + 4 * g + (j & 3) < lim ? v[j][c] : 0;
+        f32x4 t[W];
+#pragma unroll
+        for (int c = 0; c < W; ++c) t[c] = o[c];
+        product(u, pb, t);
+#pragma unroll
+        for (int c = 0; c < W; ++c) o[c] = n == i ? t[c] : o[c];
+      }
+    }
+  }
+
+  static __device__ __forceinline__ bool finite(const uint32_t (&v)[8][W / 2]) {
+    bool ok = true;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int c = 0; c < W / 2; ++c)
+        ok &= (v[j][c] & 0x7F80u) != 0x7F80u && (v[j][c] & 0x7F800000u) != 0x7F800000u;
+    return ok;
+  }
+
+  static __device__ __forceinline__ void product(const uint32_t (&v)[8][W / 2], bf16x8 pb, f32x4 (&o)[W]) {
+#pragma unroll
+    for (int c = 0; c < W; ++c) {
+      const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
+      u32x4 a;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = __builtin_amdgcn_perm(v[2 * i + 1][c / 2], v[2 * i][c / 2], sel);
+      o[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), pb, o[c], 0, 0, 0);
+    }
+  }
+
+  // Value index of o[c][j], and how a lane's values lie in memory: for each
+  // j, W consecutive ones from W (4 g + j).
+  __device__ __forceinline__ void store(__bf16* row, int g, float inv) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t w[W / 2];
+#pragma unroll
+      for (int c = 0; c < W; c += 2) w[c / 2] = pack2(o[c][j] * inv, o[c + 1][j] * inv);
+      __bf16* p = row + W * (4 * g + j);
+      if constexpr (W == 8) *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+      else *reinterpret_cast<u32x2*>(p) = u32x2{w[0], w[1]};
+    }
+  }
+  __device__ __forceinline__ void store_f32(float* row, int g) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int c = 0; c < W; c += 4)
+        *reinterpret_cast<f32x4*>(row + W * (4 * g + j) + c) = f32x4{o[c][j], o[c + 1][j], o[c + 2][j], o[c + 3][j]};
+  }
+};
+
+// fp32: 16 keys a step, v_mfma_f32_16x16x4_f32 (one summation slot per lane
+// group). Q and K: lane (n, g) holds values 16 c + 4 g .. + 3 of row n; the
+// product (c, e) takes value e of them. V: lane n holds values 64 b + 4 n ..
+// + 3 of its four keys 4 g + j; product (b, e, j) takes value e, so O^T
+// register (b, e, i) is value 64 b + 4 (4 g + i) + e of query n.
+template <int D>
+struct Rows<float, D> {
+  static constexpr int kStep = 16, C = D / 16, NB = D / 64;
+  f32x4 q[C];
+  f32x4 o[NB * 4];
+  float m, l;
+
+  __device__ __forceinline__ void init() {
+    m = kNone;
+    l = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NB * 4; ++c) o[c] = f32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void load_q(const float* row, int g) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) q[c] = *reinterpret_cast<const f32x4*>(row + 16 * c + 4 * g);
+  }
+
+  template <bool CAUSAL>
+  __device__ __forceinline__ void step(const Pages<float, D>& pg, int key0, int limit, int mine, float scale, int n,
+                                       int g) {
+    const int64_t at = pg.at(key0);
+    f32x4 k[C], v[4][NB];
+#pragma unroll
+    for (int c = 0; c < C; ++c) k[c] = *reinterpret_cast<const f32x4*>(pg.k + at + n * D + 16 * c + 4 * g);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) v[j][b] = *reinterpret_cast<const f32x4*>(pg.v + at + (4 * g + j) * D + 64 * b + 4 * n);
+    if (key0 + 16 > limit) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = key0 + 4 * g + j < limit;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[j][b][e] = in ? v[j][b][e] : 0.0f;
+      }
+    }
+    f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(k[c][e], q[c][e], s[e & 1], 0, 0, 0);
+    float z[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j] = (s[0][j] + s[1][j]) * scale;
+    if (CAUSAL || key0 + 16 > limit) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = key0 + 4 * g + j < mine ? z[j] : kNone;
+    }
+    const float top = max_groups(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
+    const float mn = fmaxf(m, top);
+    const float r = ref(mn), f = exp2_(m - r);
+    m = mn;
+    float p[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = exp2_(z[j] - r);
+    l = l * f + ((p[0] + p[1]) + (p[2] + p[3]));
+#pragma unroll
+    for (int c = 0; c < NB * 4; ++c) o[c] *= f;
+    bool odd = false;
+    if constexpr (CAUSAL) odd = __any(key0 + 16 > mine) && __any(!finite(v));
+    if (!odd) {
+      product(v, p, o);
+    } else {                        // as for bf16: each query over its own keys alone
+      for (int i = 0; i < 16; ++i) {
+        const int lim = __shfl(mine, i, 64);
+        f32x4 u[4][NB], t[NB * 4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[j][b][e] = key0 + 4 * g + j < lim ? v[j][b][e] : 0.0f;
+#pragma unroll
+        for (int c = 0; c < NB * 4; ++c) t[c] = o[c];
+        product(u, p, t);
+#pragma unroll
+        for (int c = 0; c < NB * 4; ++c) o[c] = n == i ? t[c] : o[c];
+      }
+    }
+  }
+
+  static __device__ __forceinline__ bool finite(const f32x4 (&v)[4][NB]) {
+    bool ok = true;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ok &= (__float_as_uint(v[j][b][e]) & 0x7F800000u) != 0x7F800000u;
+    return ok;
+  }
+
+  static __device__ __forceinline__ void product(const f32x4 (&v)[4][NB], const float (&p)[4], f32x4 (&o)[NB * 4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[4 * b + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[j][b][e], p[j], o[4 * b + e], 0, 0, 0);
+  }
+
+  __device__ __forceinline__ void store(float* row, int g, float inv) const {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<f32x4*>(row + 64 * b + 4 * (4 * g + i)) =
+            f32x4{o[4 * b][i] * inv, o[4 * b + 1][i] * inv, o[4 * b + 2][i] * inv, o[4 * b + 3][i] * inv};
+  }
+  __device__ __forceinline__ void store_f32(float* row, int g) const { store(row, g, 1.0f); }
+};
+
+// Partial results of a row and part, in the caller's workspace: D sums, then
+// (m, l) pairs after all sums.
+struct Parts {
+  float* o;        // rows x splits x D
+  float2* ml;      // rows x splits
+  int splits;
+};
+
+__device__ __forceinline__ int bounded_len(const AttnArgs& a, int b) {
+  const int n = a.kv_len[b];
+  return n < 0 ? 0 : n < a.max_len ? n : a.max_len;
+}
+
+__device__ __forceinline__ int bounded_cu(const AttnArgs& a, int i) {
+  const int n = a.cu_q[i];
+  return n < 0 ? 0 : n < a.T ? n : a.T;
+}
+
+// ------------------------------------------------------------------ prefill
+
+constexpr int kPrefillWaves = 4;
+
+// One workgroup: a tile of positions of one sequence for `pack` heads of a
+// group, a wave per 16 positions of a head. Tile x counts over all sequences.
+template <typename T, int D>
+__global__ __launch_bounds__(64 * kPrefillWaves) void attn_prefill_kernel(AttnArgs a, PrefillPlan p, Parts parts) {
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int tile_pos = 16 * (kPrefillWaves / p.pack);
+  const int units = a.Hq / p.pack;
+  const int unit = blockIdx.x % units;
+  int tile = blockIdx.x / units, b = 0, q0 = 0, nq = 0;
+  for (; b < a.B; ++b) {
+    q0 = bounded_cu(a, b);
+    nq = bounded_cu(a, b + 1) - q0;
+    const int tiles = nq > 0 ? (nq + tile_pos - 1) / tile_pos : 0;
+    if (tile < tiles) break;
+    tile -= tiles;
+  }
+  if (b == a.B) return;
+  const int len = bounded_len(a, b);
+  const int h = unit * p.pack + wave % p.pack;
+  const int pos0 = tile * tile_pos + 16 * (wave / p.pack);
+  if (pos0 >= nq) return;
+  const int pos = pos0 + n;
+  const int row = q0 + (pos < nq ? pos : nq - 1);
+  const int64_t first = static_cast<int64_t>(len) - nq + 1;        // keys that position 0 sees
+  int mine = static_cast<int>(first + pos < 0 ? 0 : first + pos);
+  if (mine > len) mine = len;
+  const int top = pos0 + 15 < nq ? pos0 + 15 : nq - 1;
+  int end = static_cast<int>(first + top < 0 ? 0 : first + top);
+  const int from = blockIdx.y * p.chunk;
+  if (p.splits > 1 && end > from + p.chunk) end = from + p.chunk;
+  Rows<T, D> r;
+  r.init();
+  r.load_q(static_cast<const T*>(a.Q) + row * a.ldq + static_cast<int64_t>(h) * D, g);
+  if (from < end) {
+    Pages<T, D> pg{static_cast<const T*>(a.Kc), static_cast<const T*>(a.Vc),
+                   a.page_table + static_cast<int64_t>(b) * a.max_pages, (len - 1) >> a.page_shift,
+                   a.page_shift, a.n_pages, a.Hkv, h / (a.Hq / a.Hkv)};
+    for (int key = from; key < end; key += r.kStep)
+      r.template step<true>(pg, key, len, mine, a.scale_log2, n, g);
+  }
+  const float l = sum_groups(r.l);
+  if (pos >= nq) return;
+  if (p.splits > 1) {
+    if (from >= mine && from > 0) return;            // the join takes only parts that begin before `mine`
+    const int64_t slot = (static_cast<int64_t>(row) * a.Hq + h) * parts.splits + blockIdx.y;
+    r.store_f32(parts.o + slot * D, g);
+    if (g == 0) parts.ml[slot] = float2{r.m, l};
+  } else {
+    r.store(static_cast<T*>(a.O) + row * a.ldo + static_cast<int64_t>(h) * D, g, l > 0.0f || l != l ? 1.0f / l : 0.0f);
+  }
+}
+
+// ------------------------------------------------------------------- decode
+
+constexpr int kDecodeWaves = 4;
+
+// One workgroup: 16 query rows over one part of the keys, its waves taking
+// steps in turn and joined through LDS. Prefix parts come first: their rows
+// are those of all sequences (row R: sequence R / G, head R % G of the
+// group); a sequence's own parts have its G rows.
+template <typename T, int D>
+__global__ __launch_bounds__(64 * kDecodeWaves) void attn_decode_kernel(AttnArgs a, DecodePlan p, Parts parts) {
+  __shared__ float so[kDecodeWaves][16][D + 4];
+  __shared__ float sml[kDecodeWaves][2][16];
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int G = a.Hq / a.Hkv;
+  int x = blockIdx.x;
+  const int nprefix = a.Hkv * p.ptiles * p.psplits;
+  const bool prefix = x < nprefix;
+  int kvh, R0, rows, part, len, from, to;
+  const int32_t* table;
+  if (prefix) {
+    kvh = x % a.Hkv;
+    x /= a.Hkv;
+    part = x % p.psplits;
+    R0 = x / p.psplits * 16;
+    rows = a.B * G;
+    len = a.prefix_len;
+    table = a.prefix_table;
+    from = part * p.pchunk;
+    to = from + p.pchunk;
+  } else {
+    x -= nprefix;
+    kvh = x % a.Hkv;
+    x /= a.Hkv;
+    part = x % p.splits;
+    x /= p.splits;
+    const int b = x / p.tiles;
+    R0 = b * G + x % p.tiles * 16;
+    rows = (b + 1) * G;
+    len = bounded_len(a, b);
+    table = a.page_table + static_cast<int64_t>(b) * a.max_pages;
+    from = part * p.chunk;
+    to = from + p.chunk;
+    if (from >= len && (from > 0 || p.splits + p.psplits > 1)) return;   // nothing here, and the join knows it
+    part += p.psplits;
+  }
+  if (to > len) to = len;
+  const int R = R0 + n < rows ? R0 + n : rows - 1;
+  const int b = R / G, h = kvh * G + R % G;
+  Rows<T, D> r;
+  r.init();
+  r.load_q(static_cast<const T*>(a.Q) + b * a.ldq + static_cast<int64_t>(h) * D, g);
+  if (from < to) {
+    Pages<T, D> pg{static_cast<const T*>(a.Kc), static_cast<const T*>(a.Vc), table, (len - 1) >> a.page_shift,
+                   a.page_shift, a.n_pages, a.Hkv, kvh};
+    for (int key = from + wave * r.kStep; key < to; key += kDecodeWaves * r.kStep)
+      r.template step<false>(pg, key, to, to, a.scale_log2, n, g);
+  }
+  const float lw = sum_groups(r.l);
+  r.store_f32(&so[wave][n][0], g);
+  if (g == 0) {
+    sml[wave][0][n] = r.m;
+    sml[wave][1][n] = lw;
+  }
+  __syncthreads();
+  // the waves' parts joined: 16 threads per row, D / 16 values each
+  constexpr int W = D / 16;
+  const int q = threadIdx.x / 16, d = threadIdx.x % 16 * W;
+  if (R0 + q >= rows) return;
+  float m = kNone;
+#pragma unroll
+  for (int w = 0; w < kDecodeWaves; ++w) m = fmaxf(m, sml[w][0][q]);
+  float l = 0.0f, o[W] = {};
+#pragma unroll
+  for (int w = 0; w < kDecodeWaves; ++w) {
+    const float f = exp2_(sml[w][0][q] - ref(m));
+    l = __builtin_fmaf(f, sml[w][1][q], l);
+#pragma unroll
+    for (int i = 0; i < W; ++i) o[i] = __builtin_fmaf(f, so[w][q][d + i], o[i]);
+  }
+  const int bq = (R0 + q) / G, hq = kvh * G + (R0 + q) % G;
+  if (p.splits + p.psplits > 1) {
+    const int64_t slot = (static_cast<int64_t>(bq) * a.Hq + hq) * parts.splits + part;
+#pragma unroll
+    for (int i = 0; i < W; i += 4)
+      *reinterpret_cast<f32x4*>(parts.o + slot * D + d + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
+    if (d == 0) parts.ml[slot] = float2{m, l};
+  } else {
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    T* out = static_cast<T*>(a.O) + bq * a.ldo + static_cast<int64_t>(hq) * D + d;
+#pragma unroll
+    for (int i = 0; i < W; ++i) out[i] = static_cast<T>(o[i] * inv);
+  }
+}
+
+// --------------------------------------------------------------------- join
+
+// One wave per row: the parts of its keys joined in their order. Rows of a
+// prefill see parts that begin before their own limit, rows of a decode the
+// prefix parts and those that begin before the sequence's length.
+template <typename T, int D, bool PREFILL>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int psplits, int chunk, Parts parts) {
+  constexpr int W = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + uniform(threadIdx.x >> 6);
+  const int t = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
+  if (t >= (PREFILL ? a.T : a.B)) return;
+  int keys;
+  if constexpr (PREFILL) {
+    int b = 0, q1 = 0, q0 = 0;
+    for (; b < a.B; ++b) {
+      q0 = bounded_cu(a, b);
+      q1 = bounded_cu(a, b + 1);
+      if (t >= q0 && t < q1) break;
+    }
+    if (b == a.B) return;
+    const int64_t first = static_cast<int64_t>(bounded_len(a, b)) - (q1 - q0) + 1;
+    keys = static_cast<int>(first + (t - q0) < 0 ? 0 : first + (t - q0));
+  } else {
+    keys = bounded_len(a, t);
+  }
+  const int own = keys > 0 ? (keys - 1) / chunk + 1 : 0, count = psplits + own;
+  const float2* ml = parts.ml + row * parts.splits;
+  const float* po = parts.o + row * parts.splits * D + lane * W;
+  float m = kNone;
+  for (int s = 0; s < count; ++s) m = fmaxf(m, ml[s].x);
+  const float r = ref(m);
+  float l = 0.0f, o[W] = {};
+  for (int s = 0; s < count; ++s) {
+    const float f = exp2_(ml[s].x - r);
+    l = __builtin_fmaf(f, ml[s].y, l);
+#pragma unroll
+    for (int i = 0; i < W; ++i) o[i] = __builtin_fmaf(f, po[static_cast<int64_t>(s) * D + i], o[i]);
+  }
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  T* out = static_cast<T*>(a.O) + t * a.ldo + static_cast<int64_t>(h) * D + lane * W;
+#pragma unroll
+  for (int i = 0; i < W; ++i) out[i] = static_cast<T>(o[i] * inv);
+}
+
+template <bool PREFILL>
+void launch_join(const AttnArgs& a, int64_t rows, int psplits, int chunk, const Parts& parts, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
+  if (a.bf16) {
+    if (a.D == 64) attn_join_kernel<__bf16, 64, PREFILL><<<grid, 256, 0, st>>>(a, psplits, chunk, parts);
+    else attn_join_kernel<__bf16, 128, PREFILL><<<grid, 256, 0, st>>>(a, psplits, chunk, parts);
+  } else {
+    if (a.D == 64) attn_join_kernel<float, 64, PREFILL><<<grid, 256, 0, st>>>(a, psplits, chunk, parts);
+    else attn_join_kernel<float, 128, PREFILL><<<grid, 256, 0, st>>>(a, psplits, chunk, parts);
+  }
+}
+
+Parts parts_of(void* workspace, int64_t rows, int D, int splits) {
+  float* o = static_cast<float*>(workspace);
+  return Parts{o, reinterpret_cast<float2*>(o + rows * splits * D), splits};
+}
+
+inline int64_t parts_bytes(int64_t rows, int D, int splits) {
+  return splits > 1 ? rows * splits * (D + 2) * static_cast<int64_t>(sizeof(float)) : 0;
+}
+
+inline int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+// `splits` parts of [0, len), each a multiple of 128 keys; returns the chunk
+// and leaves in splits how many of them there are.
+inline int cut(int len, int64_t& splits) {
+  if (splits < 1) splits = 1;
+  int chunk = ceil_div(ceil_div(len, splits), 128) * 128;
+  if (chunk < 128) chunk = 128;
+  splits = len > 0 ? ceil_div(len, chunk) : 1;
+  return chunk;
+}
+
+}  // namespace
+
+PrefillPlan plan_prefill(int bf16, int B, int T, int Hq, int Hkv, int D, int max_len) {
+  (void)bf16;
+  PrefillPlan p{};
+  const int G = Hq / Hkv;
+  p.pack = G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1;
+  const int tile_pos = 16 * kPrefillWaves / p.pack;
+  const int64_t units = (static_cast<int64_t>(ceil_div(T, tile_pos)) + B) * (Hq / p.pack);
+  int64_t splits = units < 512 ? 1024 / units : 1;
+  if (splits > max_len / 512) splits = max_len / 512;
+  p.chunk = cut(max_len, splits);
+  p.splits = static_cast<int>(splits);
+  p.bytes = parts_bytes(static_cast<int64_t>(T) * Hq, D, p.splits);
+  return p;
+}
+
+hipError_t launch_attn_prefill(const AttnArgs& a, const PrefillPlan& p, hipStream_t st) {
+  const int tile_pos = 16 * kPrefillWaves / p.pack;
+  const int64_t tiles = static_cast<int64_t>(a.T / tile_pos) + a.B;      // at least the sum of the sequences' tiles
+  const int64_t rows = static_cast<int64_t>(a.T) * a.Hq;
+  const Parts parts = parts_of(a.workspace, rows, a.D, p.splits);
+  const dim3 grid(static_cast<unsigned>(tiles * (a.Hq / p.pack)), p.splits), block(64 * kPrefillWaves);
+  if (a.bf16) {
+    if (a.D == 64) attn_prefill_kernel<__bf16, 64><<<grid, block, 0, st>>>(a, p, parts);
+    else attn_prefill_kernel<__bf16, 128><<<grid, block, 0, st>>>(a, p, parts);
+  } else {
+    if (a.D == 64) attn_prefill_kernel<float, 64><<<grid, block, 0, st>>>(a, p, parts);
+    else attn_prefill_kernel<float, 128><<<grid, block, 0, st>>>(a, p, parts);
+  }
+  if (p.splits > 1) launch_join<true>(a, rows, 0, p.chunk, parts, st);
+  return hipGetLastError();
+}
+
+DecodePlan plan_decode(int bf16, int B, int Hq, int Hkv, int D, int prefix_len, int max_len) {
+  (void)bf16;
+  DecodePlan p{};
+  const int G = Hq / Hkv;
+  p.tiles = ceil_div(G, 16);
+  p.ptiles = prefix_len > 0 ? ceil_div(static_cast<int64_t>(B) * G, 16) : 0;
+  int64_t s = ceil_div(1024, static_cast<int64_t>(B) * Hkv * p.tiles);
+  p.chunk = cut(max_len, s);
+  p.splits = static_cast<int>(s);
+  if (prefix_len > 0) {
+    s = ceil_div(1024, static_cast<int64_t>(Hkv) * p.ptiles);
+    p.pchunk = cut(prefix_len, s);
+    p.psplits = static_cast<int>(s);
+  }
+  p.bytes = parts_bytes(static_cast<int64_t>(B) * Hq, D, p.splits + p.psplits);
+  return p;
+}
+
+hipError_t launch_attn_decode(const AttnArgs& a, const DecodePlan& p, hipStream_t st) {
+  const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
+  const Parts parts = parts_of(a.workspace, rows, a.D, p.splits + p.psplits);
+  const int64_t blocks = static_cast<int64_t>(a.Hkv) * p.ptiles * p.psplits +
+                         static_cast<int64_t>(a.B) * p.tiles * a.Hkv * p.splits;
+  const dim3 grid(static_cast<unsigned>(blocks)), block(64 * kDecodeWaves);
+  if (a.bf16) {
+    if (a.D == 64) attn_decode_kernel<__bf16, 64><<<grid, block, 0, st>>>(a, p, parts);
+    else attn_decode_kernel<__bf16, 128><<<grid, block, 0, st>>>(a, p, parts);
+  } else {
+    if (a.D == 64) attn_decode_kernel<float, 64><<<grid, block, 0, st>>>(a, p, parts);
+    else attn_decode_kernel<float, 128><<<grid, block, 0, st>>>(a, p, parts);
+  }
+  if (p.splits + p.psplits > 1) launch_join<false>(a, rows, p.psplits, p.chunk, parts, st);
+  return hipGetLastError();
+}
+
+}  // namespace serq

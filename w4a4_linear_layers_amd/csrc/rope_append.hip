@@ -1,0 +1,272 @@
+// Rotary positions, head norms and the paged cache write in one pass (gfx950).
+//
+// From row t of the q/k/v linear's output, head by head:
+//     y = x * w / sqrt(mean(x^2) + eps),  (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s),
+// queries to Q, keys and the unchanged values to slot[t] of the cache. Every
+// value is read once and written once, so the kernel is bound by HBM for
+// prompts and by latency for single tokens.
+
+#include "serq_attn.h"
+
+namespace serq {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 256;
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<float> {
+  static constexpr int kVec = 4;     // elements of a 16-byte chunk
+  static __device__ __forceinline__ void unpack(u32x4 w, float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+  }
+  static __device__ __forceinline__ u32x4 pack(const float (&v)[4]) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[i]);
+    return w;
+  }
+  static __device__ __forceinline__ float load(const float* p) { return *p; }
+  static __device__ __forceinline__ float round(float v) { return v; }
+};
+template <>
+struct Elem<__bf16> {
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ void unpack(u32x4 w, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ u32x4 pack(const float (&v)[8]) {
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bf2 p = {static_cast<__bf16>(v[2 * i]), static_cast<__bf16>(v[2 * i + 1])};
+      w[i] = __builtin_bit_cast(uint32_t, p);
+    }
+    return w;
+  }
+  static __device__ __forceinline__ float load(const __bf16* p) { return static_cast<float>(*p); }
+  static __device__ __forceinline__ __bf16 round(float v) { return static_cast<__bf16>(v); }
+};
+
+// Where token t's keys and values go: element offset of its slot for head 0
+// (heads are D << page_shift apart), or -1.
+__device__ __forceinline__ int64_t slot_base(const RopeArgs& a, int slot, bool pos_ok) {
+  if (!pos_ok || slot < 0 || (slot >> a.page_shift) >= a.n_pages) return -1;
+  const int64_t page = slot >> a.page_shift, in = slot & ((1 << a.page_shift) - 1);
+  return ((page * a.Hkv << a.page_shift) + in) * a.D;
+}
+
+// Vector path: 16-byte aligned rows, rot_dim made of whole chunks in each
+// half (SERQ_ROPE_HALF) or in all (SERQ_ROPE_INTERLEAVED). A head is D / kVec
+// lanes of one chunk each; a workgroup holds 256 / lanes heads and walks its
+// share of the token's heads, so cosines, sines and norm weights, which
+// depend on the lane's place in the head alone, are loaded once. The other
+// half's values come from the lane that holds them.
+template <typename T, int D, bool INTER, bool NORM>
+__global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeArgs a, int heads_per_block) {
+  using E = Elem<T>;
+  constexpr int V = E::kVec, L = D / V, GROUPS = kThreads / L;
+  const int t = blockIdx.x;
+  const int lane = threadIdx.x % L, group = threadIdx.x / L;
+  const int d0 = lane * V;
+  const int heads = a.Hq + 2 * a.Hkv;
+  const int pos = a.rot ? a.pos[t] : 0;
+  const int64_t base = slot_base(a, a.slot[t], !a.rot || (pos >= 0 && pos < a.max_pos));
+  const bool pos_ok = !a.rot || (pos >= 0 && pos < a.max_pos);
+  const bool turned = d0 < a.rot;
+  const int half = a.rot / 2;
+  // y = x A + partner B with A = c, B = -s in the first half of a pair and s in the second
+  float A[V], B[V], wq[V], wk[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) A[i] = 1.0f, B[i] = 0.0f;
+  if (turned && pos_ok) {
+    const float* row = a.table + static_cast<int64_t>(pos) * a.rot;
+    if constexpr (INTER) {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const float c = row[(d0 + i) / 2], s = row[half + (d0 + i) / 2];
+        A[i] = A[i + 1] = c;
+        B[i] = -s;
+        B[i + 1] = s;
+      }
+    } else {
+      const bool second = d0 >= half;
+      const int i0 = second ? d0 - half : d0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        A[i] = row[i0 + i];
+        const float s = row[half + i0 + i];
+        B[i] = second ? s : -s;
+      }
+    }
+  }
+  if constexpr (NORM) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      wq[i] = a.q_norm ? a.q_norm[d0 + i] : 1.0f;
+      wk[i] = a.k_norm ? a.k_norm[d0 + i] : 1.0f;
+    }
+  }
+  const int step = half / V;                     // lanes to the other half
+  const int mate = INTER || !turned ? lane : (d0 < half ? lane + step : lane - step);
+  const int first = blockIdx.y * heads_per_block;
+  const int last = first + heads_per_block < heads ? first + heads_per_block : heads;
+  const T* in = static_cast<const T*>(a.QKV) + t * a.ld;
+  for (int h = first + group; h < last; h += GROUPS) {
+    const u32x4 raw = *reinterpret_cast<const u32x4*>(in + h * D + d0);
+    const bool key = h >= a.Hq, value = h >= a.Hq + a.Hkv;
+    u32x4 out = raw;
+    if (!value) {
+      float x[V], y[V];
+      E::unpack(raw, x);
+      if constexpr (NORM) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) ss = __builtin_fmaf(x[i], x[i], ss);
+#pragma unroll
+        for (int off = L / 2; off > 0; off >>= 1) ss += __shfl_xor(ss, off, L);
+        if (key ? a.k_norm != nullptr : a.q_norm != nullptr) {
+          const float r = 1.0f / __builtin_sqrtf(ss * (1.0f / D) + a.eps);
+#pragma unroll
+          for (int i = 0; i < V; ++i) x[i] *= r * (key ? wk[i] : wq[i]);
+        }
+      }
+      if constexpr (INTER) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] = x[i ^ 1];
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] = __shfl(x[i], mate, L);
+      }
+      if (turned) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = __builtin_fmaf(x[i], A[i], y[i] * B[i]);
+      }
+      if (!pos_ok) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = __builtin_nanf("");
+      }
+      out = E::pack(x);
+    }
+    if (!key) {
+      *reinterpret_cast<u32x4*>(static_cast<T*>(a.Q) + t * a.ldq + h * D + d0) = out;
+    } else if (base >= 0) {
+      const int kvh = h - a.Hq - (value ? a.Hkv : 0);
+      T* c = static_cast<T*>(value ? a.Vc : a.Kc);
+      *reinterpret_cast<u32x4*>(c + base + (static_cast<int64_t>(kvh) << a.page_shift) * D + d0) = out;
+    }
+  }
+}
+
+// Scalar path, any row alignment and rot_dim: one wave per head, values
+// d = lane + 64 e; partners are exchanged between lanes, so every value is
+// read before any is written (Q may be QKV).
+template <typename T, int D>
+__global__ __launch_bounds__(64) void rope_append_scalar_kernel(RopeArgs a) {
+  using E = Elem<T>;
+  constexpr int N = D / 64;
+  const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x;
+  const int pos = a.rot ? a.pos[t] : 0;
+  const bool pos_ok = !a.rot || (pos >= 0 && pos < a.max_pos);
+  const int64_t base = slot_base(a, a.slot[t], pos_ok);
+  const bool key = h >= a.Hq, value = h >= a.Hq + a.Hkv;
+  const T* in = static_cast<const T*>(a.QKV) + t * a.ld + static_cast<int64_t>(h) * D;
+  float x[N];
+  T raw[N];
+  float ss = 0.0f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    raw[e] = in[lane + 64 * e];
+    x[e] = E::load(&raw[e]);
+    ss = __builtin_fmaf(x[e], x[e], ss);
+  }
+  if (!value) {
+    const float* w = key ? a.k_norm : a.q_norm;
+    if (w) {
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) ss += __shfl_xor(ss, off, 64);
+      const float r = 1.0f / __builtin_sqrtf(ss * (1.0f / D) + a.eps);
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[e] *= r * w[lane + 64 * e];
+    }
+    const int half = a.rot / 2;
+    float y[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const int d = lane + 64 * e;
+      const int m = d >= a.rot ? d : a.interleaved ? d ^ 1 : d < half ? d + half : d - half;
+      float p = 0.0f;
+#pragma unroll
+      for (int f = 0; f < N; ++f) {
+        const float v = __shfl(x[f], m & 63, 64);
+        if (m / 64 == f) p = v;
+      }
+      y[e] = x[e];
+      if (d < a.rot && pos_ok) {
+        const float* row = a.table + static_cast<int64_t>(pos) * a.rot;
+        const bool second = a.interleaved ? (d & 1) : d >= half;
+        const int i = a.interleaved ? d / 2 : second ? d - half : d;
+        const float s = row[half + i];
+        y[e] = __builtin_fmaf(x[e], row[i], p * (second ? s : -s));
+      }
+      if (!pos_ok) y[e] = __builtin_nanf("");
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) raw[e] = E::round(y[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int d = lane + 64 * e;
+    if (!key) {
+      static_cast<T*>(a.Q)[t * a.ldq + static_cast<int64_t>(h) * D + d] = raw[e];
+    } else if (base >= 0) {
+      const int kvh = h - a.Hq - (value ? a.Hkv : 0);
+      static_cast<T*>(value ? a.Vc : a.Kc)[base + (static_cast<int64_t>(kvh) << a.page_shift) * D + d] = raw[e];
+    }
+  }
+}
+
+template <typename T, int D, bool INTER>
+void launch_vector(const RopeArgs& a, hipStream_t st) {
+  constexpr int GROUPS = kThreads / (D / Elem<T>::kVec);
+  const int heads = a.Hq + 2 * a.Hkv;
+  const int per = GROUPS;
+  const dim3 grid(a.M, (heads + per - 1) / per);
+  if (a.q_norm || a.k_norm) rope_append_kernel<T, D, INTER, true><<<grid, kThreads, 0, st>>>(a, per);
+  else rope_append_kernel<T, D, INTER, false><<<grid, kThreads, 0, st>>>(a, per);
+}
+
+template <typename T, int D>
+hipError_t launch_typed(const RopeArgs& a, hipStream_t st) {
+  constexpr int V = Elem<T>::kVec;
+  auto al16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  const bool whole = a.interleaved ? a.rot % V == 0 : a.rot % (2 * V) == 0;
+  const bool vec = whole && al16(a.QKV) && a.ld % V == 0 && (a.Hq == 0 || (al16(a.Q) && a.ldq % V == 0));
+  if (!vec) {
+    const dim3 grid(a.M, a.Hq + 2 * a.Hkv);
+    rope_append_scalar_kernel<T, D><<<grid, 64, 0, st>>>(a);
+  } else if (a.interleaved) {
+    launch_vector<T, D, true>(a, st);
+  } else {
+    launch_vector<T, D, false>(a, st);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rope_append(const RopeArgs& a, hipStream_t st) {
+  if (a.bf16) return a.D == 64 ? launch_typed<__bf16, 64>(a, st) : launch_typed<__bf16, 128>(a, st);
+  return a.D == 64 ? launch_typed<float, 64>(a, st) : launch_typed<float, 128>(a, st);
+}
+
+}  // namespace serq
