@@ -29,7 +29,7 @@ LIB = os.path.join(PKG, "libserq.so")
 ARCH = os.environ.get("SERQ_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["serq_abi.cpp", "calibrate.cpp", "quant_act.hip", "serq_gemm.hip", "serq_mx.hip",
-           "attn_abi.cpp", "rope_table.cpp", "rope_append.hip", "attention.hip"]
+           "attn_abi.cpp", "rope_table.cpp", "rope_append.hip", "attention.hip", "attn_tile.hip"]
 
 
 def hipcc() -> str:

@@ -15,27 +15,12 @@
 // (4 g .. 4 g + 3 of each tile) as its summation slots, and the values are
 // loaded to match. Scores never pass through LDS.
 
-#include "serq_attn.h"
+#include "attn_common.h"
 
 namespace serq {
 namespace {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
-constexpr float kNone = -__builtin_inff();
-
-__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const bf16x2 p = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
-  return __builtin_bit_cast(uint32_t, p);
-}
-
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+using namespace attn;
 
 // Maximum (sum) over the four lane groups that share a query.
 __device__ __forceinline__ float max_groups(float v) {
@@ -46,10 +31,6 @@ __device__ __forceinline__ float sum_groups(float v) {
   v += __shfl_xor(v, 16, 64);
   return v + __shfl_xor(v, 32, 64);
 }
-
-// The reference of the exponentials: the running maximum, or 0 while no
-// score but -inf has been seen (2^(-inf - 0) = 0).
-__device__ __forceinline__ float ref(float m) { return m == kNone ? 0.0f : m; }
 
 // One sequence's pages of one key/value head, for one wave.
 template <typename T, int D>
@@ -65,9 +46,7 @@ struct Pages {
   __device__ __forceinline__ int64_t at(int key) const {
     int i = key >> shift;
     i = uniform(i < last ? i : last);
-    int page = table[i];
-    page = page < 0 ? 0 : page >= n_pages ? n_pages - 1 : page;
-    page = uniform(page);
+    const int page = uniform(page_id(table, i, n_pages));
     return (((static_cast<int64_t>(page) * Hkv + h) << shift) + (key & ((1 << shift) - 1))) * D;
   }
 };
@@ -353,24 +332,6 @@ struct Rows<float, D> {
   __device__ __forceinline__ void store_f32(float* row, int g) const { store(row, g, 1.0f); }
 };
 
-// Partial results of a row and part, in the caller's workspace: D sums, then
-// (m, l) pairs after all sums.
-struct Parts {
-  float* o;        // rows x splits x D
-  float2* ml;      // rows x splits
-  int splits;
-};
-
-__device__ __forceinline__ int bounded_len(const AttnArgs& a, int b) {
-  const int n = a.kv_len[b];
-  return n < 0 ? 0 : n < a.max_len ? n : a.max_len;
-}
-
-__device__ __forceinline__ int bounded_cu(const AttnArgs& a, int i) {
-  const int n = a.cu_q[i];
-  return n < 0 ? 0 : n < a.T ? n : a.T;
-}
-
 // ------------------------------------------------------------------ prefill
 
 constexpr int kPrefillWaves = 4;
@@ -424,7 +385,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves) void attn_prefill_kernel(AttnAr
     r.store_f32(parts.o + slot * D, g);
     if (g == 0) parts.ml[slot] = float2{r.m, l};
   } else {
-    r.store(static_cast<T*>(a.O) + row * a.ldo + static_cast<int64_t>(h) * D, g, l > 0.0f || l != l ? 1.0f / l : 0.0f);
+    r.store(static_cast<T*>(a.O) + row * a.ldo + static_cast<int64_t>(h) * D, g, inverse(l));
   }
 }
 
@@ -516,7 +477,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void attn_decode_kernel(AttnArgs
       *reinterpret_cast<f32x4*>(parts.o + slot * D + d + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
     if (d == 0) parts.ml[slot] = float2{m, l};
   } else {
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    const float inv = inverse(l);
     T* out = static_cast<T*>(a.O) + bq * a.ldo + static_cast<int64_t>(hq) * D + d;
 #pragma unroll
     for (int i = 0; i < W; ++i) out[i] = static_cast<T>(o[i] * inv);
@@ -562,7 +523,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int psplits,
 #pragma unroll
     for (int i = 0; i < W; ++i) o[i] = __builtin_fmaf(f, po[static_cast<int64_t>(s) * D + i], o[i]);
   }
-  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  const float inv = inverse(l);
   T* out = static_cast<T*>(a.O) + t * a.ldo + static_cast<int64_t>(h) * D + lane * W;
 #pragma unroll
   for (int i = 0; i < W; ++i) out[i] = static_cast<T>(o[i] * inv);
@@ -604,13 +565,15 @@ inline int cut(int len, int64_t& splits) {
 }  // namespace
 
 PrefillPlan plan_prefill(int bf16, int B, int T, int Hq, int Hkv, int D, int max_len) {
-  (void)bf16;
   PrefillPlan p{};
   const int G = Hq / Hkv;
-  p.pack = G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1;
-  const int tile_pos = 16 * kPrefillWaves / p.pack;
+  p.tiled = bf16;
+  const int most = p.tiled ? 8 : 4;
+  p.pack = G % 8 == 0 && most == 8 ? 8 : G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1;
+  const int tile_pos = (p.tiled ? 256 : 16 * kPrefillWaves) / p.pack;
   const int64_t units = (static_cast<int64_t>(ceil_div(T, tile_pos)) + B) * (Hq / p.pack);
-  int64_t splits = units < 512 ? 1024 / units : 1;
+  const int want = p.tiled ? 256 : 512;
+  int64_t splits = units < want ? 2 * want / units : 1;
   if (splits > max_len / 512) splits = max_len / 512;
   p.chunk = cut(max_len, splits);
   p.splits = static_cast<int>(splits);
@@ -624,9 +587,9 @@ hipError_t launch_attn_prefill(const AttnArgs& a, const PrefillPlan& p, hipStrea
   const int64_t rows = static_cast<int64_t>(a.T) * a.Hq;
   const Parts parts = parts_of(a.workspace, rows, a.D, p.splits);
   const dim3 grid(static_cast<unsigned>(tiles * (a.Hq / p.pack)), p.splits), block(64 * kPrefillWaves);
-  if (a.bf16) {
-    if (a.D == 64) attn_prefill_kernel<__bf16, 64><<<grid, block, 0, st>>>(a, p, parts);
-    else attn_prefill_kernel<__bf16, 128><<<grid, block, 0, st>>>(a, p, parts);
+  if (p.tiled) {
+    const hipError_t e = launch_attn_tile(a, p, parts, st);
+    if (e != hipSuccess) return e;
   } else {
     if (a.D == 64) attn_prefill_kernel<float, 64><<<grid, block, 0, st>>>(a, p, parts);
     else attn_prefill_kernel<float, 128><<<grid, block, 0, st>>>(a, p, parts);

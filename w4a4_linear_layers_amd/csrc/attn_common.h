@@ -1,0 +1,62 @@
+// Device helpers that the attention kernels share.
+#pragma once
+
+#include "serq_attn.h"
+
+namespace serq {
+namespace attn {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kNone = -__builtin_inff();
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const bf16x2 p = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
+  return __builtin_bit_cast(uint32_t, p);
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The reference of the exponentials: the running maximum, or 0 while no
+// score but -inf has been seen (2^(-inf - 0) = 0).
+__device__ __forceinline__ float ref(float m) { return m == kNone ? 0.0f : m; }
+
+// 1 / l, or 0 for a row without keys; NaN stays.
+__device__ __forceinline__ float inverse(float l) { return l > 0.0f || l != l ? 1.0f / l : 0.0f; }
+
+// Partial results of a row and part, in the caller's workspace: D sums, then
+// (m, l) pairs after all sums.
+struct Parts {
+  float* o;        // rows x splits x D
+  float2* ml;      // rows x splits
+  int splits;
+};
+
+__device__ __forceinline__ int bounded_len(const AttnArgs& a, int b) {
+  const int n = a.kv_len[b];
+  return n < 0 ? 0 : n < a.max_len ? n : a.max_len;
+}
+
+__device__ __forceinline__ int bounded_cu(const AttnArgs& a, int i) {
+  const int n = a.cu_q[i];
+  return n < 0 ? 0 : n < a.T ? n : a.T;
+}
+
+// Page `i` of a row of page ids, inside the cache whatever the row says.
+__device__ __forceinline__ int page_id(const int32_t* table, int i, int n_pages) {
+  const int p = table[i];
+  return p < 0 ? 0 : p >= n_pages ? n_pages - 1 : p;
+}
+
+}  // namespace attn
+
+hipError_t launch_attn_tile(const AttnArgs& a, const PrefillPlan& p, const attn::Parts& parts, hipStream_t stream);
+
+}  // namespace serq

@@ -1,0 +1,334 @@
+// serq_attn_prefill for bf16 on LDS tiles (gfx950).
+//
+// One workgroup: eight waves of 32 query rows over the same keys. The rows
+// are `pack` query heads of one group (they share keys and values) times 256
+// / pack positions, so the diagonal wastes little and short sequences fill
+// their tiles. Keys pass in tiles of 64, K and V, through two LDS stages.
+//
+// Both products are taken transposed on v_mfma_f32_32x32x16_bf16: S^T = K Q^T
+// leaves each lane with 32 scores of one query (column = lane % 32) per tile,
+// and those registers, converted in order, are the second operand of O^T =
+// V^T P^T: the index that the instruction sums over may be renamed, so lane
+// half h = lane / 32 takes as its eight slots of 16 keys those it already
+// holds (4 h .. 4 h + 3 and 8 + 4 h .. 8 + 4 h + 3). V^T is read from LDS by
+// the transposing reads in the same order. Softmax statistics are one value
+// per lane, and scores never leave the registers.
+
+#include "attn_common.h"
+
+namespace serq {
+namespace {
+
+using namespace attn;
+
+constexpr int kWaves = 8;
+constexpr int kKeys = 64;          // keys of a tile
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// One 16-byte direct global->LDS load per lane, from sbase + voff (sbase
+// wave-uniform), into the wave's 1 KB chunk at `lds_chunk`: lane i lands at
+// + 16 i. M0 is written here and declared clobbered. The compiler neither
+// counts nor waits for these loads: wait_loads() does.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma16(const void* sbase, uint32_t voff, uint32_t lds_chunk) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(voff), "s"(sbase), "s"(lds_chunk) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// LDS accesses of this wave done, then the workgroup's barrier.
+__device__ __forceinline__ void barrier() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);          // lgkmcnt(0), no vmcnt wait
+  asm volatile("s_barrier" ::: "memory");
+}
+
+__device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                 0);
+}
+
+// Value over both lane halves: maximum or sum of a lane and lane ^ 32.
+__device__ __forceinline__ float max_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// LDS image of a tile: 64 rows of D values. The 16-byte part c of row r lies
+// at part c ^ swizzle(r), so that rows read together fall on different banks:
+// K by reads of one part of 32 rows, V by transposing reads of 64 bytes of
+// four rows.
+template <int D>
+__device__ __forceinline__ int swizzle_k(int r) { return D == 128 ? r & 15 : (r >> 1) & 7; }
+template <int D>
+__device__ __forceinline__ int swizzle_v(int r) { return D == 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2; }
+
+template <int D>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, PrefillPlan p, Parts parts) {
+  constexpr int kRow = 2 * D;                    // bytes of a row
+  constexpr int kTile = kKeys * kRow;            // bytes of a K or V tile
+  constexpr int kStage = 2 * kTile;
+  constexpr int kRows = 1024 / kRow;             // rows of one wave load
+  constexpr int kLoads = kTile / (1024 * kWaves);
+  constexpr int C = D / 16, DB = D / 32;
+  __shared__ __align__(1024) uint8_t smem[2 * kStage];
+
+  const int lane = threadIdx.x & 63, n = lane & 31, half = lane >> 5;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int tile_pos = 32 * kWaves / p.pack;
+  const int units = a.Hq / p.pack;
+  const int unit = blockIdx.x % units;
+  int tile = blockIdx.x / units, b = 0, q0 = 0, nq = 0, tiles = 0;
+  for (; b < a.B; ++b) {
+    q0 = bounded_cu(a, b);
+    nq = bounded_cu(a, b + 1) - q0;
+    tiles = nq > 0 ? (nq + tile_pos - 1) / tile_pos : 0;
+    if (tile < tiles) break;
+    tile -= tiles;
+  }
+  if (b == a.B) return;
+  tile = tiles - 1 - tile;                       // the longest first
+  const int len = bounded_len(a, b);
+  const int head = unit * p.pack + wave % p.pack;
+  const int pos0 = tile * tile_pos + 32 * (wave / p.pack);
+  const int pos = pos0 + n;
+  const int row = q0 + (pos < nq ? pos : nq - 1);
+  const int shift = len - nq + 1;                // keys that position 0 sees
+  const auto sees = [&](int i) { return i + shift < 0 ? 0 : i + shift < len ? i + shift : len; };
+  const int mine = sees(pos), low = sees(pos0), high = pos0 < nq ? sees(pos0 + 31) : 0;
+  const int from = static_cast<int>(blockIdx.y) * p.chunk;
+  int end = sees(tile * tile_pos + tile_pos - 1);  // keys that any row of the workgroup sees
+  if (p.splits > 1 && end > from + p.chunk) end = from + p.chunk;
+
+  // Q as the second operand: lane (query n, half) holds values 16 c + 8 half .. + 7.
+  // A negative scale goes into Q's sign, so the largest product is the largest score.
+  u32x4 q[C];
+  {
+    const __bf16* src = static_cast<const __bf16*>(a.Q) + row * a.ldq + static_cast<int64_t>(head) * D + 8 * half;
+    const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int c = 0; c < C; ++c) q[c] = *reinterpret_cast<const u32x4*>(src + 16 * c) ^ flip;
+  }
+  // (not 0, so that a masked score stays -inf)
+  const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
+
+  f32x16 o[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+  float m = kNone, l = 0.0f;
+
+  const uint32_t lds0 = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)(&smem[0])));
+  const int kvh = head / (a.Hq / a.Hkv);
+  const int32_t* table = a.page_table + static_cast<int64_t>(b) * a.max_pages;
+  const int last = len > 0 ? (len - 1) >> a.page_shift : 0;
+  // this lane's share of a wave load: row lane / (kRow / 16) of kRows, one part
+  const int lr = lane / (kRow / 16), lp = lane % (kRow / 16);
+  uint32_t koff[kLoads], voff[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = kRows * (wave + kWaves * i) + lr;
+    koff[i] = lr * kRow + ((lp ^ swizzle_k<D>(r)) << 4);
+    voff[i] = lr * kRow + ((lp ^ swizzle_v<D>(r)) << 4);
+  }
+  const auto page_of = [&](int key) {
+    const int i = key >> a.page_shift;
+    return page_id(table, i < last ? i : last, a.n_pages);
+  };
+  int pages[kLoads];
+  const auto look_up = [&](int key0) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) pages[i] = page_of(key0 + kRows * (wave + kWaves * i));
+  };
+  const auto load_tile = [&](int key0, int stage) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r0 = kRows * (wave + kWaves * i);
+      const int in = (key0 + r0) & ((1 << a.page_shift) - 1);
+      const int64_t at = (((static_cast<int64_t>(pages[i]) * a.Hkv + kvh) << a.page_shift) + in) * kRow;
+      const uint32_t to = uniform(lds0 + stage * kStage + r0 * kRow);
+      dma16(static_cast<const char*>(a.Kc) + at, koff[i], to);
+      dma16(static_cast<const char*>(a.Vc) + at, voff[i], to + kTile);
+    }
+  };
+
+  // Read addresses. K: part 2 c + half of row n (+ 32): its swizzled place is
+  // that of c = 0 with 2 c flipped in. V: lane i of a group of 16 names 8
+  // bytes of row 4 half + i / 4, of the 16 values d % 32 / 16 = lane / 16 % 2.
+  const int kbase = n * kRow + ((half ^ swizzle_k<D>(n)) << 4);
+  const int vr = 4 * half + ((lane & 15) >> 2);
+  const int vpart = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+  const int vbase = kTile + vr * kRow + ((vpart ^ swizzle_v<D>(vr)) << 4) + 8 * (lane & 1);
+
+  const auto v_operand = [&](int stage, int d, int kb, int t) {
+    const uint8_t* at = smem + stage * kStage + (vbase ^ (d << 6)) + (32 * kb + 16 * t) * kRow;
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at)));
+    const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + 8 * kRow)));
+    return u32x4{x[0], x[1], y[0], y[1]};
+  };
+
+  const auto tile_step = [&](int key0, int stage) {
+    const bool masked = key0 + kKeys > low;
+    f32x16 s[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[kb][i] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        s[kb] = mfma(*reinterpret_cast<const u32x4*>(smem + stage * kStage + (kbase ^ (c << 5)) + 32 * kb * kRow), q[c],
+                     s[kb]);
+    }
+    // register i of block kb is key 32 kb + 8 (i / 4) + 4 half + i % 4
+    if (masked) {
+      const int seen = mine - key0 - 4 * half;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[kb][i] = 32 * kb + 8 * (i / 4) + (i & 3) < seen ? s[kb][i] : kNone;
+    }
+    float top = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(fmaxf(top, s[0][i]), s[1][i]);
+    top = max_halves(top) * scale;
+    // The exponentials' reference need not be the maximum itself: it follows
+    // only where the maximum has outgrown it by 2^8, so that sums and weights
+    // are rarely scaled (weights stay below 2^8, their relative rounding the
+    // same).
+    if (__any(top > m + 8.0f)) {
+      const float mn = top > m + 8.0f ? top : m;       // a query's own scores alone decide
+      const float f = exp2_(m - ref(mn));
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[d] *= f;
+    }
+    const float r = ref(m);
+    u32x4 w[2][2];                       // weights in bf16, as the values they multiply
+    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float x = exp2_(__builtin_fmaf(s[kb][i], scale, -r));
+        const float y = exp2_(__builtin_fmaf(s[kb][i + 1], scale, -r));
+        sum[0] += x;
+        sum[1] += y;
+        w[kb][i / 8][(i / 2) & 3] = pack2(x, y);
+      }
+    }
+    l += sum[0] + sum[1];
+    bool odd = false;
+    if (masked) {
+      bool ok = true;
+#pragma unroll 1
+      for (int d = 0; d < DB; ++d)
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          const u32x4 v = v_operand(stage, d, j / 2, j & 1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ok &= (v[e] & 0x7F80u) != 0x7F80u && (v[e] & 0x7F800000u) != 0x7F800000u;
+        }
+      odd = __any(!ok);
+    }
+    if (!odd) {
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[d] = mfma(v_operand(stage, d, j / 2, j & 1), w[j / 2][j & 1], o[d]);
+    } else {
+      // A value that is not finite lies where some of these queries do not
+      // look, and 0 * inf is not 0: each query takes the product over its own
+      // keys with the others' values cleared.
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        for (int i = 0; i < 32; ++i) {
+          const int seen = __shfl(mine, i, 64) - key0 - 4 * half;
+          f32x16 t = o[d];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            u32x4 v = v_operand(stage, d, j / 2, j & 1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int k0 = 16 * j + 8 * (e / 2) + 2 * (e & 1);
+              v[e] = (k0 < seen ? v[e] & 0xFFFFu : 0u) | (k0 + 1 < seen ? v[e] & 0xFFFF0000u : 0u);
+            }
+            t = mfma(v, w[j / 2][j & 1], t);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[d][e] = n == i ? t[e] : o[d][e];
+        }
+      }
+    }
+  };
+
+  if (from < end) {
+    look_up(from);
+    load_tile(from, 0);
+    look_up(from + kKeys);
+    int stage = 0;
+    for (int key0 = from; key0 < end; key0 += kKeys, stage ^= 1) {
+      wait_loads();
+      barrier();                         // this tile is there, and the other stage is free
+      if (key0 + kKeys < end) {
+        load_tile(key0 + kKeys, stage ^ 1);
+        look_up(key0 + 2 * kKeys);
+      }
+      if (key0 + kKeys > len) {          // what lies past the end may be anything: V there is cleared
+        for (int i = threadIdx.x; i < kTile / 16; i += 64 * kWaves)
+          if (key0 + i / (kRow / 16) >= len)
+            *reinterpret_cast<u32x4*>(smem + stage * kStage + kTile + i * 16) = u32x4{0, 0, 0, 0};
+        barrier();
+      }
+      if (key0 >= high) continue;        // (for this wave alone)
+      tile_step(key0, stage);
+    }
+  }
+
+  l = sum_halves(l);
+  if (pos >= nq) return;
+  // o[d][i]: value 32 d + 8 (i / 4) + 4 half + i % 4 of query n
+  if (p.splits > 1) {
+    if (from >= mine && from > 0) return;            // the join takes only parts that begin before `mine`
+    const int64_t slot = (static_cast<int64_t>(row) * a.Hq + head) * parts.splits + blockIdx.y;
+    float* to = parts.o + slot * D + 4 * half;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<f32x4*>(to + 32 * d + 2 * i) = f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+    if (half == 0) parts.ml[slot] = float2{m, l};
+  } else {
+    const float inv = inverse(l);
+    __bf16* to = static_cast<__bf16*>(a.O) + row * a.ldo + static_cast<int64_t>(head) * D + 4 * half;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<u32x2*>(to + 32 * d + 2 * i) =
+            u32x2{pack2(o[d][i] * inv, o[d][i + 1] * inv), pack2(o[d][i + 2] * inv, o[d][i + 3] * inv)};
+  }
+}
+
+}  // namespace
+
+hipError_t launch_attn_tile(const AttnArgs& a, const PrefillPlan& p, const Parts& parts, hipStream_t st) {
+  const int tile_pos = 32 * kWaves / p.pack;
+  const int64_t tiles = static_cast<int64_t>(a.T / tile_pos) + a.B;      // at least the sum of the sequences' tiles
+  const dim3 grid(static_cast<unsigned>(tiles * (a.Hq / p.pack)), p.splits), block(64 * kWaves);
+  if (a.D == 64) attn_tile_kernel<64><<<grid, block, 0, st>>>(a, p, parts);
+  else attn_tile_kernel<128><<<grid, block, 0, st>>>(a, p, parts);
+  return hipGetLastError();
+}
+
+}  // namespace serq

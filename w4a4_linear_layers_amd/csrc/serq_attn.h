@@ -55,6 +55,7 @@ struct AttnArgs {
 // / pack (or 32 * waves / pack) positions per workgroup, keys in `splits`
 // parts of `chunk`.
 struct PrefillPlan {
+  int tiled;              // on LDS tiles (attn_tile.hip)
   int pack;
   int splits, chunk;
   int64_t bytes;          // workspace
