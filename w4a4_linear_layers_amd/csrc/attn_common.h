@@ -49,9 +49,11 @@ __device__ __forceinline__ int bounded_cu(const AttnArgs& a, int i) {
   return n < 0 ? 0 : n < a.T ? n : a.T;
 }
 
-// Page `i` of a row of page ids, inside the cache whatever the row says.
+// Page `i` (wave-uniform) of a row of page ids, inside the cache whatever the
+// row says. No kernel writes the tables it reads, so this is a scalar load:
+// as a vector load it would wait for the tile loads in flight around it.
 __device__ __forceinline__ int page_id(const int32_t* table, int i, int n_pages) {
-  const int p = table[i];
+  const int p = ((const __attribute__((address_space(4))) int32_t*)table)[i];
   return p < 0 ? 0 : p >= n_pages ? n_pages - 1 : p;
 }
 

@@ -14,6 +14,8 @@
 // the transposing reads in the same order. Softmax statistics are one value
 // per lane, and scores never leave the registers.
 
+#include <type_traits>
+
 #include "attn_common.h"
 
 namespace serq {
@@ -177,8 +179,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
     return u32x4{x[0], x[1], y[0], y[1]};
   };
 
-  const auto tile_step = [&](int key0, int stage) {
-    const bool masked = key0 + kKeys > low;
+  const auto tile_step = [&](int key0, int stage, auto with_mask) {
+    constexpr bool masked = decltype(with_mask)::value;
     f32x16 s[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
@@ -190,7 +192,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
                      s[kb]);
     }
     // register i of block kb is key 32 kb + 8 (i / 4) + 4 half + i % 4
-    if (masked) {
+    if constexpr (masked) {
       const int seen = mine - key0 - 4 * half;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
@@ -229,7 +231,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
     }
     l += sum[0] + sum[1];
     bool odd = false;
-    if (masked) {
+    if constexpr (masked) {
       bool ok = true;
 #pragma unroll 1
       for (int d = 0; d < DB; ++d)
@@ -272,26 +274,36 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
     }
   };
 
+  // Waits for the tile of key0, frees the other stage and starts the next tile there.
+  const auto next_tile = [&](int key0, int stage) {
+    wait_loads();
+    barrier();
+    if (key0 + kKeys < end) {
+      load_tile(key0 + kKeys, stage ^ 1);
+      look_up(key0 + 2 * kKeys);
+    }
+  };
   if (from < end) {
     look_up(from);
     load_tile(from, 0);
     look_up(from + kKeys);
-    int stage = 0;
-    for (int key0 = from; key0 < end; key0 += kKeys, stage ^= 1) {
-      wait_loads();
-      barrier();                         // this tile is there, and the other stage is free
-      if (key0 + kKeys < end) {
-        load_tile(key0 + kKeys, stage ^ 1);
-        look_up(key0 + 2 * kKeys);
-      }
+    int key0 = from, stage = 0;
+    // Tiles that all of the wave's queries see whole, then the others. (The
+    // waves of a workgroup change over at tiles of their own; each passes one
+    // barrier a tile in either loop.)
+    for (; key0 < end && key0 + kKeys <= low; key0 += kKeys, stage ^= 1) {
+      next_tile(key0, stage);
+      tile_step(key0, stage, std::false_type{});
+    }
+    for (; key0 < end; key0 += kKeys, stage ^= 1) {
+      next_tile(key0, stage);
       if (key0 + kKeys > len) {          // what lies past the end may be anything: V there is cleared
         for (int i = threadIdx.x; i < kTile / 16; i += 64 * kWaves)
           if (key0 + i / (kRow / 16) >= len)
             *reinterpret_cast<u32x4*>(smem + stage * kStage + kTile + i * 16) = u32x4{0, 0, 0, 0};
-        barrier();
+        barrier();                       // (low <= len: every wave is in this loop by now)
       }
-      if (key0 >= high) continue;        // (for this wave alone)
-      tile_step(key0, stage);
+      if (key0 < high) tile_step(key0, stage, std::true_type{});
     }
   }
 
