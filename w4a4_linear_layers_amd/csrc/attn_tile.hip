@@ -25,6 +25,7 @@ using namespace attn;
 
 constexpr int kWaves = 8;
 constexpr int kKeys = 64;          // keys of a tile
+constexpr int kRing = 3;           // tiles of K and of V in LDS
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
@@ -41,6 +42,8 @@ __device__ __forceinline__ void dma16(const void* sbase, uint32_t voff, uint32_t
 #pragma clang diagnostic pop
 
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_loads_but() { asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory"); }
 
 // LDS accesses of this wave done, then the workgroup's barrier.
 __device__ __forceinline__ void barrier() {
@@ -76,11 +79,10 @@ template <int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, PrefillPlan p, Parts parts) {
   constexpr int kRow = 2 * D;                    // bytes of a row
   constexpr int kTile = kKeys * kRow;            // bytes of a K or V tile
-  constexpr int kStage = 2 * kTile;
   constexpr int kRows = 1024 / kRow;             // rows of one wave load
   constexpr int kLoads = kTile / (1024 * kWaves);
   constexpr int C = D / 16, DB = D / 32;
-  __shared__ __align__(1024) uint8_t smem[2 * kStage];
+  __shared__ __align__(1024) uint8_t smem[2 * kRing * kTile];   // K tiles, then V tiles
 
   const int lane = threadIdx.x & 63, n = lane & 31, half = lane >> 5;
   const int wave = uniform(threadIdx.x >> 6);
@@ -142,24 +144,37 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
     koff[i] = lr * kRow + ((lp ^ swizzle_k<D>(r)) << 4);
     voff[i] = lr * kRow + ((lp ^ swizzle_v<D>(r)) << 4);
   }
-  const auto page_of = [&](int key) {
-    const int i = key >> a.page_shift;
-    return page_id(table, i < last ? i : last, a.n_pages);
-  };
-  int pages[kLoads];
-  const auto look_up = [&](int key0) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) pages[i] = page_of(key0 + kRows * (wave + kWaves * i));
-  };
-  const auto load_tile = [&](int key0, int stage) {
+  // Byte offsets of a tile's rows in either cache, for this wave's loads.
+  const uint64_t page_bytes = (static_cast<uint64_t>(a.Hkv) << a.page_shift) * kRow;
+  const uint32_t head_bytes = (static_cast<uint32_t>(kvh) << a.page_shift) * kRow;
+  const uint32_t in_mask = (1u << a.page_shift) - 1;
+  const auto look_up = [&](int t, int (&pages)[kLoads]) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int r0 = kRows * (wave + kWaves * i);
-      const int in = (key0 + r0) & ((1 << a.page_shift) - 1);
-      const int64_t at = (((static_cast<int64_t>(pages[i]) * a.Hkv + kvh) << a.page_shift) + in) * kRow;
-      const uint32_t to = uniform(lds0 + stage * kStage + r0 * kRow);
-      dma16(static_cast<const char*>(a.Kc) + at, koff[i], to);
-      dma16(static_cast<const char*>(a.Vc) + at, voff[i], to + kTile);
+      const int x = (from + t * kKeys + kRows * (wave + kWaves * i)) >> a.page_shift;
+      pages[i] = page_id(table, x < last ? x : last, a.n_pages);
+    }
+  };
+  const auto place = [&](const int (&pages)[kLoads], int t, uint64_t (&at)[kLoads]) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      at[i] = static_cast<uint32_t>(pages[i]) * page_bytes +
+              (head_bytes + ((from + t * kKeys + kRows * (wave + kWaves * i)) & in_mask) * kRow);
+  };
+  const auto load_rows = [&](const void* cache, const uint64_t (&at)[kLoads], const uint32_t (&off)[kLoads],
+                             uint32_t to) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      dma16(static_cast<const char*>(cache) + at[i], off[i], uniform(to + 1024 * (wave + kWaves * i)));
+  };
+  // This wave's rows of V tile t that lie past the end, where the cache may
+  // hold anything, cleared (they have landed).
+  const auto clear_v = [&](int t, int slot) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = kRows * (wave + kWaves * i) + lr;
+      if (from + t * kKeys + r >= len)
+        *reinterpret_cast<u32x4*>(smem + (kRing + slot) * kTile + r * kRow + lp * 16) = u32x4{0, 0, 0, 0};
     }
   };
 
@@ -169,31 +184,47 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
   const int kbase = n * kRow + ((half ^ swizzle_k<D>(n)) << 4);
   const int vr = 4 * half + ((lane & 15) >> 2);
   const int vpart = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-  const int vbase = kTile + vr * kRow + ((vpart ^ swizzle_v<D>(vr)) << 4) + 8 * (lane & 1);
+  const int vbase = kRing * kTile + vr * kRow + ((vpart ^ swizzle_v<D>(vr)) << 4) + 8 * (lane & 1);
 
-  const auto v_operand = [&](int stage, int d, int kb, int t) {
-    const uint8_t* at = smem + stage * kStage + (vbase ^ (d << 6)) + (32 * kb + 16 * t) * kRow;
+  const auto v_operand = [&](int slot, int d, int j) {
+    const uint8_t* at = smem + slot * kTile + (vbase ^ (d << 6)) + 16 * j * kRow;
     typedef __attribute__((address_space(3))) s16x4 lds4;
     const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at)));
     const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + 8 * kRow)));
     return u32x4{x[0], x[1], y[0], y[1]};
   };
 
-  const auto tile_step = [&](int key0, int stage, auto with_mask) {
-    constexpr bool masked = decltype(with_mask)::value;
-    f32x16 s[2];
+  f32x16 s[2];                           // scores: register i of block kb is key 32 kb + 8 (i / 4) + 4 half + i % 4
+  u32x4 w[4];                            // weights of 16 keys each, in bf16 as the values they multiply
+
+  const auto scores = [&](int slot) {
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int i = 0; i < 16; ++i) s[0][i] = s[1][i] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[kb][i] = 0.0f;
+    for (int c = 0; c < C; ++c) {
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-        s[kb] = mfma(*reinterpret_cast<const u32x4*>(smem + stage * kStage + (kbase ^ (c << 5)) + 32 * kb * kRow), q[c],
+      for (int kb = 0; kb < 2; ++kb)
+        s[kb] = mfma(*reinterpret_cast<const u32x4*>(smem + slot * kTile + (kbase ^ (c << 5)) + 32 * kb * kRow), q[c],
                      s[kb]);
     }
-    // register i of block kb is key 32 kb + 8 (i / 4) + 4 half + i % 4
-    if constexpr (masked) {
-      const int seen = mine - key0 - 4 * half;
+  };
+
+  // Order of a matrix phase: LDS reads kAhead products before their use.
+  const auto feed_matrix = [&] {
+    constexpr int kAhead = 6, kProducts = 2 * C + 4 * DB;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+#pragma unroll
+    for (int i = 0; i < kProducts; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      if (i + kAhead < 2 * C) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      else if (i + kAhead < kProducts) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    }
+  };
+
+  const auto softmax = [&](int t, auto with_mask) {
+    if constexpr (decltype(with_mask)::value) {
+      const int seen = mine - (from + t * kKeys) - 4 * half;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -216,7 +247,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       for (int d = 0; d < DB; ++d) o[d] *= f;
     }
     const float r = ref(m);
-    u32x4 w[2][2];                       // weights in bf16, as the values they multiply
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
@@ -226,85 +256,142 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
         const float y = exp2_(__builtin_fmaf(s[kb][i + 1], scale, -r));
         sum[0] += x;
         sum[1] += y;
-        w[kb][i / 8][(i / 2) & 3] = pack2(x, y);
+        w[2 * kb + i / 8][(i / 2) & 3] = pack2(x, y);
       }
     }
     l += sum[0] + sum[1];
-    bool odd = false;
-    if constexpr (masked) {
-      bool ok = true;
-#pragma unroll 1
-      for (int d = 0; d < DB; ++d)
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          const u32x4 v = v_operand(stage, d, j / 2, j & 1);
+    // (done in this phase: left to itself the compiler moves them to the weights' use, behind the barrier)
+    asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]), "+v"(l));
+  };
+
+  const auto values = [&](int slot) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) ok &= (v[e] & 0x7F80u) != 0x7F80u && (v[e] & 0x7F800000u) != 0x7F800000u;
-        }
-      odd = __any(!ok);
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[d] = mfma(v_operand(slot, d, j), w[j], o[d]);
+  };
+
+  // The product of a tile that not all queries see whole. Where one of its
+  // values is not finite, 0 * inf would not be 0: each query then takes the
+  // product over its own keys with the others' values cleared.
+  const auto masked_values = [&](int t, int slot) {
+    bool ok = true;
+#pragma unroll 1
+    for (int d = 0; d < DB; ++d)
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        const u32x4 v = v_operand(slot, d, j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ok &= (v[e] & 0x7F80u) != 0x7F80u && (v[e] & 0x7F800000u) != 0x7F800000u;
+      }
+    if (!__any(!ok)) {
+      values(slot);
+      return;
     }
-    if (!odd) {
 #pragma unroll
-      for (int d = 0; d < DB; ++d)
+    for (int d = 0; d < DB; ++d) {
+      for (int i = 0; i < 32; ++i) {
+        const int seen = __shfl(mine, i, 64) - (from + t * kKeys) - 4 * half;
+        f32x16 x = o[d];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[d] = mfma(v_operand(stage, d, j / 2, j & 1), w[j / 2][j & 1], o[d]);
-    } else {
-      // A value that is not finite lies where some of these queries do not
-      // look, and 0 * inf is not 0: each query takes the product over its own
-      // keys with the others' values cleared.
+        for (int j = 0; j < 4; ++j) {
+          u32x4 v = v_operand(slot, d, j);
 #pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        for (int i = 0; i < 32; ++i) {
-          const int seen = __shfl(mine, i, 64) - key0 - 4 * half;
-          f32x16 t = o[d];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            u32x4 v = v_operand(stage, d, j / 2, j & 1);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int k0 = 16 * j + 8 * (e / 2) + 2 * (e & 1);
-              v[e] = (k0 < seen ? v[e] & 0xFFFFu : 0u) | (k0 + 1 < seen ? v[e] & 0xFFFF0000u : 0u);
-            }
-            t = mfma(v, w[j / 2][j & 1], t);
+          for (int e = 0; e < 4; ++e) {
+            const int k0 = 16 * j + 8 * (e / 2) + 2 * (e & 1);
+            v[e] = (k0 < seen ? v[e] & 0xFFFFu : 0u) | (k0 + 1 < seen ? v[e] & 0xFFFF0000u : 0u);
           }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[d][e] = n == i ? t[e] : o[d][e];
+          x = mfma(v, w[j], x);
         }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[d][e] = n == i ? x[e] : o[d][e];
       }
     }
   };
 
-  // Waits for the tile of key0, frees the other stage and starts the next tile there.
-  const auto next_tile = [&](int key0, int stage) {
-    wait_loads();
+  // The waves of a SIMD (w and w + 4) work in opposite phases, so that one
+  // feeds the matrix cores while the other takes its exponentials: a wave's
+  // matrix phase of tile t is S(t) and the product of tile t - 1, its vector
+  // phase the softmax of tile t, with a barrier after each; the second group
+  // runs one phase behind the first. At the start of its vector phase of
+  // tile t the first group starts its share of the loads of K(t + 2) and V(t +
+  // 1), the second, a phase later, of K(t + 3) and V(t + 2), into places whose
+  // tiles both groups are done with. A group waits for a batch a tile later,
+  // when the next one is under way. Every batch has the same number of loads:
+  // past the last tile they fetch its pages again, into places no longer read.
+  const int steps = from < end ? (end - from + kKeys - 1) / kKeys : 0;
+  const bool second = wave >= kWaves / 2;
+  if (steps > 0) {
+    int pages[kLoads];                             // of the K tile after the next to load
+    uint64_t kat[kLoads], vat[kLoads];             // rows of the next K and V tile to load
+    int t = 0, slot = 0, slot1 = 1, slot2 = 2;     // places of tiles t, t + 1, t + 2 (and t - 1)
+    const auto load_k = [&](int at) { load_rows(a.Kc, kat, koff, lds0 + at * kTile); };
+    const auto load_v = [&](int at) { load_rows(a.Vc, vat, voff, lds0 + (kRing + at) * kTile); };
+    const auto advance = [&](int u) {              // to K(u + 1) and V(u)
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) vat[i] = kat[i];
+      place(pages, u + 1, kat);
+      look_up(u + 2, pages);
+    };
+    const auto start_loads = [&](int u, int at1, int at2) {          // K(u + 2), V(u + 1)
+      load_k(at2);
+      load_v(at1);
+      advance(u + 2);
+    };
+    const auto finish_loads = [&] {                // K(t + 1), V(t)
+      wait_loads_but<2 * kLoads>();
+      if (from + (t + 1) * kKeys > len) clear_v(t, slot);
+    };
+    look_up(0, pages);
+    place(pages, 0, kat);
+    look_up(1, pages);
+    load_k(0);
+    advance(0);                                    // K(1), V(0)
+    load_k(1);
+    load_v(0);
+    advance(1);
+    wait_loads_but<2 * kLoads>();
     barrier();
-    if (key0 + kKeys < end) {
-      load_tile(key0 + kKeys, stage ^ 1);
-      look_up(key0 + 2 * kKeys);
+    if (second) {
+      start_loads(0, 1, 2);
+      barrier();
     }
-  };
-  if (from < end) {
-    look_up(from);
-    load_tile(from, 0);
-    look_up(from + kKeys);
-    int key0 = from, stage = 0;
-    // Tiles that all of the wave's queries see whole, then the others. (The
-    // waves of a workgroup change over at tiles of their own; each passes one
-    // barrier a tile in either loop.)
-    for (; key0 < end && key0 + kKeys <= low; key0 += kKeys, stage ^= 1) {
-      next_tile(key0, stage);
-      tile_step(key0, stage, std::false_type{});
-    }
-    for (; key0 < end; key0 += kKeys, stage ^= 1) {
-      next_tile(key0, stage);
-      if (key0 + kKeys > len) {          // what lies past the end may be anything: V there is cleared
-        for (int i = threadIdx.x; i < kTile / 16; i += 64 * kWaves)
-          if (key0 + i / (kRow / 16) >= len)
-            *reinterpret_cast<u32x4*>(smem + stage * kStage + kTile + i * 16) = u32x4{0, 0, 0, 0};
-        barrier();                       // (low <= len: every wave is in this loop by now)
+    const auto after_matrix = [&] {
+      if (second) finish_loads();
+      barrier();
+      start_loads(second ? t + 1 : t, second ? slot2 : slot1, second ? slot : slot2);
+    };
+    const auto after_vector = [&] {
+      if (!second) finish_loads();
+      if (!second || t + 1 < steps) barrier();
+      const int s0 = slot;
+      slot = slot1;
+      slot1 = slot2;
+      slot2 = s0;
+    };
+    for (; t < steps && from + (t + 1) * kKeys <= low; ++t) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (t > 0) {
+        scores(slot);
+        values(slot2);
+        feed_matrix();
+      } else {
+        scores(slot);
       }
-      if (key0 < high) tile_step(key0, stage, std::true_type{});
+      __builtin_amdgcn_sched_barrier(0);
+      after_matrix();
+      softmax(t, std::false_type{});
+      after_vector();
     }
+    for (; t < steps; ++t) {
+      if (from + t * kKeys < high) scores(slot);
+      if (t > 0 && from + (t - 1) * kKeys < high) masked_values(t - 1, slot2);
+      after_matrix();
+      if (from + t * kKeys < high) softmax(t, std::true_type{});
+      after_vector();
+    }
+    if (from + (steps - 1) * kKeys < high) masked_values(steps - 1, slot2);
+    wait_loads();                                  // nothing may land here after the workgroup is gone
   }
 
   l = sum_halves(l);
