@@ -46,7 +46,7 @@ struct Pages {
   __device__ __forceinline__ int64_t at(int key) const {
     int i = key >> shift;
     i = uniform(i < last ? i : last);
-    const int page = uniform(page_id(table, i, n_pages));
+    const int page = uniform(in_cache(page_entry(table, i), n_pages));
     return (((static_cast<int64_t>(page) * Hkv + h) << shift) + (key & ((1 << shift) - 1))) * D;
   }
 };

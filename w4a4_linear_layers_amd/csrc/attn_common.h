@@ -49,12 +49,16 @@ __device__ __forceinline__ int bounded_cu(const AttnArgs& a, int i) {
   return n < 0 ? 0 : n < a.T ? n : a.T;
 }
 
-// Page `i` (wave-uniform) of a row of page ids, inside the cache whatever the
-// row says. No kernel writes the tables it reads, so this is a scalar load:
-// as a vector load it would wait for the tile loads in flight around it.
-__device__ __forceinline__ int page_id(const int32_t* table, int i, int n_pages) {
-  const int p = ((const __attribute__((address_space(4))) int32_t*)table)[i];
-  return p < 0 ? 0 : p >= n_pages ? n_pages - 1 : p;
+// Entry `i` (wave-uniform) of a row of page ids. No kernel writes the tables it
+// reads, so this is a scalar load: as a vector load it would wait for the tile
+// loads in flight around it.
+__device__ __forceinline__ int page_entry(const int32_t* table, int i) {
+  return ((const __attribute__((address_space(4))) int32_t*)table)[i];
+}
+
+// A page inside the cache, whatever the entry says.
+__device__ __forceinline__ int in_cache(int page, int n_pages) {
+  return page < 0 ? 0 : page >= n_pages ? n_pages - 1 : page;
 }
 
 }  // namespace attn

@@ -32,12 +32,14 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // One 16-byte direct global->LDS load per lane, from sbase + voff (sbase
 // wave-uniform), into the wave's 1 KB chunk at `lds_chunk`: lane i lands at
 // + 16 i. M0 is written here and declared clobbered. The compiler neither
-// counts nor waits for these loads: wait_loads() does.
+// counts nor waits for these loads: wait_loads() does. Nor does it order them
+// with LDS reads: they write where no wave reads until the next barrier but
+// one, and barriers and waits order with them (all are volatile).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(const void* sbase, uint32_t voff, uint32_t lds_chunk) {
   asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
-               :: "v"(voff), "s"(sbase), "s"(lds_chunk) : "memory", "m0");
+               :: "v"(voff), "s"(sbase), "s"(lds_chunk) : "m0");
 }
 #pragma clang diagnostic pop
 
@@ -152,20 +154,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int x = (from + t * kKeys + kRows * (wave + kWaves * i)) >> a.page_shift;
-      pages[i] = page_id(table, x < last ? x : last, a.n_pages);
+      pages[i] = page_entry(table, x < last ? x : last);
     }
   };
   const auto place = [&](const int (&pages)[kLoads], int t, uint64_t (&at)[kLoads]) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      at[i] = static_cast<uint32_t>(pages[i]) * page_bytes +
+      at[i] = static_cast<uint32_t>(in_cache(pages[i], a.n_pages)) * page_bytes +
               (head_bytes + ((from + t * kKeys + kRows * (wave + kWaves * i)) & in_mask) * kRow);
-  };
-  const auto load_rows = [&](const void* cache, const uint64_t (&at)[kLoads], const uint32_t (&off)[kLoads],
-                             uint32_t to) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      dma16(static_cast<const char*>(cache) + at[i], off[i], uniform(to + 1024 * (wave + kWaves * i)));
   };
   // This wave's rows of V tile t that lie past the end, where the cache may
   // hold anything, cleared (they have landed).
@@ -264,11 +260,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
     asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]), "+v"(l));
   };
 
-  const auto values = [&](int slot) {
+  const auto values = [&](int slot, auto&& between) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4; ++j) {
 #pragma unroll
       for (int d = 0; d < DB; ++d) o[d] = mfma(v_operand(slot, d, j), w[j], o[d]);
+      between(j);
+    }
   };
 
   // The product of a tile that not all queries see whole. Where one of its
@@ -285,7 +283,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
         for (int e = 0; e < 4; ++e) ok &= (v[e] & 0x7F80u) != 0x7F80u && (v[e] & 0x7F800000u) != 0x7F800000u;
       }
     if (!__any(!ok)) {
-      values(slot);
+      values(slot, [](int) {});
       return;
     }
 #pragma unroll
@@ -313,84 +311,106 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
   // feeds the matrix cores while the other takes its exponentials: a wave's
   // matrix phase of tile t is S(t) and the product of tile t - 1, its vector
   // phase the softmax of tile t, with a barrier after each; the second group
-  // runs one phase behind the first. At the start of its vector phase of
-  // tile t the first group starts its share of the loads of K(t + 2) and V(t +
-  // 1), the second, a phase later, of K(t + 3) and V(t + 2), into places whose
-  // tiles both groups are done with. A group waits for a batch a tile later,
-  // when the next one is under way. Every batch has the same number of loads:
-  // past the last tile they fetch its pages again, into places no longer read.
+  // runs one phase behind the first. In its matrix phase of tile t a wave
+  // starts its share of the loads of K(t + 2) and V(t + 1), into the places of
+  // K(t - 1) and V(t - 2), which both groups are done with; it waits for a
+  // batch a tile later, when the next one is under way, at the end of phase 2
+  // t + 1 in the first group's count (tile t's vector phase there, its matrix
+  // phase in the second group). Every batch has the same number of loads: past
+  // the last tile they fetch its pages again, into places no longer read.
   const int steps = from < end ? (end - from + kKeys - 1) / kKeys : 0;
   const bool second = wave >= kWaves / 2;
   if (steps > 0) {
-    int pages[kLoads];                             // of the K tile after the next to load
-    uint64_t kat[kLoads], vat[kLoads];             // rows of the next K and V tile to load
+    int pages[kLoads];                             // of the next K tile to load
+    uint64_t kat[kLoads], vat[kLoads];             // rows of the K and V tile to load
     int t = 0, slot = 0, slot1 = 1, slot2 = 2;     // places of tiles t, t + 1, t + 2 (and t - 1)
-    const auto load_k = [&](int at) { load_rows(a.Kc, kat, koff, lds0 + at * kTile); };
-    const auto load_v = [&](int at) { load_rows(a.Vc, vat, voff, lds0 + (kRing + at) * kTile); };
-    const auto advance = [&](int u) {              // to K(u + 1) and V(u)
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) vat[i] = kat[i];
-      place(pages, u + 1, kat);
-      look_up(u + 2, pages);
+    const auto load_k = [&](int i, int at) {
+      dma16(static_cast<const char*>(a.Kc) + kat[i], koff[i], uniform(lds0 + at * kTile + 1024 * (wave + kWaves * i)));
     };
-    const auto start_loads = [&](int u, int at1, int at2) {          // K(u + 2), V(u + 1)
-      load_k(at2);
-      load_v(at1);
-      advance(u + 2);
+    const auto load_v = [&](int i, int at) {
+      dma16(static_cast<const char*>(a.Vc) + vat[i], voff[i],
+            uniform(lds0 + (kRing + at) * kTile + 1024 * (wave + kWaves * i)));
     };
-    const auto finish_loads = [&] {                // K(t + 1), V(t)
+    const auto start_load = [&](int j) {           // of 2 kLoads: V(t + 1), K(t + 2)
+      if (j < kLoads) {
+        load_v(j, slot1);
+      } else if (j < 2 * kLoads) {
+        if (j == kLoads) place(pages, t + 2, kat);
+        load_k(j - kLoads, slot2);
+        vat[j - kLoads] = kat[j - kLoads];
+      }
+    };
+    const auto finish_loads = [&](auto tail) {     // K(t + 1), V(t)
       wait_loads_but<2 * kLoads>();
-      if (from + (t + 1) * kKeys > len) clear_v(t, slot);
+      if (decltype(tail)::value && from + (t + 1) * kKeys > len) clear_v(t, slot);
     };
-    look_up(0, pages);
-    place(pages, 0, kat);
-    look_up(1, pages);
-    load_k(0);
-    advance(0);                                    // K(1), V(0)
-    load_k(1);
-    load_v(0);
-    advance(1);
-    wait_loads_but<2 * kLoads>();
-    barrier();
-    if (second) {
-      start_loads(0, 1, 2);
+    const auto after_matrix = [&](bool wait, auto tail) {
+      if (wait) finish_loads(tail);
       barrier();
-    }
-    const auto after_matrix = [&] {
-      if (second) finish_loads();
-      barrier();
-      start_loads(second ? t + 1 : t, second ? slot2 : slot1, second ? slot : slot2);
+      look_up(t + 3, pages);                       // (a scalar load; among LDS reads it would stall them)
     };
-    const auto after_vector = [&] {
-      if (!second) finish_loads();
-      if (!second || t + 1 < steps) barrier();
+    const auto after_vector = [&](bool wait, auto tail) {
+      if (wait) finish_loads(tail);
+      barrier();
       const int s0 = slot;
       slot = slot1;
       slot1 = slot2;
       slot2 = s0;
+      ++t;
     };
-    for (; t < steps && from + (t + 1) * kKeys <= low; ++t) {
-      __builtin_amdgcn_sched_barrier(0);
-      if (t > 0) {
+    look_up(0, pages);
+    place(pages, 0, kat);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) load_k(i, 0);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) vat[i] = kat[i];
+    look_up(1, pages);
+    place(pages, 1, kat);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      load_k(i, 1);
+      load_v(i, 0);
+      vat[i] = kat[i];
+    }
+    look_up(2, pages);
+    wait_loads_but<2 * kLoads>();
+    barrier();
+    if (second) barrier();
+#pragma unroll
+    for (int j = 0; j < 2 * kLoads; ++j) start_load(j);
+    scores(slot);
+    after_matrix(second, std::true_type{});
+    // Tiles that all of the wave's queries see whole, then the others. (The
+    // waves change over at tiles of their own, and pass the same barriers in
+    // either loop.) No whole tile reaches past the end: low <= len.
+    const auto whole_tiles = [&](auto second_group) {
+      constexpr bool kSecond = decltype(second_group)::value;
+      while (t + 1 < steps && from + (t + 1) * kKeys <= low) {
+        softmax(t, std::false_type{});
+        after_vector(!kSecond, std::false_type{});
+        __builtin_amdgcn_sched_barrier(0);
         scores(slot);
-        values(slot2);
+        values(slot2, start_load);
         feed_matrix();
-      } else {
-        scores(slot);
+        __builtin_amdgcn_sched_barrier(0);
+        after_matrix(kSecond, std::true_type{});
       }
-      __builtin_amdgcn_sched_barrier(0);
-      after_matrix();
-      softmax(t, std::false_type{});
-      after_vector();
-    }
-    for (; t < steps; ++t) {
-      if (from + t * kKeys < high) scores(slot);
-      if (t > 0 && from + (t - 1) * kKeys < high) masked_values(t - 1, slot2);
-      after_matrix();
+    };
+    if (second) whole_tiles(std::true_type{});
+    else whole_tiles(std::false_type{});
+    while (true) {
       if (from + t * kKeys < high) softmax(t, std::true_type{});
-      after_vector();
+      after_vector(!second, std::true_type{});
+      if (t < steps) {
+#pragma unroll
+        for (int j = 0; j < 2 * kLoads; ++j) start_load(j);
+        if (from + t * kKeys < high) scores(slot);
+      }
+      if (from + (t - 1) * kKeys < high) masked_values(t - 1, slot2);
+      if (t == steps) break;
+      after_matrix(second, std::true_type{});
     }
-    if (from + (steps - 1) * kKeys < high) masked_values(steps - 1, slot2);
+    if (!second) barrier();                        // the second group's last
     wait_loads();                                  // nothing may land here after the workgroup is gone
   }
 
