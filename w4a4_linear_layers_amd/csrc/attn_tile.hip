@@ -219,6 +219,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
   };
 
   const auto softmax = [&](int t, auto with_mask) {
+    asm volatile("" : "+v"(s[0]), "+v"(s[1]));       // (not before: the compiler would start it among the products)
     if constexpr (decltype(with_mask)::value) {
       const int seen = mine - (from + t * kKeys) - 4 * half;
 #pragma unroll
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       }
     }
     l += sum[0] + sum[1];
-    // (done in this phase: left to itself the compiler moves them to the weights' use, behind the barrier)
+    // (done in this phase: left to itself the compiler moves them to the weights' use)
     asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]), "+v"(l));
   };
 
@@ -308,16 +309,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
   };
 
   // The waves of a SIMD (w and w + 4) work in opposite phases, so that one
-  // feeds the matrix cores while the other takes its exponentials: a wave's
+  // feeds the matrix cores while the other takes its exponentials. A wave's
   // matrix phase of tile t is S(t) and the product of tile t - 1, its vector
-  // phase the softmax of tile t, with a barrier after each; the second group
-  // runs one phase behind the first. In its matrix phase of tile t a wave
-  // starts its share of the loads of K(t + 2) and V(t + 1), into the places of
-  // K(t - 1) and V(t - 2), which both groups are done with; it waits for a
-  // batch a tile later, when the next one is under way, at the end of phase 2
-  // t + 1 in the first group's count (tile t's vector phase there, its matrix
-  // phase in the second group). Every batch has the same number of loads: past
-  // the last tile they fetch its pages again, into places no longer read.
+  // phase the softmax of tile t. Period t, with one barrier at its end, is
+  // matrix phase t and vector phase t in the first group of four waves, vector
+  // phase t - 1 and matrix phase t in the second.
+  //
+  // In its matrix phase of tile t a wave starts its share of the loads of K(t
+  // + 2) and V(t + 1), into the places of K(t - 1) and V(t - 2), last read in
+  // period t - 1; at the end of period t it waits for the batch before, K(t +
+  // 1) and V(t). Every batch has the same number of loads: past the last tile
+  // they fetch its pages again, into places no longer read.
   const int steps = from < end ? (end - from + kKeys - 1) / kKeys : 0;
   const bool second = wave >= kWaves / 2;
   if (steps > 0) {
@@ -344,14 +346,18 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       wait_loads_but<2 * kLoads>();
       if (decltype(tail)::value && from + (t + 1) * kKeys > len) clear_v(t, slot);
     };
-    const auto after_matrix = [&](bool wait, auto tail) {
-      if (wait) finish_loads(tail);
-      barrier();
+    const auto after_matrix = [&](bool ends) {
+      if (ends) {
+        finish_loads(std::true_type{});
+        barrier();
+      }
       look_up(t + 3, pages);                       // (a scalar load; among LDS reads it would stall them)
     };
-    const auto after_vector = [&](bool wait, auto tail) {
-      if (wait) finish_loads(tail);
-      barrier();
+    const auto after_vector = [&](bool ends, auto tail) {
+      if (ends) {
+        finish_loads(tail);
+        barrier();
+      }
       const int s0 = slot;
       slot = slot1;
       slot1 = slot2;
@@ -375,11 +381,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
     look_up(2, pages);
     wait_loads_but<2 * kLoads>();
     barrier();
-    if (second) barrier();
 #pragma unroll
     for (int j = 0; j < 2 * kLoads; ++j) start_load(j);
     scores(slot);
-    after_matrix(second, std::true_type{});
+    after_matrix(second);
     // Tiles that all of the wave's queries see whole, then the others. (The
     // waves change over at tiles of their own, and pass the same barriers in
     // either loop.) No whole tile reaches past the end: low <= len.
@@ -388,12 +393,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       while (t + 1 < steps && from + (t + 1) * kKeys <= low) {
         softmax(t, std::false_type{});
         after_vector(!kSecond, std::false_type{});
+        __builtin_amdgcn_s_setprio(1);
         __builtin_amdgcn_sched_barrier(0);
         scores(slot);
         values(slot2, start_load);
         feed_matrix();
         __builtin_amdgcn_sched_barrier(0);
-        after_matrix(kSecond, std::true_type{});
+        __builtin_amdgcn_s_setprio(0);
+        after_matrix(kSecond);
       }
     };
     if (second) whole_tiles(std::true_type{});
@@ -408,9 +415,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       }
       if (from + (t - 1) * kKeys < high) masked_values(t - 1, slot2);
       if (t == steps) break;
-      after_matrix(second, std::true_type{});
+      after_matrix(second);
     }
-    if (!second) barrier();                        // the second group's last
     wait_loads();                                  // nothing may land here after the workgroup is gone
   }
 
