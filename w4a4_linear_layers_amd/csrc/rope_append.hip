@@ -14,6 +14,7 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
+constexpr int kFewTokens = 256;      // below: a workgroup per set of heads
 
 template <typename T>
 struct Elem;
@@ -67,20 +68,30 @@ __device__ __forceinline__ int64_t slot_base(const RopeArgs& a, int slot, bool p
 
 // Vector path: 16-byte aligned rows, rot_dim made of whole chunks in each
 // half (SERQ_ROPE_HALF) or in all (SERQ_ROPE_INTERLEAVED). A head is D / kVec
-// lanes of one chunk each; a workgroup holds 256 / lanes heads and walks its
-// share of the token's heads, so cosines, sines and norm weights, which
-// depend on the lane's place in the head alone, are loaded once. The other
-// half's values come from the lane that holds them.
-template <typename T, int D, bool INTER, bool NORM>
-__global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeArgs a, int heads_per_block) {
+// lanes of one chunk each; a workgroup holds 256 / lanes heads of one token
+// at a time and NB such sets, all of whose loads it starts before the first
+// use, since the cosines and sines come only after the position they belong
+// to. What depends on the lane's place in the head alone (cosines, sines, norm
+// weights) is loaded once for all its heads; the other half's values come from
+// the lane that holds them.
+template <typename T, int D, bool INTER, bool NORM, int NB>
+__global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeArgs a) {
   using E = Elem<T>;
   constexpr int V = E::kVec, L = D / V, GROUPS = kThreads / L;
   const int t = blockIdx.x;
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
   const int d0 = lane * V;
   const int heads = a.Hq + 2 * a.Hkv;
+  const int first = blockIdx.y * (GROUPS * NB) + group;
+  const T* in = static_cast<const T*>(a.QKV) + t * a.ld + d0;
+  u32x4 raw[NB];
+#pragma unroll
+  for (int k = 0; k < NB; ++k) {
+    const int h = first + GROUPS * k;
+    if (h < heads) raw[k] = *reinterpret_cast<const u32x4*>(in + static_cast<int64_t>(h) * D);
+  }
+  const int slot = a.slot[t];
   const int pos = a.rot ? a.pos[t] : 0;
-  const int64_t base = slot_base(a, a.slot[t], !a.rot || (pos >= 0 && pos < a.max_pos));
   const bool pos_ok = !a.rot || (pos >= 0 && pos < a.max_pos);
   const bool turned = d0 < a.rot;
   const int half = a.rot / 2;
@@ -116,18 +127,18 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeArgs a, int h
       wk[i] = a.k_norm ? a.k_norm[d0 + i] : 1.0f;
     }
   }
+  const int64_t base = slot_base(a, slot, pos_ok);
   const int step = half / V;                     // lanes to the other half
   const int mate = INTER || !turned ? lane : (d0 < half ? lane + step : lane - step);
-  const int first = blockIdx.y * heads_per_block;
-  const int last = first + heads_per_block < heads ? first + heads_per_block : heads;
-  const T* in = static_cast<const T*>(a.QKV) + t * a.ld;
-  for (int h = first + group; h < last; h += GROUPS) {
-    const u32x4 raw = *reinterpret_cast<const u32x4*>(in + h * D + d0);
+#pragma unroll
+  for (int k = 0; k < NB; ++k) {
+    const int h = first + GROUPS * k;
+    if (h >= heads) break;
     const bool key = h >= a.Hq, value = h >= a.Hq + a.Hkv;
-    u32x4 out = raw;
+    u32x4 out = raw[k];
     if (!value) {
       float x[V], y[V];
-      E::unpack(raw, x);
+      E::unpack(raw[k], x);
       if constexpr (NORM) {
         float ss = 0.0f;
 #pragma unroll
@@ -158,7 +169,7 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeArgs a, int h
       out = E::pack(x);
     }
     if (!key) {
-      *reinterpret_cast<u32x4*>(static_cast<T*>(a.Q) + t * a.ldq + h * D + d0) = out;
+      *reinterpret_cast<u32x4*>(static_cast<T*>(a.Q) + t * a.ldq + static_cast<int64_t>(h) * D + d0) = out;
     } else if (base >= 0) {
       const int kvh = h - a.Hq - (value ? a.Hkv : 0);
       T* c = static_cast<T*>(value ? a.Vc : a.Kc);
@@ -235,14 +246,15 @@ __global__ __launch_bounds__(64) void rope_append_scalar_kernel(RopeArgs a) {
   }
 }
 
-template <typename T, int D, bool INTER>
+template <typename T, int D, bool INTER, bool NORM>
 void launch_vector(const RopeArgs& a, hipStream_t st) {
   constexpr int GROUPS = kThreads / (D / Elem<T>::kVec);
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int per = GROUPS;
-  const dim3 grid(a.M, (heads + per - 1) / per);
-  if (a.q_norm || a.k_norm) rope_append_kernel<T, D, INTER, true><<<grid, kThreads, 0, st>>>(a, per);
-  else rope_append_kernel<T, D, INTER, false><<<grid, kThreads, 0, st>>>(a, per);
+  const int sets = (a.Hq + 2 * a.Hkv + GROUPS - 1) / GROUPS;
+  if (a.M < kFewTokens || sets == 1) {
+    rope_append_kernel<T, D, INTER, NORM, 1><<<dim3(a.M, sets), kThreads, 0, st>>>(a);
+  } else {
+    rope_append_kernel<T, D, INTER, NORM, 3><<<dim3(a.M, (sets + 2) / 3), kThreads, 0, st>>>(a);
+  }
 }
 
 template <typename T, int D>
@@ -254,10 +266,10 @@ hipError_t launch_typed(const RopeArgs& a, hipStream_t st) {
   if (!vec) {
     const dim3 grid(a.M, a.Hq + 2 * a.Hkv);
     rope_append_scalar_kernel<T, D><<<grid, 64, 0, st>>>(a);
-  } else if (a.interleaved) {
-    launch_vector<T, D, true>(a, st);
   } else {
-    launch_vector<T, D, false>(a, st);
+    const bool norm = a.q_norm || a.k_norm;
+    if (a.interleaved) norm ? launch_vector<T, D, true, true>(a, st) : launch_vector<T, D, true, false>(a, st);
+    else norm ? launch_vector<T, D, false, true>(a, st) : launch_vector<T, D, false, false>(a, st);
   }
   return hipGetLastError();
 }
