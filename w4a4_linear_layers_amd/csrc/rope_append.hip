@@ -58,6 +58,21 @@ struct Elem<__bf16> {
   static __device__ __forceinline__ __bf16 round(float v) { return static_cast<__bf16>(v); }
 };
 
+// N floats in 8- or 16-byte loads (the table's rows and the norms are 16-byte
+// aligned where the vector path runs): one dword a load, the sixteen cosines
+// and sines and sixteen weights of a lane cost more than its data.
+template <int N>
+__device__ __forceinline__ void load_floats(const float* p, float (&v)[N]) {
+  typedef float f32xk __attribute__((ext_vector_type(N < 4 ? N : 4)));
+  constexpr int K = N < 4 ? N : 4;
+#pragma unroll
+  for (int i = 0; i < N; i += K) {
+    const f32xk x = *reinterpret_cast<const f32xk*>(p + i);
+#pragma unroll
+    for (int j = 0; j < K; ++j) v[i + j] = x[j];
+  }
+}
+
 // Where token t's keys and values go: element offset of its slot for head 0
 // (heads are D << page_shift apart), or -1.
 __device__ __forceinline__ int64_t slot_base(const RopeArgs& a, int slot, bool pos_ok) {
@@ -102,30 +117,28 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeArgs a) {
   if (turned && pos_ok) {
     const float* row = a.table + static_cast<int64_t>(pos) * a.rot;
     if constexpr (INTER) {
+      float c[V / 2], s[V / 2];
+      load_floats<V / 2>(row + d0 / 2, c);
+      load_floats<V / 2>(row + half + d0 / 2, s);
 #pragma unroll
-      for (int i = 0; i < V; i += 2) {
-        const float c = row[(d0 + i) / 2], s = row[half + (d0 + i) / 2];
-        A[i] = A[i + 1] = c;
-        B[i] = -s;
-        B[i + 1] = s;
+      for (int i = 0; i < V; ++i) {
+        A[i] = c[i / 2];
+        B[i] = i & 1 ? s[i / 2] : -s[i / 2];
       }
     } else {
       const bool second = d0 >= half;
       const int i0 = second ? d0 - half : d0;
+      load_floats<V>(row + i0, A);
+      load_floats<V>(row + half + i0, B);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        A[i] = row[i0 + i];
-        const float s = row[half + i0 + i];
-        B[i] = second ? s : -s;
-      }
+      for (int i = 0; i < V; ++i) B[i] = second ? B[i] : -B[i];
     }
   }
   if constexpr (NORM) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      wq[i] = a.q_norm ? a.q_norm[d0 + i] : 1.0f;
-      wk[i] = a.k_norm ? a.k_norm[d0 + i] : 1.0f;
-    }
+    for (int i = 0; i < V; ++i) wq[i] = wk[i] = 1.0f;
+    if (a.q_norm) load_floats<V>(a.q_norm + d0, wq);
+    if (a.k_norm) load_floats<V>(a.k_norm + d0, wk);
   }
   const int64_t base = slot_base(a, slot, pos_ok);
   const int step = half / V;                     // lanes to the other half
@@ -146,7 +159,7 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeArgs a) {
 #pragma unroll
         for (int off = L / 2; off > 0; off >>= 1) ss += __shfl_xor(ss, off, L);
         if (key ? a.k_norm != nullptr : a.q_norm != nullptr) {
-          const float r = 1.0f / __builtin_sqrtf(ss * (1.0f / D) + a.eps);
+          const float r = __builtin_amdgcn_rsqf(ss * (1.0f / D) + a.eps);
 #pragma unroll
           for (int i = 0; i < V; ++i) x[i] *= r * (key ? wk[i] : wq[i]);
         }
@@ -205,7 +218,7 @@ __global__ __launch_bounds__(64) void rope_append_scalar_kernel(RopeArgs a) {
     if (w) {
 #pragma unroll
       for (int off = 32; off > 0; off >>= 1) ss += __shfl_xor(ss, off, 64);
-      const float r = 1.0f / __builtin_sqrtf(ss * (1.0f / D) + a.eps);
+      const float r = __builtin_amdgcn_rsqf(ss * (1.0f / D) + a.eps);
 #pragma unroll
       for (int e = 0; e < N; ++e) x[e] *= r * w[lane + 64 * e];
     }
