@@ -19,18 +19,13 @@ from . import _lib
 from ._lib import SERQ_BF16, SERQ_EINVAL, SERQ_F32, SerqError, check
 
 lib = _lib.lib
+try:
+    import torch
+except ImportError:  # pragma: no cover - library use without PyTorch
+    torch = None
 
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
-
-
-def _dtype(t, what):
-    import torch
-    if t.dtype == torch.bfloat16:
-        return SERQ_BF16
-    if t.dtype == torch.float32:
-        return SERQ_F32
-    raise ValueError(f"{what} must be float32 or bfloat16")
 
 
 @dataclass
@@ -44,17 +39,24 @@ class KvCache:
 
     def __post_init__(self):
         k, v = self.k, self.v
-        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+        shape = k.shape
+        if len(shape) != 4 or shape != v.shape or k.dtype is not v.dtype or k.device != v.device:
             raise ValueError("k and v must be (pages, kv heads, page size, head dim) tensors alike")
         if not k.is_cuda or not k.is_contiguous() or not v.is_contiguous():
             raise ValueError("device tensors must be contiguous CUDA tensors")
-        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
-        self.dtype = _dtype(k, "the cache")
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = shape
+        self.torch_dtype = k.dtype
+        if k.dtype is torch.bfloat16:
+            self.dtype = SERQ_BF16
+        elif k.dtype is torch.float32:
+            self.dtype = SERQ_F32
+        else:
+            raise ValueError("the cache must be float32 or bfloat16")
+        self.pointers = k.data_ptr(), v.data_ptr()
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, *, dtype=None, device="cuda"):
         """A cache of uninitialised pages (bfloat16 unless ``dtype`` says otherwise)."""
-        import torch
         shape = (n_pages, n_kv_heads, page_size, head_dim)
         dtype = torch.bfloat16 if dtype is None else dtype
         return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
@@ -75,49 +77,66 @@ def rope_table(rot_dim: int, max_pos: int, *, theta: float = 10000.0, scaling: s
     return t
 
 
+# The current stream's handle. torch.cuda.current_stream() builds a Stream
+# object around it, which takes longer than the smallest of these kernels.
+_raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
+
+
 def _stream(t):
-    import torch
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+# The checks below run on every call of a decoding step, where a handful of
+# microseconds is what the kernels take: each attribute is read once.
+
 def _ints(t, shape, what):
-    import torch
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous CUDA int32 tensor of shape {shape}")
     return t.data_ptr()
 
 
-def _rows(t, cache, what):
+def _rows(t, shape, cache, what):
     """Row stride of a (rows, heads, head dim) tensor whose rows are whole."""
-    if t.dim() != 3 or t.shape[2] != cache.head_dim or not t.is_cuda or t.dtype != cache.k.dtype:
+    n, h, d = shape
+    if d != cache.head_dim or t.dtype is not cache.torch_dtype or not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA (rows, heads, {cache.head_dim}) tensor of the cache's dtype")
-    n, h, d = t.shape
     s0, s1, s2 = t.stride()
-    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
+    if s2 != 1 or (s1 != d and h > 1):
         raise ValueError(f"{what}: heads must lie one after another in a row")
     return s0 if n > 1 else h * d
 
 
-def _out(out, q, cache):
-    import torch
+def _shape3(t, what):
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{what} must be (rows, heads, head dim)")
+    return shape
+
+
+def _out(out, q, shape, cache):
+    """(output, its row stride)"""
     if out is None:
-        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if out.shape != q.shape:
-        raise ValueError(f"out must be of shape {tuple(q.shape)}")
-    return out
+        return torch.empty(shape, dtype=q.dtype, device=q.device), shape[1] * shape[2]
+    if out.shape != shape:
+        raise ValueError(f"out must be of shape {tuple(shape)}")
+    return out, _rows(out, shape, cache, "out")
 
 
 def _space(workspace, need, q):
-    import torch
-    if need < 0:
-        raise ValueError("sizes that the library does not take")
-    if need == 0:
-        return None, 0
+    """(tensor that holds it, address, bytes)"""
+    if need <= 0:
+        if need < 0:
+            raise ValueError("sizes that the library does not take")
+        return None, None, 0
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
+        return workspace, workspace.data_ptr(), need
+    size = workspace.numel() * workspace.element_size()
+    if not workspace.is_cuda or not workspace.is_contiguous() or size < need:
         raise ValueError(f"workspace must be a contiguous CUDA tensor of {need} bytes or more")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), size
 
 
 def rope_append(qkv, n_heads: int, cache: KvCache, pos, slot, table, *, layout: str = "half", q_norm=None, k_norm=None,
@@ -127,35 +146,38 @@ def rope_append(qkv, n_heads: int, cache: KvCache, pos, slot, table, *, layout: 
     (n_heads + 2 kv heads) * head dim (unit column stride), ``pos`` and
     ``slot`` M int32, ``table`` (max_pos, rot_dim) float32 on the device or
     None for no rotation. Returns M x n_heads x head dim."""
-    import torch
-    if qkv.dim() != 2 or not qkv.is_cuda or qkv.dtype != cache.k.dtype:
+    shape = qkv.shape
+    if len(shape) != 2 or not qkv.is_cuda or qkv.dtype is not cache.torch_dtype:
         raise ValueError("qkv must be a two-dimensional CUDA tensor of the cache's dtype")
-    M, width = qkv.shape
+    M, width = shape
     D, Hkv = cache.head_dim, cache.n_kv_heads
-    if width != (n_heads + 2 * Hkv) * D or (M > 0 and qkv.stride(1) != 1):
+    ld, unit = qkv.stride()
+    if width != (n_heads + 2 * Hkv) * D or (unit != 1 and M > 0):
         raise ValueError(f"qkv must have {(n_heads + 2 * Hkv) * D} columns of unit stride")
-    ld = qkv.stride(0) if M > 1 else width
+    if M <= 1:
+        ld = width
     if layout not in _LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}")
     rot = max_pos = 0
+    tp = pp = None
     if table is not None:
-        if table.dim() != 2 or table.dtype != torch.float32 or not table.is_cuda or not table.is_contiguous():
+        if table.dtype is not torch.float32 or table.dim() != 2 or not table.is_cuda or not table.is_contiguous():
             raise ValueError("table must be a contiguous CUDA (max_pos, rot_dim) float32 tensor")
         max_pos, rot = table.shape
-    for w in (q_norm, k_norm):
-        if w is not None and (w.dtype != torch.float32 or not w.is_cuda or not w.is_contiguous() or w.numel() != D):
-            raise ValueError(f"norms must be contiguous CUDA float32 tensors of {D}")
-    pp = _ints(pos, (M,), "pos") if rot else None
+        if rot:
+            tp, pp = table.data_ptr(), _ints(pos, (M,), "pos")
+    wp = [None, None]
+    for i, w in enumerate((q_norm, k_norm)):
+        if w is not None:
+            if w.dtype is not torch.float32 or w.shape != (D,) or not w.is_cuda or not w.is_contiguous():
+                raise ValueError(f"norms must be contiguous CUDA float32 tensors of {D}")
+            wp[i] = w.data_ptr()
     sp = _ints(slot, (M,), "slot")
-    q = torch.empty((M, n_heads, D), dtype=qkv.dtype, device=qkv.device) if out is None else out
-    if out is not None and tuple(out.shape) != (M, n_heads, D):
-        raise ValueError(f"out must be of shape {(M, n_heads, D)}")
-    ldq = _rows(q, cache, "out")
+    q, ldq = _out(out, qkv, (M, n_heads, D), cache)
+    kc, vc = cache.pointers
     check("serq_rope_append", lib.serq_rope_append(
-        qkv.data_ptr(), cache.dtype, ld, M, n_heads, Hkv, D, q_norm.data_ptr() if q_norm is not None else None,
-        k_norm.data_ptr() if k_norm is not None else None, eps, table.data_ptr() if rot else None, rot, max_pos,
-        _LAYOUTS[layout], pp, sp, q.data_ptr(), ldq, cache.k.data_ptr(), cache.v.data_ptr(), cache.n_pages,
-        cache.page_size, _stream(qkv)))
+        qkv.data_ptr(), cache.dtype, ld, M, n_heads, Hkv, D, wp[0], wp[1], eps, tp, rot, max_pos, _LAYOUTS[layout], pp,
+        sp, q.data_ptr(), ldq, kc, vc, cache.n_pages, cache.page_size, _stream(qkv)))
     return q
 
 
@@ -172,19 +194,23 @@ def attn_prefill(q, cu_q, cache: KvCache, page_table, kv_len, *, max_len: int, s
     device; ``max_len`` bounds kv_len; ``scale`` is head_dim ** -0.5 unless
     given. A workspace is taken from torch's allocator unless given. Returns
     T x heads x head dim."""
-    ldq = _rows(q, cache, "q")
-    T, Hq, D = q.shape
-    B, wide = page_table.shape
+    shape = _shape3(q, "q")
+    ldq = _rows(q, shape, cache, "q")
+    T, Hq, D = shape
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be sequences x pages")
+    pages = page_table.shape
+    B = pages[0]
+    tp = _ints(page_table, pages, "page_table")
     cp = _ints(cu_q, (B + 1,), "cu_q")
-    tp = _ints(page_table, (B, wide), "page_table")
     kp = _ints(kv_len, (B,), "kv_len")
-    o = _out(out, q, cache)
-    ldo = _rows(o, cache, "out")
-    ws, size = _space(workspace, attn_prefill_workspace(cache, B, T, Hq, max_len), q)
+    o, ldo = _out(out, q, shape, cache)
+    Hkv = cache.n_kv_heads
+    kc, vc = cache.pointers
+    hold, wp, size = _space(workspace, lib.serq_attn_prefill_workspace(cache.dtype, B, T, Hq, Hkv, D, max_len), q)
     check("serq_attn_prefill", lib.serq_attn_prefill(
-        q.data_ptr(), cache.dtype, ldq, cp, B, T, Hq, cache.n_kv_heads, D, cache.k.data_ptr(), cache.v.data_ptr(),
-        cache.n_pages, cache.page_size, tp, wide, kp, max_len, D ** -0.5 if scale is None else scale, o.data_ptr(),
-        ldo, ws.data_ptr() if size else None, size, _stream(q)))
+        q.data_ptr(), cache.dtype, ldq, cp, B, T, Hq, Hkv, D, kc, vc, cache.n_pages, cache.page_size, tp, pages[1], kp,
+        max_len, D ** -0.5 if scale is None else scale, o.data_ptr(), ldo, wp, size, _stream(q)))
     return o
 
 
@@ -201,24 +227,25 @@ def attn_decode(q, cache: KvCache, page_table, kv_len, *, max_len: int, prefix=N
     and ``kv_len`` B int32 give each sequence's own tokens, ``prefix`` (int32
     page ids) and ``prefix_len`` the tokens that all of them share before
     those. Returns B x heads x head dim."""
-    ldq = _rows(q, cache, "q")
-    B, Hq, D = q.shape
-    if page_table.dim() != 2 or page_table.shape[0] != B:
+    shape = _shape3(q, "q")
+    ldq = _rows(q, shape, cache, "q")
+    B, Hq, D = shape
+    pages = page_table.shape
+    if len(pages) != 2 or pages[0] != B:
         raise ValueError(f"page_table must be {B} x pages")
-    wide = page_table.shape[1]
-    tp = _ints(page_table, (B, wide), "page_table")
+    tp = _ints(page_table, pages, "page_table")
     kp = _ints(kv_len, (B,), "kv_len")
     pp = None
     if prefix_len > 0:
-        pages = -(-prefix_len // cache.page_size)
-        if prefix is None or prefix.numel() < pages:
-            raise ValueError(f"prefix must hold {pages} page ids")
+        need = -(-prefix_len // cache.page_size)
+        if prefix is None or prefix.numel() < need:
+            raise ValueError(f"prefix must hold {need} page ids")
         pp = _ints(prefix, (prefix.numel(),), "prefix")
-    o = _out(out, q, cache)
-    ldo = _rows(o, cache, "out")
-    ws, size = _space(workspace, attn_decode_workspace(cache, B, Hq, prefix_len, max_len), q)
+    o, ldo = _out(out, q, shape, cache)
+    Hkv = cache.n_kv_heads
+    kc, vc = cache.pointers
+    hold, wp, size = _space(workspace, lib.serq_attn_decode_workspace(cache.dtype, B, Hq, Hkv, D, prefix_len, max_len), q)
     check("serq_attn_decode", lib.serq_attn_decode(
-        q.data_ptr(), cache.dtype, ldq, B, Hq, cache.n_kv_heads, D, cache.k.data_ptr(), cache.v.data_ptr(),
-        cache.n_pages, cache.page_size, pp, prefix_len, tp, wide, kp, max_len, D ** -0.5 if scale is None else scale,
-        o.data_ptr(), ldo, ws.data_ptr() if size else None, size, _stream(q)))
+        q.data_ptr(), cache.dtype, ldq, B, Hq, Hkv, D, kc, vc, cache.n_pages, cache.page_size, pp, prefix_len, tp,
+        pages[1], kp, max_len, D ** -0.5 if scale is None else scale, o.data_ptr(), ldo, wp, size, _stream(q)))
     return o

@@ -513,16 +513,37 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int psplits,
   const int own = keys > 0 ? (keys - 1) / chunk + 1 : 0, count = psplits + own;
   const float2* ml = parts.ml + row * parts.splits;
   const float* po = parts.o + row * parts.splits * D + lane * W;
+  // The parts' maxima and sums by lanes, 64 at a time; then their sums of
+  // values, eight loads in flight.
   float m = kNone;
-  for (int s = 0; s < count; ++s) m = fmaxf(m, ml[s].x);
+  for (int s = lane; s < count; s += 64) m = fmaxf(m, ml[s].x);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
   const float r = ref(m);
   float l = 0.0f, o[W] = {};
-  for (int s = 0; s < count; ++s) {
-    const float f = exp2_(ml[s].x - r);
-    l = __builtin_fmaf(f, ml[s].y, l);
+  for (int s0 = 0; s0 < count; s0 += 64) {
+    const int n = count - s0 < 64 ? count - s0 : 64;
+    const float2 x = lane < n ? ml[s0 + lane] : float2{kNone, 0.0f};
+    const float f = exp2_(x.x - r);                // this lane's part's weight
+    l = __builtin_fmaf(f, x.y, l);
+    for (int s = 0; s < n; s += 8) {
+      float v[8][W];
 #pragma unroll
-    for (int i = 0; i < W; ++i) o[i] = __builtin_fmaf(f, po[static_cast<int64_t>(s) * D + i], o[i]);
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[k][i] = s + k < n ? po[static_cast<int64_t>(s0 + s + k) * D + i] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float w = __shfl(f, (s + k) & 63, 64);
+        if (s + k < n) {
+#pragma unroll
+          for (int i = 0; i < W; ++i) o[i] = __builtin_fmaf(w, v[k][i], o[i]);
+        }
+      }
+    }
   }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) l += __shfl_xor(l, off, 64);
   const float inv = inverse(l);
   T* out = static_cast<T*>(a.O) + t * a.ldo + static_cast<int64_t>(h) * D + lane * W;
 #pragma unroll
@@ -552,10 +573,12 @@ inline int64_t parts_bytes(int64_t rows, int D, int splits) {
 
 inline int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-// `splits` parts of [0, len), each a multiple of 128 keys; returns the chunk
-// and leaves in splits how many of them there are.
+// At most `splits` parts of [0, len), each a multiple of 128 keys; returns the
+// part's size and leaves in splits how many there are.
+constexpr int kMostSplits = 128;
 inline int cut(int len, int64_t& splits) {
   if (splits < 1) splits = 1;
+  if (splits > kMostSplits) splits = kMostSplits;
   int chunk = ceil_div(ceil_div(len, splits), 128) * 128;
   if (chunk < 128) chunk = 128;
   splits = len > 0 ? ceil_div(len, chunk) : 1;
@@ -604,7 +627,7 @@ DecodePlan plan_decode(int bf16, int B, int Hq, int Hkv, int D, int prefix_len, 
   const int G = Hq / Hkv;
   p.tiles = ceil_div(G, 16);
   p.ptiles = prefix_len > 0 ? ceil_div(static_cast<int64_t>(B) * G, 16) : 0;
-  int64_t s = ceil_div(1024, static_cast<int64_t>(B) * Hkv * p.tiles);
+  int64_t s = ceil_div(8192, static_cast<int64_t>(B) * Hkv * p.tiles);
   p.chunk = cut(max_len, s);
   p.splits = static_cast<int>(s);
   if (prefix_len > 0) {
