@@ -486,16 +486,11 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void attn_decode_kernel(AttnArgs
 
 // --------------------------------------------------------------------- join
 
-// One wave per row: the parts of its keys joined in their order. Rows of a
-// prefill see parts that begin before their own limit, rows of a decode the
-// prefix parts and those that begin before the sequence's length.
-template <typename T, int D, bool PREFILL>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int psplits, int chunk, Parts parts) {
-  constexpr int W = D / 64;
-  const int lane = threadIdx.x & 63;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + uniform(threadIdx.x >> 6);
-  const int t = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
-  if (t >= (PREFILL ? a.T : a.B)) return;
+// The parts of a row's keys joined in their order. Rows of a prefill see parts
+// that begin before their own limit, rows of a decode the prefix parts and
+// those that begin before the sequence's length.
+template <bool PREFILL>
+__device__ __forceinline__ int parts_of_row(const AttnArgs& a, int t, int psplits, int chunk) {
   int keys;
   if constexpr (PREFILL) {
     int b = 0, q1 = 0, q0 = 0;
@@ -504,13 +499,25 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int psplits,
       q1 = bounded_cu(a, b + 1);
       if (t >= q0 && t < q1) break;
     }
-    if (b == a.B) return;
+    if (b == a.B) return -1;
     const int64_t first = static_cast<int64_t>(bounded_len(a, b)) - (q1 - q0) + 1;
     keys = static_cast<int>(first + (t - q0) < 0 ? 0 : first + (t - q0));
   } else {
     keys = bounded_len(a, t);
   }
-  const int own = keys > 0 ? (keys - 1) / chunk + 1 : 0, count = psplits + own;
+  return psplits + (keys > 0 ? (keys - 1) / chunk + 1 : 0);
+}
+
+// Many rows: one wave each.
+template <typename T, int D, bool PREFILL>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int psplits, int chunk, Parts parts) {
+  constexpr int W = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + uniform(threadIdx.x >> 6);
+  const int t = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
+  if (t >= (PREFILL ? a.T : a.B)) return;
+  const int count = parts_of_row<PREFILL>(a, t, psplits, chunk);
+  if (count < 0) return;
   const float2* ml = parts.ml + row * parts.splits;
   const float* po = parts.o + row * parts.splits * D + lane * W;
   // The parts' maxima and sums by lanes, 64 at a time; then their sums of
@@ -550,15 +557,91 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int psplits,
   for (int i = 0; i < W; ++i) out[i] = static_cast<T>(o[i] * inv);
 }
 
+// Few rows: a workgroup each, D / 8 lanes to a part, so that the whole row is
+// in flight at once. At most 256 parts (2 kMostSplits).
+constexpr int kMostSplits = 128;
+template <typename T, int D, bool PREFILL>
+__global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs a, int psplits, int chunk, Parts parts) {
+  constexpr int L = D / 8, GROUPS = 256 / L;
+  static_assert(2 * kMostSplits <= 256, "a thread per part");
+  __shared__ float weight[256], so[GROUPS][D], red[2][4];
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const int64_t row = blockIdx.x;
+  const int t = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
+  const int count = parts_of_row<PREFILL>(a, t, psplits, chunk);
+  if (count < 0) return;
+  const float2 x = tid < count ? parts.ml[row * parts.splits + tid] : float2{kNone, 0.0f};
+  const int group = tid / L, d = tid % L * 8;
+  const float* po = parts.o + row * parts.splits * D + d;
+  f32x4 v[2][2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int s = group + GROUPS * k;
+    if (s < count) {
+      v[k][0] = *reinterpret_cast<const f32x4*>(po + static_cast<int64_t>(s) * D);
+      v[k][1] = *reinterpret_cast<const f32x4*>(po + static_cast<int64_t>(s) * D + 4);
+    }
+  }
+  float m = x.x;
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  if ((tid & 63) == 0) red[0][wave] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  const float f = exp2_(x.x - ref(m));
+  weight[tid] = f;
+  float l = f * x.y;
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) l += __shfl_xor(l, off, 64);
+  if ((tid & 63) == 0) red[1][wave] = l;
+  __syncthreads();
+  l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  float o[8] = {};
+  for (int s = group, k = 0; s < count; s += GROUPS, ++k) {
+    f32x4 p, q;
+    if (k < 2) {
+      p = k ? v[1][0] : v[0][0];
+      q = k ? v[1][1] : v[0][1];
+    } else {
+      p = *reinterpret_cast<const f32x4*>(po + static_cast<int64_t>(s) * D);
+      q = *reinterpret_cast<const f32x4*>(po + static_cast<int64_t>(s) * D + 4);
+    }
+    const float w = weight[s];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[i] = __builtin_fmaf(w, p[i], o[i]);
+      o[4 + i] = __builtin_fmaf(w, q[i], o[4 + i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) *reinterpret_cast<f32x4*>(&so[group][d + i]) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
+  __syncthreads();
+  if (tid >= D) return;
+  float y = 0.0f;
+#pragma unroll
+  for (int k = 0; k < GROUPS; ++k) y += so[k][tid];
+  static_cast<T*>(a.O)[t * a.ldo + static_cast<int64_t>(h) * D + tid] = static_cast<T>(y * inverse(l));
+}
+
+constexpr int64_t kFewRows = 2048;
+
+template <typename T, int D, bool PREFILL>
+void launch_join_typed(const AttnArgs& a, int64_t rows, int psplits, int chunk, const Parts& parts, hipStream_t st) {
+  if (rows <= kFewRows)
+    attn_join_few_kernel<T, D, PREFILL><<<dim3(static_cast<unsigned>(rows)), 256, 0, st>>>(a, psplits, chunk, parts);
+  else
+    attn_join_kernel<T, D, PREFILL><<<dim3(static_cast<unsigned>((rows + 3) / 4)), 256, 0, st>>>(a, psplits, chunk,
+                                                                                                 parts);
+}
+
 template <bool PREFILL>
 void launch_join(const AttnArgs& a, int64_t rows, int psplits, int chunk, const Parts& parts, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
   if (a.bf16) {
-    if (a.D == 64) attn_join_kernel<__bf16, 64, PREFILL><<<grid, 256, 0, st>>>(a, psplits, chunk, parts);
-    else attn_join_kernel<__bf16, 128, PREFILL><<<grid, 256, 0, st>>>(a, psplits, chunk, parts);
+    if (a.D == 64) launch_join_typed<__bf16, 64, PREFILL>(a, rows, psplits, chunk, parts, st);
+    else launch_join_typed<__bf16, 128, PREFILL>(a, rows, psplits, chunk, parts, st);
   } else {
-    if (a.D == 64) attn_join_kernel<float, 64, PREFILL><<<grid, 256, 0, st>>>(a, psplits, chunk, parts);
-    else attn_join_kernel<float, 128, PREFILL><<<grid, 256, 0, st>>>(a, psplits, chunk, parts);
+    if (a.D == 64) launch_join_typed<float, 64, PREFILL>(a, rows, psplits, chunk, parts, st);
+    else launch_join_typed<float, 128, PREFILL>(a, rows, psplits, chunk, parts, st);
   }
 }
 
@@ -575,7 +658,6 @@ inline int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) 
 
 // At most `splits` parts of [0, len), each a multiple of 128 keys; returns the
 // part's size and leaves in splits how many there are.
-constexpr int kMostSplits = 128;
 inline int cut(int len, int64_t& splits) {
   if (splits < 1) splits = 1;
   if (splits > kMostSplits) splits = kMostSplits;
