@@ -405,7 +405,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void attn_decode_kernel(AttnArgs
   const int wave = uniform(threadIdx.x >> 6);
   const int G = a.Hq / a.Hkv;
   int x = blockIdx.x;
-  const int nprefix = a.Hkv * p.ptiles * p.psplits;
+  const int nprefix = p.ptiled ? 0 : a.Hkv * p.ptiles * p.psplits;
   const bool prefix = x < nprefix;
   int kvh, R0, rows, part, len, from, to;
   const int32_t* table;
@@ -656,18 +656,21 @@ inline int64_t parts_bytes(int64_t rows, int D, int splits) {
 
 inline int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-// At most `splits` parts of [0, len), each a multiple of 128 keys; returns the
+// At most `splits` parts of [0, len), each a multiple of `unit` keys; returns the
 // part's size and leaves in splits how many there are.
-inline int cut(int len, int64_t& splits) {
+inline int cut(int len, int64_t& splits, int unit = 128) {
   if (splits < 1) splits = 1;
   if (splits > kMostSplits) splits = kMostSplits;
-  int chunk = ceil_div(ceil_div(len, splits), 128) * 128;
-  if (chunk < 128) chunk = 128;
+  int chunk = ceil_div(ceil_div(len, splits), unit) * unit;
+  if (chunk < unit) chunk = unit;
   splits = len > 0 ? ceil_div(len, chunk) : 1;
   return chunk;
 }
 
 }  // namespace
+
+constexpr int kTileRows = 256;       // rows of a workgroup of the tile kernel
+constexpr int kPrefixTileRows = 96;  // rows a key/value head from which the prefix goes there
 
 PrefillPlan plan_prefill(int bf16, int B, int T, int Hq, int Hkv, int D, int max_len) {
   PrefillPlan p{};
@@ -693,7 +696,7 @@ hipError_t launch_attn_prefill(const AttnArgs& a, const PrefillPlan& p, hipStrea
   const Parts parts = parts_of(a.workspace, rows, a.D, p.splits);
   const dim3 grid(static_cast<unsigned>(tiles * (a.Hq / p.pack)), p.splits), block(64 * kPrefillWaves);
   if (p.tiled) {
-    const hipError_t e = launch_attn_tile(a, p, parts, st);
+    const hipError_t e = launch_attn_tile(a, TileShape{p.pack, p.splits, p.chunk}, parts, st);
     if (e != hipSuccess) return e;
   } else {
     if (a.D == 64) attn_prefill_kernel<float, 64><<<grid, block, 0, st>>>(a, p, parts);
@@ -704,17 +707,18 @@ hipError_t launch_attn_prefill(const AttnArgs& a, const PrefillPlan& p, hipStrea
 }
 
 DecodePlan plan_decode(int bf16, int B, int Hq, int Hkv, int D, int prefix_len, int max_len) {
-  (void)bf16;
   DecodePlan p{};
   const int G = Hq / Hkv;
+  const int64_t rows = static_cast<int64_t>(B) * G;
   p.tiles = ceil_div(G, 16);
-  p.ptiles = prefix_len > 0 ? ceil_div(static_cast<int64_t>(B) * G, 16) : 0;
   int64_t s = ceil_div(8192, static_cast<int64_t>(B) * Hkv * p.tiles);
   p.chunk = cut(max_len, s);
   p.splits = static_cast<int>(s);
   if (prefix_len > 0) {
-    s = ceil_div(1024, static_cast<int64_t>(Hkv) * p.ptiles);
-    p.pchunk = cut(prefix_len, s);
+    p.ptiled = bf16 && rows >= kPrefixTileRows;
+    p.ptiles = ceil_div(rows, p.ptiled ? kTileRows : 16);
+    s = ceil_div(p.ptiled ? 256 : 1024, static_cast<int64_t>(Hkv) * p.ptiles);
+    p.pchunk = cut(prefix_len, s, p.ptiled ? 64 : 128);
     p.psplits = static_cast<int>(s);
   }
   p.bytes = parts_bytes(static_cast<int64_t>(B) * Hq, D, p.splits + p.psplits);
@@ -724,7 +728,11 @@ DecodePlan plan_decode(int bf16, int B, int Hq, int Hkv, int D, int prefix_len, 
 hipError_t launch_attn_decode(const AttnArgs& a, const DecodePlan& p, hipStream_t st) {
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
   const Parts parts = parts_of(a.workspace, rows, a.D, p.splits + p.psplits);
-  const int64_t blocks = static_cast<int64_t>(a.Hkv) * p.ptiles * p.psplits +
+  if (p.ptiled) {
+    const hipError_t e = launch_attn_prefix_tile(a, TileShape{1, p.psplits, p.pchunk}, parts, st);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t blocks = (p.ptiled ? 0 : static_cast<int64_t>(a.Hkv) * p.ptiles * p.psplits) +
                          static_cast<int64_t>(a.B) * p.tiles * a.Hkv * p.splits;
   const dim3 grid(static_cast<unsigned>(blocks)), block(64 * kDecodeWaves);
   if (a.bf16) {

@@ -63,6 +63,13 @@ __device__ __forceinline__ int in_cache(int page, int n_pages) {
 
 }  // namespace attn
 
-hipError_t launch_attn_tile(const AttnArgs& a, const PrefillPlan& p, const attn::Parts& parts, hipStream_t stream);
+// What the tile kernel needs of a plan.
+struct TileShape {
+  int pack;            // query heads of a group per workgroup (prefill)
+  int splits, chunk;   // parts of the keys
+};
+
+hipError_t launch_attn_tile(const AttnArgs& a, const TileShape& p, const attn::Parts& parts, hipStream_t stream);
+hipError_t launch_attn_prefix_tile(const AttnArgs& a, const TileShape& p, const attn::Parts& parts, hipStream_t stream);
 
 }  // namespace serq

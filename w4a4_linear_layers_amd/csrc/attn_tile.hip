@@ -77,8 +77,11 @@ __device__ __forceinline__ int swizzle_k(int r) { return D == 128 ? r & 15 : (r 
 template <int D>
 __device__ __forceinline__ int swizzle_v(int r) { return D == 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2; }
 
-template <int D>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, PrefillPlan p, Parts parts) {
+// PREFIX: the prefix part of serq_attn_decode instead. The rows are those of
+// all sequences (row R: sequence R / G, head R % G of the group), 256 to a
+// workgroup, and all of them see all keys.
+template <int D, bool PREFIX>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, TileShape p, Parts parts) {
   constexpr int kRow = 2 * D;                    // bytes of a row
   constexpr int kTile = kKeys * kRow;            // bytes of a K or V tile
   constexpr int kRows = 1024 / kRow;             // rows of one wave load
@@ -88,29 +91,48 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
 
   const int lane = threadIdx.x & 63, n = lane & 31, half = lane >> 5;
   const int wave = uniform(threadIdx.x >> 6);
-  const int tile_pos = 32 * kWaves / p.pack;
-  const int units = a.Hq / p.pack;
-  const int unit = blockIdx.x % units;
-  int tile = blockIdx.x / units, b = 0, q0 = 0, nq = 0, tiles = 0;
-  for (; b < a.B; ++b) {
-    q0 = bounded_cu(a, b);
-    nq = bounded_cu(a, b + 1) - q0;
-    tiles = nq > 0 ? (nq + tile_pos - 1) / tile_pos : 0;
-    if (tile < tiles) break;
-    tile -= tiles;
-  }
-  if (b == a.B) return;
-  tile = tiles - 1 - tile;                       // the longest first
-  const int len = bounded_len(a, b);
-  const int head = unit * p.pack + wave % p.pack;
-  const int pos0 = tile * tile_pos + 32 * (wave / p.pack);
-  const int pos = pos0 + n;
-  const int row = q0 + (pos < nq ? pos : nq - 1);
-  const int shift = len - nq + 1;                // keys that position 0 sees
-  const auto sees = [&](int i) { return i + shift < 0 ? 0 : i + shift < len ? i + shift : len; };
-  const int mine = sees(pos), low = sees(pos0), high = pos0 < nq ? sees(pos0 + 31) : 0;
+  const int G = a.Hq / a.Hkv;
   const int from = static_cast<int>(blockIdx.y) * p.chunk;
-  int end = sees(tile * tile_pos + tile_pos - 1);  // keys that any row of the workgroup sees
+  int row, head, kvh, len, mine, low, high, end;
+  bool valid;
+  const int32_t* table;
+  if constexpr (PREFIX) {
+    kvh = blockIdx.x % a.Hkv;
+    const int rows = a.B * G, R0 = static_cast<int>(blockIdx.x / a.Hkv) * (32 * kWaves) + 32 * wave;
+    valid = R0 + n < rows;
+    const int R = valid ? R0 + n : rows - 1;
+    row = R / G;
+    head = kvh * G + R % G;
+    len = mine = low = end = a.prefix_len;
+    high = R0 < rows ? len : 0;
+    table = a.prefix_table;
+  } else {
+    const int tile_pos = 32 * kWaves / p.pack;
+    const int units = a.Hq / p.pack;
+    const int unit = blockIdx.x % units;
+    int tile = blockIdx.x / units, b = 0, q0 = 0, nq = 0, tiles = 0;
+    for (; b < a.B; ++b) {
+      q0 = bounded_cu(a, b);
+      nq = bounded_cu(a, b + 1) - q0;
+      tiles = nq > 0 ? (nq + tile_pos - 1) / tile_pos : 0;
+      if (tile < tiles) break;
+      tile -= tiles;
+    }
+    if (b == a.B) return;
+    tile = tiles - 1 - tile;                     // the longest first
+    len = bounded_len(a, b);
+    head = unit * p.pack + wave % p.pack;
+    kvh = head / G;
+    const int pos0 = tile * tile_pos + 32 * (wave / p.pack);
+    const int pos = pos0 + n;
+    valid = pos < nq;
+    row = q0 + (valid ? pos : nq - 1);
+    const int shift = len - nq + 1;              // keys that position 0 sees
+    const auto sees = [&](int i) { return i + shift < 0 ? 0 : i + shift < len ? i + shift : len; };
+    mine = sees(pos), low = sees(pos0), high = pos0 < nq ? sees(pos0 + 31) : 0;
+    end = sees(tile * tile_pos + tile_pos - 1);  // keys that any row of the workgroup sees
+    table = a.page_table + static_cast<int64_t>(b) * a.max_pages;
+  }
   if (p.splits > 1 && end > from + p.chunk) end = from + p.chunk;
 
   // Q as the second operand: lane (query n, half) holds values 16 c + 8 half .. + 7.
@@ -134,8 +156,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
 
   const uint32_t lds0 = static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)(&smem[0])));
-  const int kvh = head / (a.Hq / a.Hkv);
-  const int32_t* table = a.page_table + static_cast<int64_t>(b) * a.max_pages;
   const int last = len > 0 ? (len - 1) >> a.page_shift : 0;
   // this lane's share of a wave load: row lane / (kRow / 16) of kRows, one part
   const int lr = lane / (kRow / 16), lp = lane % (kRow / 16);
@@ -421,10 +441,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
   }
 
   l = sum_halves(l);
-  if (pos >= nq) return;
+  if (!valid) return;
   // o[d][i]: value 32 d + 8 (i / 4) + 4 half + i % 4 of query n
-  if (p.splits > 1) {
-    if (from >= mine && from > 0) return;            // the join takes only parts that begin before `mine`
+  if (PREFIX || p.splits > 1) {
+    if (!PREFIX && from >= mine && from > 0) return;   // the join takes only parts that begin before `mine`
     const int64_t slot = (static_cast<int64_t>(row) * a.Hq + head) * parts.splits + blockIdx.y;
     float* to = parts.o + slot * D + 4 * half;
 #pragma unroll
@@ -447,12 +467,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
 
 }  // namespace
 
-hipError_t launch_attn_tile(const AttnArgs& a, const PrefillPlan& p, const Parts& parts, hipStream_t st) {
+hipError_t launch_attn_tile(const AttnArgs& a, const TileShape& p, const Parts& parts, hipStream_t st) {
   const int tile_pos = 32 * kWaves / p.pack;
   const int64_t tiles = static_cast<int64_t>(a.T / tile_pos) + a.B;      // at least the sum of the sequences' tiles
   const dim3 grid(static_cast<unsigned>(tiles * (a.Hq / p.pack)), p.splits), block(64 * kWaves);
-  if (a.D == 64) attn_tile_kernel<64><<<grid, block, 0, st>>>(a, p, parts);
-  else attn_tile_kernel<128><<<grid, block, 0, st>>>(a, p, parts);
+  if (a.D == 64) attn_tile_kernel<64, false><<<grid, block, 0, st>>>(a, p, parts);
+  else attn_tile_kernel<128, false><<<grid, block, 0, st>>>(a, p, parts);
+  return hipGetLastError();
+}
+
+hipError_t launch_attn_prefix_tile(const AttnArgs& a, const TileShape& p, const Parts& parts, hipStream_t st) {
+  const int64_t rows = static_cast<int64_t>(a.B) * (a.Hq / a.Hkv);
+  const int64_t tiles = (rows + 32 * kWaves - 1) / (32 * kWaves);
+  const dim3 grid(static_cast<unsigned>(tiles * a.Hkv), p.splits), block(64 * kWaves);
+  if (a.D == 64) attn_tile_kernel<64, true><<<grid, block, 0, st>>>(a, p, parts);
+  else attn_tile_kernel<128, true><<<grid, block, 0, st>>>(a, p, parts);
   return hipGetLastError();
 }
 

@@ -66,6 +66,7 @@ struct PrefillPlan {
 struct DecodePlan {
   int splits, chunk, tiles;
   int psplits, pchunk, ptiles;
+  int ptiled;             // the prefix on LDS tiles (attn_tile.hip)
   int64_t bytes;          // workspace
 };
 
