@@ -345,15 +345,8 @@ __global__ __launch_bounds__(64 * kPrefillWaves) void attn_prefill_kernel(AttnAr
   const int tile_pos = 16 * (kPrefillWaves / p.pack);
   const int units = a.Hq / p.pack;
   const int unit = blockIdx.x % units;
-  int tile = blockIdx.x / units, b = 0, q0 = 0, nq = 0;
-  for (; b < a.B; ++b) {
-    q0 = bounded_cu(a, b);
-    nq = bounded_cu(a, b + 1) - q0;
-    const int tiles = nq > 0 ? (nq + tile_pos - 1) / tile_pos : 0;
-    if (tile < tiles) break;
-    tile -= tiles;
-  }
-  if (b == a.B) return;
+  int tile = blockIdx.x / units, b, q0, nq;
+  if (!find_tile(a, tile_pos, tile, b, q0, nq)) return;
   const int len = bounded_len(a, b);
   const int h = unit * p.pack + wave % p.pack;
   const int pos0 = tile * tile_pos + 16 * (wave / p.pack);
@@ -493,14 +486,9 @@ template <bool PREFILL>
 __device__ __forceinline__ int parts_of_row(const AttnArgs& a, int t, int psplits, int chunk) {
   int keys;
   if constexpr (PREFILL) {
-    int b = 0, q1 = 0, q0 = 0;
-    for (; b < a.B; ++b) {
-      q0 = bounded_cu(a, b);
-      q1 = bounded_cu(a, b + 1);
-      if (t >= q0 && t < q1) break;
-    }
-    if (b == a.B) return -1;
-    const int64_t first = static_cast<int64_t>(bounded_len(a, b)) - (q1 - q0) + 1;
+    int b, q0, nq;
+    if (!find_row(a, t, b, q0, nq)) return -1;
+    const int64_t first = static_cast<int64_t>(bounded_len(a, b)) - nq + 1;
     keys = static_cast<int>(first + (t - q0) < 0 ? 0 : first + (t - q0));
   } else {
     keys = bounded_len(a, t);

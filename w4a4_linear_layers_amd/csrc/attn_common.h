@@ -49,6 +49,56 @@ __device__ __forceinline__ int bounded_cu(const AttnArgs& a, int i) {
   return n < 0 ? 0 : n < a.T ? n : a.T;
 }
 
+// The sequence that holds tile `tile` of tile_pos positions, counted over all
+// sequences: its number, first packed row and rows, and the tile's number
+// within it. 64 sequences at a time, one per lane. False past the last.
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile_pos, int& tile, int& b, int& q0, int& nq) {
+  const int lane = threadIdx.x & 63;
+  for (int base = 0; base < a.B; base += 64) {
+    const int i = base + lane;
+    const int first = i < a.B ? bounded_cu(a, i) : 0;
+    const int n = i < a.B ? bounded_cu(a, i + 1) - first : 0;
+    const int tiles = n > 0 ? (n + tile_pos - 1) / tile_pos : 0;
+    int upto = tiles;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int v = __shfl_up(upto, off, 64);
+      if (lane >= off) upto += v;
+    }
+    const unsigned long long past = __ballot(upto > tile);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      b = base + at;
+      q0 = uniform(__shfl(first, at, 64));
+      nq = uniform(__shfl(n, at, 64));
+      tile -= uniform(__shfl(upto - tiles, at, 64));
+      return true;
+    }
+    tile -= uniform(__shfl(upto, 63, 64));
+  }
+  return false;
+}
+
+// The first sequence that holds packed row t (its number, first row and
+// rows); false if none does.
+__device__ __forceinline__ bool find_row(const AttnArgs& a, int t, int& b, int& q0, int& nq) {
+  const int lane = threadIdx.x & 63;
+  for (int base = 0; base < a.B; base += 64) {
+    const int i = base + lane;
+    const int first = i < a.B ? bounded_cu(a, i) : 0;
+    const int end = i < a.B ? bounded_cu(a, i + 1) : 0;
+    const unsigned long long here = __ballot(t >= first && t < end);
+    if (here) {
+      const int at = __builtin_ctzll(here);
+      b = base + at;
+      q0 = uniform(__shfl(first, at, 64));
+      nq = uniform(__shfl(end - first, at, 64));
+      return true;
+    }
+  }
+  return false;
+}
+
 // Entry `i` (wave-uniform) of a row of page ids. No kernel writes the tables it
 // reads, so this is a scalar load: as a vector load it would wait for the tile
 // loads in flight around it.

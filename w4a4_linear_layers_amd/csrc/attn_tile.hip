@@ -88,12 +88,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
   constexpr int kLoads = kTile / (1024 * kWaves);
   constexpr int C = D / 16, DB = D / 32;
   __shared__ __align__(1024) uint8_t smem[2 * kRing * kTile];   // K tiles, then V tiles
+  __shared__ __align__(16) int odd_rows[kRing][kWaves];         // V tiles: whether a wave's rows hold NaN or infinities
 
   const int lane = threadIdx.x & 63, n = lane & 31, half = lane >> 5;
   const int wave = uniform(threadIdx.x >> 6);
   const int G = a.Hq / a.Hkv;
   const int from = static_cast<int>(blockIdx.y) * p.chunk;
   int row, head, kvh, len, mine, low, high, end;
+  int whole;                                     // keys that all rows of the workgroup see
   bool valid;
   const int32_t* table;
   if constexpr (PREFIX) {
@@ -103,23 +105,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
     const int R = valid ? R0 + n : rows - 1;
     row = R / G;
     head = kvh * G + R % G;
-    len = mine = low = end = a.prefix_len;
+    len = mine = low = end = whole = a.prefix_len;
     high = R0 < rows ? len : 0;
     table = a.prefix_table;
   } else {
     const int tile_pos = 32 * kWaves / p.pack;
     const int units = a.Hq / p.pack;
     const int unit = blockIdx.x % units;
-    int tile = blockIdx.x / units, b = 0, q0 = 0, nq = 0, tiles = 0;
-    for (; b < a.B; ++b) {
-      q0 = bounded_cu(a, b);
-      nq = bounded_cu(a, b + 1) - q0;
-      tiles = nq > 0 ? (nq + tile_pos - 1) / tile_pos : 0;
-      if (tile < tiles) break;
-      tile -= tiles;
-    }
-    if (b == a.B) return;
-    tile = tiles - 1 - tile;                     // the longest first
+    int tile = blockIdx.x / units, b, q0, nq;
+    if (!find_tile(a, tile_pos, tile, b, q0, nq)) return;
+    tile = (nq - 1) / tile_pos - tile;           // the longest first
     len = bounded_len(a, b);
     head = unit * p.pack + wave % p.pack;
     kvh = head / G;
@@ -130,6 +125,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
     const int shift = len - nq + 1;              // keys that position 0 sees
     const auto sees = [&](int i) { return i + shift < 0 ? 0 : i + shift < len ? i + shift : len; };
     mine = sees(pos), low = sees(pos0), high = pos0 < nq ? sees(pos0 + 31) : 0;
+    whole = sees(tile * tile_pos);
     end = sees(tile * tile_pos + tile_pos - 1);  // keys that any row of the workgroup sees
     table = a.page_table + static_cast<int64_t>(b) * a.max_pages;
   }
@@ -183,15 +179,25 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
       at[i] = static_cast<uint32_t>(in_cache(pages[i], a.n_pages)) * page_bytes +
               (head_bytes + ((from + t * kKeys + kRows * (wave + kWaves * i)) & in_mask) * kRow);
   };
-  // This wave's rows of V tile t that lie past the end, where the cache may
-  // hold anything, cleared (they have landed).
-  const auto clear_v = [&](int t, int slot) {
+  // V tile t, which some row of the workgroup does not see whole, has landed:
+  // this wave's rows past the end, where the cache may hold anything, are
+  // cleared, and it is noted whether the others are finite.
+  const auto look_over = [&](int t, int slot) {
+    bool ok = true;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int r = kRows * (wave + kWaves * i) + lr;
-      if (from + t * kKeys + r >= len)
-        *reinterpret_cast<u32x4*>(smem + (kRing + slot) * kTile + r * kRow + lp * 16) = u32x4{0, 0, 0, 0};
+      u32x4* at = reinterpret_cast<u32x4*>(smem + (kRing + slot) * kTile + r * kRow + lp * 16);
+      if (from + t * kKeys + r >= len) {
+        *at = u32x4{0, 0, 0, 0};
+      } else {
+        const u32x4 v = *at;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ok &= (v[e] & 0x7F80u) != 0x7F80u && (v[e] & 0x7F800000u) != 0x7F800000u;
+      }
     }
+    const int odd = __any(!ok);
+    if (lane == 0) odd_rows[slot][wave] = odd;
   };
 
   // Read addresses. K: part 2 c + half of row n (+ 32): its swizzled place is
@@ -202,8 +208,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
   const int vpart = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
   const int vbase = kRing * kTile + vr * kRow + ((vpart ^ swizzle_v<D>(vr)) << 4) + 8 * (lane & 1);
 
-  const auto v_operand = [&](int slot, int d, int j) {
-    const uint8_t* at = smem + slot * kTile + (vbase ^ (d << 6)) + 16 * j * kRow;
+  // (The bases of a tile are made opaque: left to itself the compiler keeps all
+  // twelve addresses of all stages in registers, and spills them.)
+  const auto v_place = [&](int slot) {
+    int base = vbase + slot * kTile;
+    asm("" : "+v"(base));
+    return base;
+  };
+  const auto v_operand = [&](int base, int d, int j) {
+    const uint8_t* at = smem + (base ^ (d << 6)) + 16 * j * kRow;
     typedef __attribute__((address_space(3))) s16x4 lds4;
     const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at)));
     const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + 8 * kRow)));
@@ -214,13 +227,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
   u32x4 w[4];                            // weights of 16 keys each, in bf16 as the values they multiply
 
   const auto scores = [&](int slot) {
+    int base = kbase + slot * kTile;
+    asm("" : "+v"(base));
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[0][i] = s[1][i] = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
-        s[kb] = mfma(*reinterpret_cast<const u32x4*>(smem + slot * kTile + (kbase ^ (c << 5)) + 32 * kb * kRow), q[c],
+        s[kb] = mfma(*reinterpret_cast<const u32x4*>(smem + (base ^ (c << 5)) + 32 * kb * kRow), q[c],
                      s[kb]);
     }
   };
@@ -282,10 +297,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
   };
 
   const auto values = [&](int slot, auto&& between) {
+    const int base = v_place(slot);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
-      for (int d = 0; d < DB; ++d) o[d] = mfma(v_operand(slot, d, j), w[j], o[d]);
+      for (int d = 0; d < DB; ++d) o[d] = mfma(v_operand(base, d, j), w[j], o[d]);
       between(j);
     }
   };
@@ -294,16 +310,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
   // values is not finite, 0 * inf would not be 0: each query then takes the
   // product over its own keys with the others' values cleared.
   const auto masked_values = [&](int t, int slot) {
-    bool ok = true;
-#pragma unroll 1
-    for (int d = 0; d < DB; ++d)
-#pragma unroll 1
-      for (int j = 0; j < 4; ++j) {
-        const u32x4 v = v_operand(slot, d, j);
+    int odd = 0;
+    if (from + (t + 1) * kKeys > whole) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ok &= (v[e] & 0x7F80u) != 0x7F80u && (v[e] & 0x7F800000u) != 0x7F800000u;
-      }
-    if (!__any(!ok)) {
+      for (int i = 0; i < kWaves; ++i) odd |= odd_rows[slot][i];
+    }
+    if (!uniform(odd)) {
       values(slot, [](int) {});
       return;
     }
@@ -314,7 +326,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
         f32x16 x = o[d];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          u32x4 v = v_operand(slot, d, j);
+          u32x4 v = v_operand(v_place(slot), d, j);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int k0 = 16 * j + 8 * (e / 2) + 2 * (e & 1);
@@ -362,20 +374,20 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
         vat[j - kLoads] = kat[j - kLoads];
       }
     };
-    const auto finish_loads = [&](auto tail) {     // K(t + 1), V(t)
+    const auto finish_loads = [&] {                // K(t + 1), V(t)
       wait_loads_but<2 * kLoads>();
-      if (decltype(tail)::value && from + (t + 1) * kKeys > len) clear_v(t, slot);
+      if (from + (t + 1) * kKeys > whole) look_over(t, slot);
     };
     const auto after_matrix = [&](bool ends) {
       if (ends) {
-        finish_loads(std::true_type{});
+        finish_loads();
         barrier();
       }
       look_up(t + 3, pages);                       // (a scalar load; among LDS reads it would stall them)
     };
-    const auto after_vector = [&](bool ends, auto tail) {
+    const auto after_vector = [&](bool ends) {
       if (ends) {
-        finish_loads(tail);
+        finish_loads();
         barrier();
       }
       const int s0 = slot;
@@ -384,21 +396,22 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
       slot2 = s0;
       ++t;
     };
-    look_up(0, pages);
-    place(pages, 0, kat);
+    int pages0[kLoads], pages1[kLoads];
+    look_up(0, pages0);
+    look_up(1, pages1);
+    look_up(2, pages);
+    place(pages0, 0, kat);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) load_k(i, 0);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) vat[i] = kat[i];
-    look_up(1, pages);
-    place(pages, 1, kat);
+    place(pages1, 1, kat);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       load_k(i, 1);
       load_v(i, 0);
       vat[i] = kat[i];
     }
-    look_up(2, pages);
     wait_loads_but<2 * kLoads>();
     barrier();
 #pragma unroll
@@ -412,7 +425,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
       constexpr bool kSecond = decltype(second_group)::value;
       while (t + 1 < steps && from + (t + 1) * kKeys <= low) {
         softmax(t, std::false_type{});
-        after_vector(!kSecond, std::false_type{});
+        after_vector(!kSecond);
         __builtin_amdgcn_s_setprio(1);
         __builtin_amdgcn_sched_barrier(0);
         scores(slot);
@@ -427,7 +440,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
     else whole_tiles(std::false_type{});
     while (true) {
       if (from + t * kKeys < high) softmax(t, std::true_type{});
-      after_vector(!second, std::true_type{});
+      after_vector(!second);
       if (t < steps) {
 #pragma unroll
         for (int j = 0; j < 2 * kLoads; ++j) start_load(j);
