@@ -234,17 +234,32 @@ struct Rows<float, D> {
     for (int c = 0; c < C; ++c) q[c] = *reinterpret_cast<const f32x4*>(row + 16 * c + 4 * g);
   }
 
-  template <bool CAUSAL>
-  __device__ __forceinline__ void step(const Pages<float, D>& pg, int key0, int limit, int mine, float scale, int n,
-                                       int g) {
-    const int64_t at = pg.at(key0);
+  struct Keys {
     f32x4 k[C], v[4][NB];
+  };
+  static __device__ __forceinline__ void fetch(const Pages<float, D>& pg, int key0, int n, int g, Keys& x) {
+    const int64_t at = pg.at(key0);
 #pragma unroll
-    for (int c = 0; c < C; ++c) k[c] = *reinterpret_cast<const f32x4*>(pg.k + at + n * D + 16 * c + 4 * g);
+    for (int c = 0; c < C; ++c) x.k[c] = *reinterpret_cast<const f32x4*>(pg.k + at + n * D + 16 * c + 4 * g);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) v[j][b] = *reinterpret_cast<const f32x4*>(pg.v + at + (4 * g + j) * D + 64 * b + 4 * n);
+      for (int b = 0; b < NB; ++b)
+        x.v[j][b] = *reinterpret_cast<const f32x4*>(pg.v + at + (4 * g + j) * D + 64 * b + 4 * n);
+  }
+
+  template <bool CAUSAL>
+  __device__ __forceinline__ void step(const Pages<float, D>& pg, int key0, int limit, int mine, float scale, int n,
+                                       int g) {
+    Keys x;
+    fetch(pg, key0, n, g, x);
+    step<CAUSAL>(x, key0, limit, mine, scale, n, g);
+  }
+
+  template <bool CAUSAL>
+  __device__ __forceinline__ void step(Keys& x, int key0, int limit, int mine, float scale, int n, int g) {
+    auto& k = x.k;
+    auto& v = x.v;
     if (key0 + 16 > limit) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -336,20 +351,24 @@ struct Rows<float, D> {
 
 constexpr int kPrefillWaves = 4;
 
-// One workgroup: a tile of positions of one sequence for `pack` heads of a
-// group, a wave per 16 positions of a head. Tile x counts over all sequences.
-template <typename T, int D>
-__global__ __launch_bounds__(64 * kPrefillWaves) void attn_prefill_kernel(AttnArgs a, PrefillPlan p, Parts parts) {
+// fp32 (bf16 goes to attn_tile.hip). One workgroup: a tile of positions of one
+// sequence for `pack` heads of a group, a wave per 16 positions of a head.
+template <int D>
+__global__ __launch_bounds__(64 * kPrefillWaves, 2) void attn_prefill_kernel(AttnArgs a, PrefillPlan p, Parts parts) {
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = uniform(threadIdx.x >> 6);
-  const int tile_pos = 16 * (kPrefillWaves / p.pack);
   const int units = a.Hq / p.pack;
   const int unit = blockIdx.x % units;
-  int tile = blockIdx.x / units, b, q0, nq;
-  if (!find_tile(a, tile_pos, tile, b, q0, nq)) return;
-  const int len = bounded_len(a, b);
+  TileAt at;
+  if (!find_tile(a, p.tile_pos, blockIdx.x / units, at)) return;
+  int chunk = 0, count = 1;
+  if (p.splits > 1) {
+    count = parts_for(a, p, at.total, chunk);
+    if (static_cast<int>(blockIdx.y) >= count) return;
+  }
+  const int nq = at.nq, q0 = at.q0, len = at.len;
   const int h = unit * p.pack + wave % p.pack;
-  const int pos0 = tile * tile_pos + 16 * (wave / p.pack);
+  const int pos0 = at.tile * p.tile_pos + 16 * (wave / p.pack);
   if (pos0 >= nq) return;
   const int pos = pos0 + n;
   const int row = q0 + (pos < nq ? pos : nq - 1);
@@ -358,27 +377,36 @@ __global__ __launch_bounds__(64 * kPrefillWaves) void attn_prefill_kernel(AttnAr
   if (mine > len) mine = len;
   const int top = pos0 + 15 < nq ? pos0 + 15 : nq - 1;
   int end = static_cast<int>(first + top < 0 ? 0 : first + top);
-  const int from = blockIdx.y * p.chunk;
-  if (p.splits > 1 && end > from + p.chunk) end = from + p.chunk;
-  Rows<T, D> r;
+  const int from = static_cast<int>(blockIdx.y) * chunk;
+  if (count > 1 && end > from + chunk) end = from + chunk;
+  Rows<float, D> r;
   r.init();
-  r.load_q(static_cast<const T*>(a.Q) + row * a.ldq + static_cast<int64_t>(h) * D, g);
+  r.load_q(static_cast<const float*>(a.Q) + row * a.ldq + static_cast<int64_t>(h) * D, g);
   if (from < end) {
-    Pages<T, D> pg{static_cast<const T*>(a.Kc), static_cast<const T*>(a.Vc),
-                   a.page_table + static_cast<int64_t>(b) * a.max_pages, (len - 1) >> a.page_shift,
+    Pages<float, D> pg{static_cast<const float*>(a.Kc), static_cast<const float*>(a.Vc),
+                   a.page_table + static_cast<int64_t>(at.b) * a.max_pages, (len - 1) >> a.page_shift,
                    a.page_shift, a.n_pages, a.Hkv, h / (a.Hq / a.Hkv)};
-    for (int key = from; key < end; key += r.kStep)
-      r.template step<true>(pg, key, len, mine, a.scale_log2, n, g);
+    // the next keys are on their way while these are worked on
+    typename Rows<float, D>::Keys x[2];
+    r.fetch(pg, from, n, g, x[0]);
+    for (int key = from;;) {
+      r.fetch(pg, key + 16, n, g, x[1]);
+      r.template step<true>(x[0], key, len, mine, a.scale_log2, n, g);
+      if ((key += 16) >= end) break;
+      r.fetch(pg, key + 16, n, g, x[0]);
+      r.template step<true>(x[1], key, len, mine, a.scale_log2, n, g);
+      if ((key += 16) >= end) break;
+    }
   }
   const float l = sum_groups(r.l);
   if (pos >= nq) return;
-  if (p.splits > 1) {
+  if (count > 1) {
     if (from >= mine && from > 0) return;            // the join takes only parts that begin before `mine`
     const int64_t slot = (static_cast<int64_t>(row) * a.Hq + h) * parts.splits + blockIdx.y;
     r.store_f32(parts.o + slot * D, g);
     if (g == 0) parts.ml[slot] = float2{r.m, l};
   } else {
-    r.store(static_cast<T*>(a.O) + row * a.ldo + static_cast<int64_t>(h) * D, g, inverse(l));
+    r.store(static_cast<float*>(a.O) + row * a.ldo + static_cast<int64_t>(h) * D, g, inverse(l));
   }
 }
 
@@ -483,10 +511,11 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void attn_decode_kernel(AttnArgs
 // that begin before their own limit, rows of a decode the prefix parts and
 // those that begin before the sequence's length.
 template <bool PREFILL>
-__device__ __forceinline__ int parts_of_row(const AttnArgs& a, int t, int psplits, int chunk) {
+__device__ __forceinline__ int parts_of_row(const AttnArgs& a, const PrefillPlan& p, int t, int psplits, int chunk) {
   int keys;
   if constexpr (PREFILL) {
     int b, q0, nq;
+    if (parts_for(a, p, count_tiles(a, p.tile_pos), chunk) == 1) return -1;      // (the output is there)
     if (!find_row(a, t, b, q0, nq)) return -1;
     const int64_t first = static_cast<int64_t>(bounded_len(a, b)) - nq + 1;
     keys = static_cast<int>(first + (t - q0) < 0 ? 0 : first + (t - q0));
@@ -498,13 +527,14 @@ __device__ __forceinline__ int parts_of_row(const AttnArgs& a, int t, int psplit
 
 // Many rows: one wave each.
 template <typename T, int D, bool PREFILL>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int psplits, int chunk, Parts parts) {
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, PrefillPlan p, int psplits, int chunk,
+                                                       Parts parts) {
   constexpr int W = D / 64;
   const int lane = threadIdx.x & 63;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + uniform(threadIdx.x >> 6);
   const int t = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
   if (t >= (PREFILL ? a.T : a.B)) return;
-  const int count = parts_of_row<PREFILL>(a, t, psplits, chunk);
+  const int count = parts_of_row<PREFILL>(a, p, t, psplits, chunk);
   if (count < 0) return;
   const float2* ml = parts.ml + row * parts.splits;
   const float* po = parts.o + row * parts.splits * D + lane * W;
@@ -549,14 +579,15 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int psplits,
 // in flight at once. At most 256 parts (2 kMostSplits).
 constexpr int kMostSplits = 128;
 template <typename T, int D, bool PREFILL>
-__global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs a, int psplits, int chunk, Parts parts) {
+__global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs a, PrefillPlan p, int psplits, int chunk,
+                                                       Parts parts) {
   constexpr int L = D / 8, GROUPS = 256 / L;
   static_assert(2 * kMostSplits <= 256, "a thread per part");
   __shared__ float weight[256], so[GROUPS][D], red[2][4];
   const int tid = threadIdx.x, wave = tid >> 6;
   const int64_t row = blockIdx.x;
   const int t = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
-  const int count = parts_of_row<PREFILL>(a, t, psplits, chunk);
+  const int count = parts_of_row<PREFILL>(a, p, t, psplits, chunk);
   if (count < 0) return;
   const float2 x = tid < count ? parts.ml[row * parts.splits + tid] : float2{kNone, 0.0f};
   const int group = tid / L, d = tid % L * 8;
@@ -614,22 +645,24 @@ __global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs a, int pspl
 constexpr int64_t kFewRows = 2048;
 
 template <typename T, int D, bool PREFILL>
-void launch_join_typed(const AttnArgs& a, int64_t rows, int psplits, int chunk, const Parts& parts, hipStream_t st) {
+void launch_join_typed(const AttnArgs& a, const PrefillPlan& p, int64_t rows, int psplits, int chunk,
+                       const Parts& parts, hipStream_t st) {
   if (rows <= kFewRows)
-    attn_join_few_kernel<T, D, PREFILL><<<dim3(static_cast<unsigned>(rows)), 256, 0, st>>>(a, psplits, chunk, parts);
+    attn_join_few_kernel<T, D, PREFILL><<<dim3(static_cast<unsigned>(rows)), 256, 0, st>>>(a, p, psplits, chunk, parts);
   else
-    attn_join_kernel<T, D, PREFILL><<<dim3(static_cast<unsigned>((rows + 3) / 4)), 256, 0, st>>>(a, psplits, chunk,
+    attn_join_kernel<T, D, PREFILL><<<dim3(static_cast<unsigned>((rows + 3) / 4)), 256, 0, st>>>(a, p, psplits, chunk,
                                                                                                  parts);
 }
 
 template <bool PREFILL>
-void launch_join(const AttnArgs& a, int64_t rows, int psplits, int chunk, const Parts& parts, hipStream_t st) {
+void launch_join(const AttnArgs& a, const PrefillPlan& p, int64_t rows, int psplits, int chunk, const Parts& parts,
+                 hipStream_t st) {
   if (a.bf16) {
-    if (a.D == 64) launch_join_typed<__bf16, 64, PREFILL>(a, rows, psplits, chunk, parts, st);
-    else launch_join_typed<__bf16, 128, PREFILL>(a, rows, psplits, chunk, parts, st);
+    if (a.D == 64) launch_join_typed<__bf16, 64, PREFILL>(a, p, rows, psplits, chunk, parts, st);
+    else launch_join_typed<__bf16, 128, PREFILL>(a, p, rows, psplits, chunk, parts, st);
   } else {
-    if (a.D == 64) launch_join_typed<float, 64, PREFILL>(a, rows, psplits, chunk, parts, st);
-    else launch_join_typed<float, 128, PREFILL>(a, rows, psplits, chunk, parts, st);
+    if (a.D == 64) launch_join_typed<float, 64, PREFILL>(a, p, rows, psplits, chunk, parts, st);
+    else launch_join_typed<float, 128, PREFILL>(a, p, rows, psplits, chunk, parts, st);
   }
 }
 
@@ -661,36 +694,34 @@ constexpr int kTileRows = 256;       // rows of a workgroup of the tile kernel
 constexpr int kPrefixTileRows = 96;  // rows a key/value head from which the prefix goes there
 
 PrefillPlan plan_prefill(int bf16, int B, int T, int Hq, int Hkv, int D, int max_len) {
+  (void)B;
   PrefillPlan p{};
   const int G = Hq / Hkv;
   p.tiled = bf16;
-  const int most = p.tiled ? 8 : 4;
-  p.pack = G % 8 == 0 && most == 8 ? 8 : G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1;
-  const int tile_pos = (p.tiled ? 256 : 16 * kPrefillWaves) / p.pack;
-  const int64_t units = (static_cast<int64_t>(ceil_div(T, tile_pos)) + B) * (Hq / p.pack);
-  const int want = p.tiled ? 256 : 512;
-  int64_t splits = units < want ? 2 * want / units : 1;
-  if (splits > max_len / 512) splits = max_len / 512;
-  p.chunk = cut(max_len, splits);
-  p.splits = static_cast<int>(splits);
+  p.pack = p.tiled && G % 8 == 0 ? 8 : G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1;
+  p.tile_pos = (p.tiled ? kTileRows : 16 * kPrefillWaves) / p.pack;
+  p.target = p.tiled ? 256 : 768;     // workgroups that run at once: one of the tile kernel's a CU, three of the other
+  int64_t splits = p.target / (static_cast<int64_t>(ceil_div(T, p.tile_pos)) * (Hq / p.pack));
+  if (splits > max_len / 256) splits = max_len / 256;
+  if (splits > kMostSplits) splits = kMostSplits;
+  p.splits = splits < 1 ? 1 : static_cast<int>(splits);
   p.bytes = parts_bytes(static_cast<int64_t>(T) * Hq, D, p.splits);
   return p;
 }
 
 hipError_t launch_attn_prefill(const AttnArgs& a, const PrefillPlan& p, hipStream_t st) {
-  const int tile_pos = 16 * kPrefillWaves / p.pack;
-  const int64_t tiles = static_cast<int64_t>(a.T / tile_pos) + a.B;      // at least the sum of the sequences' tiles
   const int64_t rows = static_cast<int64_t>(a.T) * a.Hq;
   const Parts parts = parts_of(a.workspace, rows, a.D, p.splits);
-  const dim3 grid(static_cast<unsigned>(tiles * (a.Hq / p.pack)), p.splits), block(64 * kPrefillWaves);
   if (p.tiled) {
-    const hipError_t e = launch_attn_tile(a, TileShape{p.pack, p.splits, p.chunk}, parts, st);
+    const hipError_t e = launch_attn_tile(a, p, parts, st);
     if (e != hipSuccess) return e;
   } else {
-    if (a.D == 64) attn_prefill_kernel<float, 64><<<grid, block, 0, st>>>(a, p, parts);
-    else attn_prefill_kernel<float, 128><<<grid, block, 0, st>>>(a, p, parts);
+    const int64_t tiles = static_cast<int64_t>(a.T / p.tile_pos) + a.B;  // at least the sum of the sequences' tiles
+    const dim3 grid(static_cast<unsigned>(tiles * (a.Hq / p.pack)), p.splits), block(64 * kPrefillWaves);
+    if (a.D == 64) attn_prefill_kernel<64><<<grid, block, 0, st>>>(a, p, parts);
+    else attn_prefill_kernel<128><<<grid, block, 0, st>>>(a, p, parts);
   }
-  if (p.splits > 1) launch_join<true>(a, rows, 0, p.chunk, parts, st);
+  if (p.splits > 1) launch_join<true>(a, p, rows, 0, 0, parts, st);
   return hipGetLastError();
 }
 
@@ -717,7 +748,7 @@ hipError_t launch_attn_decode(const AttnArgs& a, const DecodePlan& p, hipStream_
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
   const Parts parts = parts_of(a.workspace, rows, a.D, p.splits + p.psplits);
   if (p.ptiled) {
-    const hipError_t e = launch_attn_prefix_tile(a, TileShape{1, p.psplits, p.pchunk}, parts, st);
+    const hipError_t e = launch_attn_prefix_tile(a, p.psplits, p.pchunk, parts, st);
     if (e != hipSuccess) return e;
   }
   const int64_t blocks = (p.ptiled ? 0 : static_cast<int64_t>(a.Hkv) * p.ptiles * p.psplits) +
@@ -730,7 +761,7 @@ hipError_t launch_attn_decode(const AttnArgs& a, const DecodePlan& p, hipStream_
     if (a.D == 64) attn_decode_kernel<float, 64><<<grid, block, 0, st>>>(a, p, parts);
     else attn_decode_kernel<float, 128><<<grid, block, 0, st>>>(a, p, parts);
   }
-  if (p.splits + p.psplits > 1) launch_join<false>(a, rows, p.psplits, p.chunk, parts, st);
+  if (p.splits + p.psplits > 1) launch_join<false>(a, PrefillPlan{}, rows, p.psplits, p.chunk, parts, st);
   return hipGetLastError();
 }
 

@@ -49,34 +49,115 @@ __device__ __forceinline__ int bounded_cu(const AttnArgs& a, int i) {
   return n < 0 ? 0 : n < a.T ? n : a.T;
 }
 
-// The sequence that holds tile `tile` of tile_pos positions, counted over all
-// sequences: its number, first packed row and rows, and the tile's number
-// within it. 64 sequences at a time, one per lane. False past the last.
-__device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile_pos, int& tile, int& b, int& q0, int& nq) {
+// Sum and maximum over the wave's lanes.
+__device__ __forceinline__ int wave_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);      // row_shr:1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);      // row_bcast:15, 31
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
+// One tile of tile_pos positions: sequence b (its first packed row, rows and
+// keys), the tile's number within it; and how many tiles there are in all.
+struct TileAt {
+  int b, q0, nq, len, tile, total;
+};
+
+// Tile `idx` of all sequences; false past the last. Up to 64 sequences lie in
+// the lanes, and tiles come in the order of the keys they see, most first, so
+// that the workgroups that run last are short: with class = (keys before the
+// tile) / tile_pos, the class of tile idx is the largest c with more than idx
+// tiles of class >= c, found by bisection. (Sequence by sequence, the longest
+// first: 169 us against 157 for three fp32 sequences of 500 to 2000 tokens,
+// even for bf16.) More sequences than lanes come one after another, each one's
+// longest tile first.
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile_pos, int idx, TileAt& at) {
   const int lane = threadIdx.x & 63;
-  for (int base = 0; base < a.B; base += 64) {
-    const int i = base + lane;
-    const int first = i < a.B ? bounded_cu(a, i) : 0;
-    const int n = i < a.B ? bounded_cu(a, i + 1) - first : 0;
-    const int tiles = n > 0 ? (n + tile_pos - 1) / tile_pos : 0;
-    int upto = tiles;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int v = __shfl_up(upto, off, 64);
-      if (lane >= off) upto += v;
+  const auto load = [&](int i, int& first, int& n, int& len, int& tiles) {
+    const bool in = i < a.B;
+    first = in ? bounded_cu(a, i) : 0;
+    n = in ? bounded_cu(a, i + 1) - first : 0;
+    len = in ? bounded_len(a, i) : 0;
+    tiles = n > 0 ? (n + tile_pos - 1) / tile_pos : 0;
+  };
+  const auto take = [&](int b, int from, int first, int n, int len, int tile) {
+    at.b = uniform(b);
+    at.q0 = __builtin_amdgcn_readlane(first, from);
+    at.nq = __builtin_amdgcn_readlane(n, from);
+    at.len = __builtin_amdgcn_readlane(len, from);
+    at.tile = uniform(tile);
+  };
+  int first, n, len, tiles;
+  if (a.B <= 64) {
+    load(lane, first, n, len, tiles);
+    at.total = wave_sum(tiles);
+    if (idx >= at.total) return false;
+    const int base = len > n ? (len - n) / tile_pos : 0;
+    const auto from_class = [&](int c) {           // tiles of class >= c
+      const int k = base + tiles - c;
+      return wave_sum(k < 0 ? 0 : k < tiles ? k : tiles);
+    };
+    int lo = 0, hi = (a.max_len + a.T) / tile_pos + 2;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (from_class(mid) > idx) lo = mid;
+      else hi = mid;
     }
-    const unsigned long long past = __ballot(upto > tile);
-    if (past) {
-      const int at = __builtin_ctzll(past);
-      b = base + at;
-      q0 = uniform(__shfl(first, at, 64));
-      nq = uniform(__shfl(n, at, 64));
-      tile -= uniform(__shfl(upto - tiles, at, 64));
-      return true;
-    }
-    tile -= uniform(__shfl(upto, 63, 64));
+    lo = uniform(lo);
+    const int rank = idx - from_class(lo + 1);
+    const bool has = base <= lo && lo < base + tiles;
+    const unsigned long long all = __ballot(has);
+    const int before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(all >> 32),
+                                                 __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(all), 0));
+    const int from = __builtin_ctzll(__ballot(has && before == rank));
+    take(from, from, first, n, len, lo - __builtin_amdgcn_readlane(base, from));
+    return true;
   }
-  return false;
+  bool found = false;
+  at.total = 0;
+  for (int start = 0; start < a.B; start += 64) {
+    load(start + lane, first, n, len, tiles);
+    const int sum = wave_sum(tiles);
+    if (!found && idx < at.total + sum) {
+      int upto = tiles;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int v = __shfl_up(upto, off, 64);
+        if (lane >= off) upto += v;
+      }
+      const int want = idx - at.total;
+      const int from = __builtin_ctzll(__ballot(upto > want));
+      take(start + from, from, first, n, len, __builtin_amdgcn_readlane(upto, from) - 1 - want);
+      found = true;
+    }
+    at.total += sum;
+  }
+  return found;
+}
+
+// All tiles of a call.
+__device__ __forceinline__ int count_tiles(const AttnArgs& a, int tile_pos) {
+  int sum = 0;
+  for (int i = threadIdx.x & 63; i < a.B; i += 64) {
+    const int n = bounded_cu(a, i + 1) - bounded_cu(a, i);
+    sum += n > 0 ? (n + tile_pos - 1) / tile_pos : 0;
+  }
+  return wave_sum(sum);
+}
+
+// How a prefill's keys are cut, known once its tiles are counted: as many
+// parts as fill the card with the workgroups there are, at most the plan's.
+// (The host knows bounds alone; a part too many for one round of workgroups
+// costs a whole round.)
+__device__ __forceinline__ int parts_for(const AttnArgs& a, const PrefillPlan& p, int total, int& chunk) {
+  const int groups = total * (a.Hq / p.pack);
+  int parts = groups > 0 ? p.target / groups : 1;
+  parts = uniform(parts < 1 ? 1 : parts < p.splits ? parts : p.splits);
+  chunk = uniform(((a.max_len + parts - 1) / parts + 63) & ~63);
+  return parts;
 }
 
 // The first sequence that holds packed row t (its number, first row and
@@ -113,13 +194,9 @@ __device__ __forceinline__ int in_cache(int page, int n_pages) {
 
 }  // namespace attn
 
-// What the tile kernel needs of a plan.
-struct TileShape {
-  int pack;            // query heads of a group per workgroup (prefill)
-  int splits, chunk;   // parts of the keys
-};
-
-hipError_t launch_attn_tile(const AttnArgs& a, const TileShape& p, const attn::Parts& parts, hipStream_t stream);
-hipError_t launch_attn_prefix_tile(const AttnArgs& a, const TileShape& p, const attn::Parts& parts, hipStream_t stream);
+hipError_t launch_attn_tile(const AttnArgs& a, const PrefillPlan& p, const attn::Parts& parts, hipStream_t stream);
+// The prefix of a decode in `splits` parts of `chunk` keys.
+hipError_t launch_attn_prefix_tile(const AttnArgs& a, int splits, int chunk, const attn::Parts& parts,
+                                   hipStream_t stream);
 
 }  // namespace serq

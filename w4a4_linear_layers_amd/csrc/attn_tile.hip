@@ -81,7 +81,8 @@ __device__ __forceinline__ int swizzle_v(int r) { return D == 128 ? (r & 3) << 2
 // all sequences (row R: sequence R / G, head R % G of the group), 256 to a
 // workgroup, and all of them see all keys.
 template <int D, bool PREFIX>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, TileShape p, Parts parts) {
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, PrefillPlan p, int chunk,
+                                                                   Parts parts) {
   constexpr int kRow = 2 * D;                    // bytes of a row
   constexpr int kTile = kKeys * kRow;            // bytes of a K or V tile
   constexpr int kRows = 1024 / kRow;             // rows of one wave load
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
   const int lane = threadIdx.x & 63, n = lane & 31, half = lane >> 5;
   const int wave = uniform(threadIdx.x >> 6);
   const int G = a.Hq / a.Hkv;
-  const int from = static_cast<int>(blockIdx.y) * p.chunk;
+  bool split = PREFIX;
   int row, head, kvh, len, mine, low, high, end;
   int whole;                                     // keys that all rows of the workgroup see
   bool valid;
@@ -109,13 +110,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
     high = R0 < rows ? len : 0;
     table = a.prefix_table;
   } else {
-    const int tile_pos = 32 * kWaves / p.pack;
     const int units = a.Hq / p.pack;
     const int unit = blockIdx.x % units;
-    int tile = blockIdx.x / units, b, q0, nq;
-    if (!find_tile(a, tile_pos, tile, b, q0, nq)) return;
-    tile = (nq - 1) / tile_pos - tile;           // the longest first
-    len = bounded_len(a, b);
+    TileAt at;
+    if (!find_tile(a, p.tile_pos, blockIdx.x / units, at)) return;
+    if (p.splits > 1) {
+      const int count = parts_for(a, p, at.total, chunk);
+      if (static_cast<int>(blockIdx.y) >= count) return;
+      split = count > 1;
+    }
+    const int nq = at.nq, q0 = at.q0, tile_pos = p.tile_pos, tile = at.tile;
+    len = at.len;
     head = unit * p.pack + wave % p.pack;
     kvh = head / G;
     const int pos0 = tile * tile_pos + 32 * (wave / p.pack);
@@ -127,9 +132,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
     mine = sees(pos), low = sees(pos0), high = pos0 < nq ? sees(pos0 + 31) : 0;
     whole = sees(tile * tile_pos);
     end = sees(tile * tile_pos + tile_pos - 1);  // keys that any row of the workgroup sees
-    table = a.page_table + static_cast<int64_t>(b) * a.max_pages;
+    table = a.page_table + static_cast<int64_t>(at.b) * a.max_pages;
   }
-  if (p.splits > 1 && end > from + p.chunk) end = from + p.chunk;
+  const int from = static_cast<int>(blockIdx.y) * chunk;
+  if (split && end > from + chunk) end = from + chunk;
 
   // Q as the second operand: lane (query n, half) holds values 16 c + 8 half .. + 7.
   // A negative scale goes into Q's sign, so the largest product is the largest score.
@@ -456,7 +462,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
   l = sum_halves(l);
   if (!valid) return;
   // o[d][i]: value 32 d + 8 (i / 4) + 4 half + i % 4 of query n
-  if (PREFIX || p.splits > 1) {
+  if (split) {
     if (!PREFIX && from >= mine && from > 0) return;   // the join takes only parts that begin before `mine`
     const int64_t slot = (static_cast<int64_t>(row) * a.Hq + head) * parts.splits + blockIdx.y;
     float* to = parts.o + slot * D + 4 * half;
@@ -480,21 +486,20 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, T
 
 }  // namespace
 
-hipError_t launch_attn_tile(const AttnArgs& a, const TileShape& p, const Parts& parts, hipStream_t st) {
-  const int tile_pos = 32 * kWaves / p.pack;
-  const int64_t tiles = static_cast<int64_t>(a.T / tile_pos) + a.B;      // at least the sum of the sequences' tiles
+hipError_t launch_attn_tile(const AttnArgs& a, const PrefillPlan& p, const Parts& parts, hipStream_t st) {
+  const int64_t tiles = static_cast<int64_t>(a.T / p.tile_pos) + a.B;    // at least the sum of the sequences' tiles
   const dim3 grid(static_cast<unsigned>(tiles * (a.Hq / p.pack)), p.splits), block(64 * kWaves);
-  if (a.D == 64) attn_tile_kernel<64, false><<<grid, block, 0, st>>>(a, p, parts);
-  else attn_tile_kernel<128, false><<<grid, block, 0, st>>>(a, p, parts);
+  if (a.D == 64) attn_tile_kernel<64, false><<<grid, block, 0, st>>>(a, p, 0, parts);
+  else attn_tile_kernel<128, false><<<grid, block, 0, st>>>(a, p, 0, parts);
   return hipGetLastError();
 }
 
-hipError_t launch_attn_prefix_tile(const AttnArgs& a, const TileShape& p, const Parts& parts, hipStream_t st) {
+hipError_t launch_attn_prefix_tile(const AttnArgs& a, int splits, int chunk, const Parts& parts, hipStream_t st) {
   const int64_t rows = static_cast<int64_t>(a.B) * (a.Hq / a.Hkv);
   const int64_t tiles = (rows + 32 * kWaves - 1) / (32 * kWaves);
-  const dim3 grid(static_cast<unsigned>(tiles * a.Hkv), p.splits), block(64 * kWaves);
-  if (a.D == 64) attn_tile_kernel<64, true><<<grid, block, 0, st>>>(a, p, parts);
-  else attn_tile_kernel<128, true><<<grid, block, 0, st>>>(a, p, parts);
+  const dim3 grid(static_cast<unsigned>(tiles * a.Hkv), splits), block(64 * kWaves);
+  if (a.D == 64) attn_tile_kernel<64, true><<<grid, block, 0, st>>>(a, PrefillPlan{}, chunk, parts);
+  else attn_tile_kernel<128, true><<<grid, block, 0, st>>>(a, PrefillPlan{}, chunk, parts);
   return hipGetLastError();
 }
 

@@ -51,13 +51,13 @@ struct AttnArgs {
   int bf16;
 };
 
-// How serq_attn_prefill is cut: `pack` query heads of a group and 16 * waves
-// / pack (or 32 * waves / pack) positions per workgroup, keys in `splits`
-// parts of `chunk`.
+// How serq_attn_prefill is cut: `pack` query heads of a group and tile_pos
+// positions per workgroup; keys in up to `splits` parts, so many that there
+// are about `target` workgroups.
 struct PrefillPlan {
   int tiled;              // on LDS tiles (attn_tile.hip)
-  int pack;
-  int splits, chunk;
+  int pack, tile_pos;
+  int splits, target;
   int64_t bytes;          // workspace
 };
 
