@@ -24,12 +24,16 @@ using namespace attn;
 
 // Maximum (sum) over the four lane groups that share a query.
 __device__ __forceinline__ float max_groups(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16, 64));
-  return fmaxf(v, __shfl_xor(v, 32, 64));
+  const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+  const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
 }
 __device__ __forceinline__ float sum_groups(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
+  const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+  const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(y[0]) + __uint_as_float(y[1]);
 }
 
 // One sequence's pages of one key/value head, for one wave.
@@ -41,12 +45,16 @@ struct Pages {
   int last;            // last page index in use (keys exist)
   int shift, n_pages, Hkv, h;
 
-  // Element offset of key `key` (a multiple of 16, wave-uniform); keys past
+  // The table's entry of key `key` (a multiple of 16, wave-uniform); keys past
   // the last page give that page again.
-  __device__ __forceinline__ int64_t at(int key) const {
-    int i = key >> shift;
-    i = uniform(i < last ? i : last);
-    const int page = uniform(in_cache(page_entry(table, i), n_pages));
+  __device__ __forceinline__ int entry(int key) const {
+    const int i = key >> shift;
+    return page_entry(table, uniform(i < last ? i : last));
+  }
+  // Element offset of that key.
+  __device__ __forceinline__ int64_t at(int key) const { return at(key, entry(key)); }
+  __device__ __forceinline__ int64_t at(int key, int entry) const {
+    const int page = uniform(in_cache(entry, n_pages));
     return (((static_cast<int64_t>(page) * Hkv + h) << shift) + (key & ((1 << shift) - 1))) * D;
   }
 };
@@ -73,6 +81,19 @@ struct Rows<__bf16, D> {
 #pragma unroll
     for (int c = 0; c < W; ++c) o[c] = f32x4{0, 0, 0, 0};
   }
+  // The exponentials' reference follows the maximum only where that has
+  // outgrown it by 2^8, so that the sums are rarely scaled.
+  __device__ __forceinline__ void grow(float top) {
+    if (__any(top > m + 8.0f)) {
+      const float mn = top > m + 8.0f ? top : m;     // a query's own scores alone decide
+      const float f = exp2_(m - ref(mn));
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int c = 0; c < W; ++c) o[c] *= f;
+    }
+  }
+
   __device__ __forceinline__ void load_q(const __bf16* row, int g) {
 #pragma unroll
     for (int c = 0; c < C; ++c) q[c] = *reinterpret_cast<const u32x4*>(row + 32 * c + 8 * g);
@@ -128,20 +149,16 @@ struct Rows<__bf16, D> {
     float top = z[0];
 #pragma unroll
     for (int j = 1; j < 8; ++j) top = fmaxf(top, z[j]);
-    const float mn = fmaxf(m, max_groups(top));
-    const float r = ref(mn), f = exp2_(m - r);
-    m = mn;
-    l *= f;
+    grow(max_groups(top));
+    const float r = ref(m);
     uint32_t p[4];
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
       const float a = exp2_(z[j] - r), b = exp2_(z[j + 1] - r);
       l += a + b;
-      p[j / 2] = pack2(a, b);       // weights in [0, 1]; 8 bits each, as the values they multiply
+      p[j / 2] = pack2(a, b);       // weights in 8 bits each, as the values they multiply
     }
     const bf16x8 pb = __builtin_bit_cast(bf16x8, u32x4{p[0], p[1], p[2], p[3]});
-#pragma unroll
-    for (int c = 0; c < W; ++c) o[c] *= f;
     bool odd = false;
     if constexpr (CAUSAL) odd = __any(key0 + 32 > mine) && __any(!finite(v));
     if (!odd) {
@@ -229,6 +246,19 @@ struct Rows<float, D> {
 #pragma unroll
     for (int c = 0; c < NB * 4; ++c) o[c] = f32x4{0, 0, 0, 0};
   }
+  // The exponentials' reference follows the maximum only where that has
+  // outgrown it by 2^8, so that the sums are rarely scaled.
+  __device__ __forceinline__ void grow(float top) {
+    if (__any(top > m + 8.0f)) {
+      const float mn = top > m + 8.0f ? top : m;     // a query's own scores alone decide
+      const float f = exp2_(m - ref(mn));
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int c = 0; c < NB * 4; ++c) o[c] *= f;
+    }
+  }
+
   __device__ __forceinline__ void load_q(const float* row, int g) {
 #pragma unroll
     for (int c = 0; c < C; ++c) q[c] = *reinterpret_cast<const f32x4*>(row + 16 * c + 4 * g);
@@ -237,8 +267,7 @@ struct Rows<float, D> {
   struct Keys {
     f32x4 k[C], v[4][NB];
   };
-  static __device__ __forceinline__ void fetch(const Pages<float, D>& pg, int key0, int n, int g, Keys& x) {
-    const int64_t at = pg.at(key0);
+  static __device__ __forceinline__ void fetch(const Pages<float, D>& pg, int64_t at, int n, int g, Keys& x) {
 #pragma unroll
     for (int c = 0; c < C; ++c) x.k[c] = *reinterpret_cast<const f32x4*>(pg.k + at + n * D + 16 * c + 4 * g);
 #pragma unroll
@@ -252,7 +281,7 @@ struct Rows<float, D> {
   __device__ __forceinline__ void step(const Pages<float, D>& pg, int key0, int limit, int mine, float scale, int n,
                                        int g) {
     Keys x;
-    fetch(pg, key0, n, g, x);
+    fetch(pg, pg.at(key0), n, g, x);
     step<CAUSAL>(x, key0, limit, mine, scale, n, g);
   }
 
@@ -283,15 +312,12 @@ struct Rows<float, D> {
       for (int j = 0; j < 4; ++j) z[j] = key0 + 4 * g + j < mine ? z[j] : kNone;
     }
     const float top = max_groups(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
-    const float mn = fmaxf(m, top);
-    const float r = ref(mn), f = exp2_(m - r);
-    m = mn;
+    grow(top);
+    const float r = ref(m);
     float p[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) p[j] = exp2_(z[j] - r);
-    l = l * f + ((p[0] + p[1]) + (p[2] + p[3]));
-#pragma unroll
-    for (int c = 0; c < NB * 4; ++c) o[c] *= f;
+    l += (p[0] + p[1]) + (p[2] + p[3]);
     bool odd = false;
     if constexpr (CAUSAL) odd = __any(key0 + 16 > mine) && __any(!finite(v));
     if (!odd) {
@@ -349,14 +375,20 @@ struct Rows<float, D> {
 
 // ------------------------------------------------------------------ prefill
 
-constexpr int kPrefillWaves = 4;
+constexpr int kPrefillWaves = 4, kPrefillRows = 32;
 
 // fp32 (bf16 goes to attn_tile.hip). One workgroup: a tile of positions of one
-// sequence for `pack` heads of a group, a wave per 16 positions of a head.
+// sequence for `pack` heads of a group, 32 rows in all. Two waves to 16 rows,
+// every other 16 keys each, joined through LDS: a chain of steps is half as
+// long as with one, which is what a batch of few long sequences waits for.
 template <int D>
 __global__ __launch_bounds__(64 * kPrefillWaves, 2) void attn_prefill_kernel(AttnArgs a, PrefillPlan p, Parts parts) {
+  using R = Rows<float, D>;
+  constexpr int NO = R::NB * 4;
+  __shared__ f32x4 so[2][NO][64];
+  __shared__ float sml[2][2][64];
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-  const int wave = uniform(threadIdx.x >> 6);
+  const int wave = uniform(threadIdx.x >> 6), sub = wave & 1, turn = wave >> 1;
   const int units = a.Hq / p.pack;
   const int unit = blockIdx.x % units;
   TileAt at;
@@ -367,44 +399,60 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void attn_prefill_kernel(Att
     if (static_cast<int>(blockIdx.y) >= count) return;
   }
   const int nq = at.nq, q0 = at.q0, len = at.len;
-  const int h = unit * p.pack + wave % p.pack;
-  const int pos0 = at.tile * p.tile_pos + 16 * (wave / p.pack);
-  if (pos0 >= nq) return;
+  const int h = unit * p.pack + sub % p.pack;
+  const int pos0 = at.tile * p.tile_pos + 16 * (sub / p.pack);
   const int pos = pos0 + n;
   const int row = q0 + (pos < nq ? pos : nq - 1);
   const int64_t first = static_cast<int64_t>(len) - nq + 1;        // keys that position 0 sees
   int mine = static_cast<int>(first + pos < 0 ? 0 : first + pos);
   if (mine > len) mine = len;
   const int top = pos0 + 15 < nq ? pos0 + 15 : nq - 1;
-  int end = static_cast<int>(first + top < 0 ? 0 : first + top);
+  int end = pos0 < nq && first + top > 0 ? static_cast<int>(first + top) : 0;
   const int from = static_cast<int>(blockIdx.y) * chunk;
   if (count > 1 && end > from + chunk) end = from + chunk;
-  Rows<float, D> r;
+  R r;
   r.init();
   r.load_q(static_cast<const float*>(a.Q) + row * a.ldq + static_cast<int64_t>(h) * D, g);
-  if (from < end) {
+  if (from + 16 * turn < end) {
     Pages<float, D> pg{static_cast<const float*>(a.Kc), static_cast<const float*>(a.Vc),
                    a.page_table + static_cast<int64_t>(at.b) * a.max_pages, (len - 1) >> a.page_shift,
                    a.page_shift, a.n_pages, a.Hkv, h / (a.Hq / a.Hkv)};
-    // the next keys are on their way while these are worked on
-    typename Rows<float, D>::Keys x[2];
-    r.fetch(pg, from, n, g, x[0]);
-    for (int key = from;;) {
-      r.fetch(pg, key + 16, n, g, x[1]);
+    // the next keys are on their way while these are worked on, and the page
+    // of those after them
+    typename R::Keys x[2];
+    int key = from + 16 * turn;
+    int entry = pg.entry(key + 32);
+    r.fetch(pg, pg.at(key), n, g, x[0]);
+    while (true) {
+      r.fetch(pg, pg.at(key + 32, entry), n, g, x[1]);
+      entry = pg.entry(key + 64);
       r.template step<true>(x[0], key, len, mine, a.scale_log2, n, g);
-      if ((key += 16) >= end) break;
-      r.fetch(pg, key + 16, n, g, x[0]);
+      if ((key += 32) >= end) break;
+      r.fetch(pg, pg.at(key + 32, entry), n, g, x[0]);
+      entry = pg.entry(key + 64);
       r.template step<true>(x[1], key, len, mine, a.scale_log2, n, g);
-      if ((key += 16) >= end) break;
+      if ((key += 32) >= end) break;
     }
   }
-  const float l = sum_groups(r.l);
-  if (pos >= nq) return;
+  float l = sum_groups(r.l);
+  if (turn) {
+#pragma unroll
+    for (int c = 0; c < NO; ++c) so[sub][c][lane] = r.o[c];
+    sml[sub][0][lane] = r.m;
+    sml[sub][1][lane] = l;
+  }
+  __syncthreads();
+  if (turn || pos >= nq) return;
+  const float m1 = sml[sub][0][lane], m = fmaxf(r.m, m1);
+  const float f0 = exp2_(r.m - ref(m)), f1 = exp2_(m1 - ref(m));
+  l = f0 * l + f1 * sml[sub][1][lane];
+#pragma unroll
+  for (int c = 0; c < NO; ++c) r.o[c] = r.o[c] * f0 + so[sub][c][lane] * f1;
   if (count > 1) {
     if (from >= mine && from > 0) return;            // the join takes only parts that begin before `mine`
     const int64_t slot = (static_cast<int64_t>(row) * a.Hq + h) * parts.splits + blockIdx.y;
     r.store_f32(parts.o + slot * D, g);
-    if (g == 0) parts.ml[slot] = float2{r.m, l};
+    if (g == 0) parts.ml[slot] = float2{m, l};
   } else {
     r.store(static_cast<float*>(a.O) + row * a.ldo + static_cast<int64_t>(h) * D, g, inverse(l));
   }
@@ -698,8 +746,8 @@ PrefillPlan plan_prefill(int bf16, int B, int T, int Hq, int Hkv, int D, int max
   PrefillPlan p{};
   const int G = Hq / Hkv;
   p.tiled = bf16;
-  p.pack = p.tiled && G % 8 == 0 ? 8 : G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1;
-  p.tile_pos = (p.tiled ? kTileRows : 16 * kPrefillWaves) / p.pack;
+  p.pack = p.tiled && G % 8 == 0 ? 8 : p.tiled && G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1;
+  p.tile_pos = (p.tiled ? kTileRows : kPrefillRows) / p.pack;
   p.target = p.tiled ? 256 : 768;     // workgroups that run at once: one of the tile kernel's a CU, three of the other
   int64_t splits = p.target / (static_cast<int64_t>(ceil_div(T, p.tile_pos)) * (Hq / p.pack));
   if (splits > max_len / 256) splits = max_len / 256;
