@@ -467,7 +467,7 @@ constexpr int kDecodeWaves = 4;
 // are those of all sequences (row R: sequence R / G, head R % G of the
 // group); a sequence's own parts have its G rows.
 template <typename T, int D>
-__global__ __launch_bounds__(64 * kDecodeWaves) void attn_decode_kernel(AttnArgs a, DecodePlan p, Parts parts) {
+__global__ __launch_bounds__(64 * kDecodeWaves, sizeof(T) == 2 ? 3 : 2) void attn_decode_kernel(AttnArgs a, DecodePlan p, Parts parts) {
   __shared__ float so[kDecodeWaves][16][D + 4];
   __shared__ float sml[kDecodeWaves][2][16];
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
