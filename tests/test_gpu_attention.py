@@ -453,3 +453,14 @@ def test_prefill_in_place():
     S.attn_prefill(q, *args, max_len=1500, out=q)
     torch.cuda.synchronize()
     assert torch.equal(q, apart)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_prefill_many_sequences(dtype):
+    """More sequences than a wave has lanes, and as many as it has: empty
+    ones, equal lengths, old contexts among them."""
+    new = [(7 * i) % 5 for i in range(130)]
+    kv = [n + (11 * i) % 23 if n else (i % 3) for i, n in enumerate(new)]
+    run_prefill(21, new, kv, 2, 1, 64, 16, dtype)
+    run_prefill(22, new[:64], kv[:64], 2, 1, 64, 16, dtype)
+    run_prefill(23, [70, 0, 70, 1, 33, 70], [70, 9, 75, 300, 33, 70], 2, 2, 64, 16, dtype)

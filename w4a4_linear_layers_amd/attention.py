@@ -118,7 +118,7 @@ def _shape3(t, what):
 def _out(out, q, shape, cache):
     """(output, its row stride)"""
     if out is None:
-        return torch.empty(shape, dtype=q.dtype, device=q.device), shape[1] * shape[2]
+        return q.new_empty(shape), shape[1] * shape[2]
     if out.shape != shape:
         raise ValueError(f"out must be of shape {tuple(shape)}")
     return out, _rows(out, shape, cache, "out")
@@ -131,7 +131,7 @@ def _space(workspace, need, q):
             raise ValueError("sizes that the library does not take")
         return None, None, 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty((need + 3) // 2)       # (of q's type: at least two bytes each)
         return workspace, workspace.data_ptr(), need
     size = workspace.numel() * workspace.element_size()
     if not workspace.is_cuda or not workspace.is_contiguous() or size < need:

@@ -392,7 +392,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void attn_prefill_kernel(Att
   const int units = a.Hq / p.pack;
   const int unit = blockIdx.x % units;
   TileAt at;
-  if (!find_tile(a, p.tile_pos, blockIdx.x / units, at)) return;
+  if (!find_tile<true>(a, p.tile_pos, blockIdx.x / units, at)) return;
   int chunk = 0, count = 1;
   if (p.splits > 1) {
     count = parts_for(a, p, at.total, chunk);

@@ -49,16 +49,17 @@ __device__ __forceinline__ int bounded_cu(const AttnArgs& a, int i) {
   return n < 0 ? 0 : n < a.T ? n : a.T;
 }
 
-// Sum and maximum over the wave's lanes.
-__device__ __forceinline__ int wave_sum(int v) {
+// Sums over the lanes up to each one, and over all.
+__device__ __forceinline__ int wave_scan(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);      // row_shr:1, 2, 4, 8
   v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
   v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
   v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
   v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);      // row_bcast:15, 31
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
-  return __builtin_amdgcn_readlane(v, 63);
+  return v;
 }
+__device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_scan(v), 63); }
 
 // One tile of tile_pos positions: sequence b (its first packed row, rows and
 // keys), the tile's number within it; and how many tiles there are in all.
@@ -67,13 +68,17 @@ struct TileAt {
 };
 
 // Tile `idx` of all sequences; false past the last. Up to 64 sequences lie in
-// the lanes, and tiles come in the order of the keys they see, most first, so
-// that the workgroups that run last are short: with class = (keys before the
-// tile) / tile_pos, the class of tile idx is the largest c with more than idx
-// tiles of class >= c, found by bisection. (Sequence by sequence, the longest
-// first: 169 us against 157 for three fp32 sequences of 500 to 2000 tokens,
-// even for bf16.) More sequences than lanes come one after another, each one's
-// longest tile first.
+// the lanes and come in an order in which the workgroups that run last are
+// short. BY_KEYS: by the keys a tile sees, most first: with class = (keys
+// before the tile) / tile_pos, the class of tile idx is the largest c with
+// more than idx tiles of class >= c, found by bisection. Otherwise sequence by
+// sequence, the one with the most keys first, each one's longest tile first:
+// sorted by counting, which takes a fifth of the bisection's 2000 cycles. (The
+// fp32 kernel, whose workgroups share a CU, gains from the former, 157 us
+// against 169 for three sequences of 500 to 2000 tokens; on LDS tiles both
+// orders run alike.) More sequences than lanes come one after another, each
+// one's longest tile first.
+template <bool BY_KEYS>
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile_pos, int idx, TileAt& at) {
   const int lane = threadIdx.x & 63;
   const auto load = [&](int i, int& first, int& n, int& len, int& tiles) {
@@ -93,41 +98,59 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile_pos, int i
   int first, n, len, tiles;
   if (a.B <= 64) {
     load(lane, first, n, len, tiles);
-    at.total = wave_sum(tiles);
-    if (idx >= at.total) return false;
-    const int base = len > n ? (len - n) / tile_pos : 0;
-    const auto from_class = [&](int c) {           // tiles of class >= c
-      const int k = base + tiles - c;
-      return wave_sum(k < 0 ? 0 : k < tiles ? k : tiles);
-    };
-    int lo = 0, hi = (a.max_len + a.T) / tile_pos + 2;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (from_class(mid) > idx) lo = mid;
-      else hi = mid;
+    if (a.B == 1) {
+      at.total = __builtin_amdgcn_readfirstlane(tiles);
+      if (idx >= at.total) return false;
+      take(0, 0, first, n, len, at.total - 1 - idx);
+      return true;
     }
-    lo = uniform(lo);
-    const int rank = idx - from_class(lo + 1);
-    const bool has = base <= lo && lo < base + tiles;
-    const unsigned long long all = __ballot(has);
-    const int before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(all >> 32),
-                                                 __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(all), 0));
-    const int from = __builtin_ctzll(__ballot(has && before == rank));
-    take(from, from, first, n, len, lo - __builtin_amdgcn_readlane(base, from));
+    if constexpr (BY_KEYS) {
+      at.total = wave_sum(tiles);
+      if (idx >= at.total) return false;
+      const int base = len > n ? (len - n) / tile_pos : 0;
+      const auto from_class = [&](int c) {         // tiles of class >= c
+        const int k = base + tiles - c;
+        return wave_sum(k < 0 ? 0 : k < tiles ? k : tiles);
+      };
+      int lo = 0, hi = (a.max_len + a.T) / tile_pos + 2;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (from_class(mid) > idx) lo = mid;
+        else hi = mid;
+      }
+      lo = uniform(lo);
+      const int rank = idx - from_class(lo + 1);
+      const bool has = base <= lo && lo < base + tiles;
+      const unsigned long long all = __ballot(has);
+      const int before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(all >> 32),
+                                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(all), 0));
+      const int from = __builtin_ctzll(__ballot(has && before == rank));
+      take(from, from, first, n, len, lo - __builtin_amdgcn_readlane(base, from));
+    } else {
+      int rank = 0;                                // sequences before this one; those past B stay last
+      for (int j = 0; j < a.B; ++j) {
+        const int other = __builtin_amdgcn_readlane(len, j);
+        rank += other > len || (other == len && j < lane) ? 1 : 0;
+      }
+      rank = lane < a.B ? rank : lane;
+      const int order = __builtin_amdgcn_ds_permute(rank << 2, lane);
+      const int sorted = __builtin_amdgcn_ds_permute(rank << 2, tiles);
+      const int upto = wave_scan(sorted);
+      at.total = __builtin_amdgcn_readlane(upto, 63);
+      if (idx >= at.total) return false;
+      const int place = __builtin_ctzll(__ballot(upto > idx));
+      const int from = __builtin_amdgcn_readlane(order, place);
+      take(from, from, first, n, len, __builtin_amdgcn_readlane(upto, place) - 1 - idx);
+    }
     return true;
   }
   bool found = false;
   at.total = 0;
   for (int start = 0; start < a.B; start += 64) {
     load(start + lane, first, n, len, tiles);
-    const int sum = wave_sum(tiles);
+    const int upto = wave_scan(tiles);
+    const int sum = __builtin_amdgcn_readlane(upto, 63);
     if (!found && idx < at.total + sum) {
-      int upto = tiles;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int v = __shfl_up(upto, off, 64);
-        if (lane >= off) upto += v;
-      }
       const int want = idx - at.total;
       const int from = __builtin_ctzll(__ballot(upto > want));
       take(start + from, from, first, n, len, __builtin_amdgcn_readlane(upto, from) - 1 - want);

@@ -113,7 +113,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
     const int units = a.Hq / p.pack;
     const int unit = blockIdx.x % units;
     TileAt at;
-    if (!find_tile(a, p.tile_pos, blockIdx.x / units, at)) return;
+    if (!find_tile<false>(a, p.tile_pos, blockIdx.x / units, at)) return;
     if (p.splits > 1) {
       const int count = parts_for(a, p, at.total, chunk);
       if (static_cast<int>(blockIdx.y) >= count) return;
@@ -322,7 +322,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       for (int i = 0; i < kWaves; ++i) odd |= odd_rows[slot][i];
     }
     if (!uniform(odd)) {
+      __builtin_amdgcn_sched_barrier(0);
       values(slot, [](int) {});
+#pragma unroll
+      for (int i = 0; i < 6; ++i) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+      for (int i = 0; i < 4 * DB; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        if (i + 6 < 4 * DB) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
       return;
     }
 #pragma unroll
