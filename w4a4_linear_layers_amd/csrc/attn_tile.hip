@@ -41,7 +41,20 @@ __device__ __forceinline__ void dma16(const void* sbase, uint32_t voff, uint32_t
   asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
                :: "v"(voff), "s"(sbase), "s"(lds_chunk) : "m0");
 }
+// The same from an address of each lane's own.
+__device__ __forceinline__ void dma16(const void* src, uint32_t lds_chunk) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(src), "s"(lds_chunk) : "m0");
+}
 #pragma clang diagnostic pop
+
+// Pointer of another lane.
+template <typename T>
+__device__ __forceinline__ T* shuffle(T* p, int from) {
+  const uint64_t x = reinterpret_cast<uint64_t>(p);
+  const uint64_t lo = static_cast<uint32_t>(__shfl(static_cast<int>(x), from, 64));
+  const uint64_t hi = static_cast<uint32_t>(__shfl(static_cast<int>(x >> 32), from, 64));
+  return reinterpret_cast<T*>(hi << 32 | lo);
+}
 
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 template <int N>
@@ -88,7 +101,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
   constexpr int kRows = 1024 / kRow;             // rows of one wave load
   constexpr int kLoads = kTile / (1024 * kWaves);
   constexpr int C = D / 16, DB = D / 32;
-  __shared__ __align__(1024) uint8_t smem[2 * kRing * kTile];   // K tiles, then V tiles
+  // K tiles, then V tiles, and half a tile per wave counted with them for Q at
+  // the start (in K's third place and from V's second on, which are loaded
+  // only when Q is in registers) and O at the end.
+  __shared__ __align__(1024) uint8_t smem[(2 * kRing + 1) * kTile];
   __shared__ __align__(16) int odd_rows[kRing][kWaves];         // V tiles: whether a wave's rows hold NaN or infinities
 
   const int lane = threadIdx.x & 63, n = lane & 31, half = lane >> 5;
@@ -137,15 +153,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
   const int from = static_cast<int>(blockIdx.y) * chunk;
   if (split && end > from + chunk) end = from + chunk;
 
-  // Q as the second operand: lane (query n, half) holds values 16 c + 8 half .. + 7.
-  // A negative scale goes into Q's sign, so the largest product is the largest score.
-  u32x4 q[C];
-  {
-    const __bf16* src = static_cast<const __bf16*>(a.Q) + row * a.ldq + static_cast<int64_t>(head) * D + 8 * half;
-    const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-#pragma unroll
-    for (int c = 0; c < C; ++c) q[c] = *reinterpret_cast<const u32x4*>(src + 16 * c) ^ flip;
-  }
+  u32x4 q[C];              // Q as the second operand: lane (query n, half) holds values 16 c + 8 half .. + 7
   // (not 0, so that a masked score stays -inf)
   const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
 
@@ -415,6 +423,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
     look_up(0, pages0);
     look_up(1, pages1);
     look_up(2, pages);
+    // Q by whole rows through LDS: read as an operand from memory, each load
+    // would touch 32 rows, 4000 cycles for the workgroup's 64.
+    const int qplace = wave < 2 ? 2 * kTile + wave * (kTile / 2) : (kRing + 1) * kTile + (wave - 2) * (kTile / 2);
+    const char* qrow = reinterpret_cast<const char*>(static_cast<const __bf16*>(a.Q) + row * a.ldq +
+                                                     static_cast<int64_t>(head) * D);
+#pragma unroll
+    for (int k = 0; k < 32 / kRows; ++k) {
+      const int r = kRows * k + lr;
+      dma16(shuffle(qrow, r) + ((lp ^ swizzle_k<D>(r)) << 4), uniform(lds0 + qplace + 1024 * k));
+    }
     place(pages0, 0, kat);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) load_k(i, 0);
@@ -427,7 +445,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       load_v(i, 0);
       vat[i] = kat[i];
     }
-    wait_loads_but<2 * kLoads>();
+    wait_loads_but<2 * kLoads>();                  // Q, K(0)
+    // A negative scale goes into Q's sign, so that the largest product is the
+    // largest score.
+    const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int c = 0; c < C; ++c) q[c] = *reinterpret_cast<const u32x4*>(smem + qplace + (kbase ^ (c << 5))) ^ flip;
     barrier();
 #pragma unroll
     for (int j = 0; j < 2 * kLoads; ++j) start_load(j);
@@ -468,28 +491,55 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
     wait_loads();                                  // nothing may land here after the workgroup is gone
   }
 
+  // o[d][i]: value 32 d + 8 (i / 4) + 4 half + i % 4 of query n. Through LDS,
+  // a wave's rows apart, so that rows are stored whole.
   l = sum_halves(l);
-  if (!valid) return;
-  // o[d][i]: value 32 d + 8 (i / 4) + 4 half + i % 4 of query n
+  constexpr int kPad = kRow + 16;
+  uint8_t* const mine_o = smem + wave * 32 * kPad;
+  const auto store_rows = [&](char* to) {          // kRow bytes of each row; `to` of lane r: row r, null for none
+    constexpr int N = 32 / kRows;
+    char* at[N];
+    u32x4 v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int r = kRows * k + lr;
+      at[k] = shuffle(to, r);
+      v[k] = *reinterpret_cast<const u32x4*>(mine_o + r * kPad + lp * 16);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (at[k]) *reinterpret_cast<u32x4*>(at[k] + lp * 16) = v[k];
+  };
+  barrier();                                       // no wave reads tiles any more
   if (split) {
-    if (!PREFIX && from >= mine && from > 0) return;   // the join takes only parts that begin before `mine`
+    // (the join takes only parts that begin before `mine`)
+    const bool wanted = valid && (PREFIX || from < mine || from == 0);
     const int64_t slot = (static_cast<int64_t>(row) * a.Hq + head) * parts.splits + blockIdx.y;
-    float* to = parts.o + slot * D + 4 * half;
+    char* to = wanted ? reinterpret_cast<char*>(parts.o + slot * D) : nullptr;
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<f32x4*>(to + 32 * d + 2 * i) = f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
-    if (half == 0) parts.ml[slot] = float2{m, l};
+      for (int d = 0; d < DB / 2; ++d) {
+        const f32x16& x = o[h * (DB / 2) + d];
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<f32x4*>(mine_o + n * kPad + (32 * d + 2 * i + 4 * half) * 4) =
+              f32x4{x[i], x[i + 1], x[i + 2], x[i + 3]};
+      }
+      store_rows(to ? to + h * kRow : nullptr);
+    }
+    if (wanted && half == 0) parts.ml[slot] = float2{m, l};
   } else {
     const float inv = inverse(l);
-    __bf16* to = static_cast<__bf16*>(a.O) + row * a.ldo + static_cast<int64_t>(head) * D + 4 * half;
+    char* to = valid ? reinterpret_cast<char*>(static_cast<__bf16*>(a.O) + row * a.ldo + static_cast<int64_t>(head) * D)
+                     : nullptr;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<u32x2*>(to + 32 * d + 2 * i) =
+        *reinterpret_cast<u32x2*>(mine_o + n * kPad + (32 * d + 2 * i + 4 * half) * 2) =
             u32x2{pack2(o[d][i] * inv, o[d][i + 1] * inv), pack2(o[d][i + 2] * inv, o[d][i + 3] * inv)};
+    store_rows(to);
   }
 }
 
