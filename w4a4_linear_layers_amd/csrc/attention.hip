@@ -779,7 +779,7 @@ DecodePlan plan_decode(int bf16, int B, int Hq, int Hkv, int D, int prefix_len, 
   const int64_t rows = static_cast<int64_t>(B) * G;
   p.tiles = ceil_div(G, 16);
   int64_t s = ceil_div(8192, static_cast<int64_t>(B) * Hkv * p.tiles);
-  p.chunk = cut(max_len, s);
+  p.chunk = cut(max_len, s, static_cast<int64_t>(B) * Hkv * p.tiles >= 512 ? 256 : 128);
   p.splits = static_cast<int>(s);
   if (prefix_len > 0) {
     p.ptiled = bf16 && rows >= kPrefixTileRows;

@@ -25,7 +25,7 @@ using namespace attn;
 
 constexpr int kWaves = 8;
 constexpr int kKeys = 64;          // keys of a tile
-constexpr int kRing = 3;           // tiles of K and of V in LDS
+constexpr int kRing = 4;           // tiles of K and of V in LDS (a power of two)
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
@@ -102,8 +102,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
   constexpr int kLoads = kTile / (1024 * kWaves);
   constexpr int C = D / 16, DB = D / 32;
   // K tiles, then V tiles, and half a tile per wave counted with them for Q at
-  // the start (in K's third place and from V's second on, which are loaded
-  // only when Q is in registers) and O at the end.
+  // the start (in K's last place and V's last two, which are loaded only when Q
+  // is in registers) and O at the end.
   __shared__ __align__(1024) uint8_t smem[(2 * kRing + 1) * kTile];
   __shared__ __align__(16) int odd_rows[kRing][kWaves];         // V tiles: whether a wave's rows hold NaN or infinities
 
@@ -371,16 +371,19 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
   // phase t - 1 and matrix phase t in the second.
   //
   // In its matrix phase of tile t a wave starts its share of the loads of K(t
-  // + 2) and V(t + 1), into the places of K(t - 1) and V(t - 2), last read in
-  // period t - 1; at the end of period t it waits for the batch before, K(t +
-  // 1) and V(t). Every batch has the same number of loads: past the last tile
-  // they fetch its pages again, into places no longer read.
+  // + kRing - 1) and V(t + kRing - 2), into the places of K(t - 1) and V(t -
+  // 2), last read in period t - 1; at the end of period t it waits for K(t +
+  // 1) and V(t), while the kRing - 2 batches after them are under way. Every
+  // batch has the same number of loads: past the last tile they fetch its pages
+  // again, into places no longer read. (Four places: keys that no other
+  // workgroup has fetched yet come from HBM.)
   const int steps = from < end ? (end - from + kKeys - 1) / kKeys : 0;
   const bool second = wave >= kWaves / 2;
   if (steps > 0) {
     int pages[kLoads];                             // of the next K tile to load
     uint64_t kat[kLoads], vat[kLoads];             // rows of the K and V tile to load
-    int t = 0, slot = 0, slot1 = 1, slot2 = 2;     // places of tiles t, t + 1, t + 2 (and t - 1)
+    int t = 0, slot = 0;                           // tile t and its place
+    const auto place_of = [&](int ahead) { return (slot + ahead) & (kRing - 1); };
     const auto load_k = [&](int i, int at) {
       dma16(static_cast<const char*>(a.Kc) + kat[i], koff[i], uniform(lds0 + at * kTile + 1024 * (wave + kWaves * i)));
     };
@@ -388,17 +391,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       dma16(static_cast<const char*>(a.Vc) + vat[i], voff[i],
             uniform(lds0 + (kRing + at) * kTile + 1024 * (wave + kWaves * i)));
     };
-    const auto start_load = [&](int j) {           // of 2 kLoads: V(t + 1), K(t + 2)
+    const auto start_load = [&](int j) {           // of 2 kLoads: V(t + kRing - 2), K(t + kRing - 1)
       if (j < kLoads) {
-        load_v(j, slot1);
+        load_v(j, place_of(kRing - 2));
       } else if (j < 2 * kLoads) {
-        if (j == kLoads) place(pages, t + 2, kat);
-        load_k(j - kLoads, slot2);
+        if (j == kLoads) place(pages, t + kRing - 1, kat);
+        load_k(j - kLoads, place_of(kRing - 1));
         vat[j - kLoads] = kat[j - kLoads];
       }
     };
     const auto finish_loads = [&] {                // K(t + 1), V(t)
-      wait_loads_but<2 * kLoads>();
+      wait_loads_but<(kRing - 2) * 2 * kLoads>();
       if (from + (t + 1) * kKeys > whole) look_over(t, slot);
     };
     const auto after_matrix = [&](bool ends) {
@@ -406,26 +409,24 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
         finish_loads();
         barrier();
       }
-      look_up(t + 3, pages);                       // (a scalar load; among LDS reads it would stall them)
+      look_up(t + kRing, pages);                   // (a scalar load; among LDS reads it would stall them)
     };
     const auto after_vector = [&](bool ends) {
       if (ends) {
         finish_loads();
         barrier();
       }
-      const int s0 = slot;
-      slot = slot1;
-      slot1 = slot2;
-      slot2 = s0;
+      slot = place_of(1);
       ++t;
     };
-    int pages0[kLoads], pages1[kLoads];
-    look_up(0, pages0);
-    look_up(1, pages1);
-    look_up(2, pages);
+    int early[kRing - 1][kLoads];
+#pragma unroll
+    for (int u = 0; u < kRing - 1; ++u) look_up(u, early[u]);
+    look_up(kRing - 1, pages);
     // Q by whole rows through LDS: read as an operand from memory, each load
     // would touch 32 rows, 4000 cycles for the workgroup's 64.
-    const int qplace = wave < 2 ? 2 * kTile + wave * (kTile / 2) : (kRing + 1) * kTile + (wave - 2) * (kTile / 2);
+    const int qplace = wave < 2 ? (kRing - 1) * kTile + wave * (kTile / 2)
+                                : (2 * kRing - 2) * kTile + (wave - 2) * (kTile / 2);
     const char* qrow = reinterpret_cast<const char*>(static_cast<const __bf16*>(a.Q) + row * a.ldq +
                                                      static_cast<int64_t>(head) * D);
 #pragma unroll
@@ -433,19 +434,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       const int r = kRows * k + lr;
       dma16(shuffle(qrow, r) + ((lp ^ swizzle_k<D>(r)) << 4), uniform(lds0 + qplace + 1024 * k));
     }
-    place(pages0, 0, kat);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) load_k(i, 0);
+    for (int u = 0; u < kRing - 1; ++u) {          // K(u) and V(u - 1)
+      place(early[u], u, kat);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) vat[i] = kat[i];
-    place(pages1, 1, kat);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      load_k(i, 1);
-      load_v(i, 0);
-      vat[i] = kat[i];
+      for (int i = 0; i < kLoads; ++i) {
+        load_k(i, u);
+        if (u > 0) load_v(i, u - 1);
+        vat[i] = kat[i];
+      }
     }
-    wait_loads_but<2 * kLoads>();                  // Q, K(0)
+    wait_loads_but<(kRing - 2) * 2 * kLoads>();    // Q, K(0)
     // A negative scale goes into Q's sign, so that the largest product is the
     // largest score.
     const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
@@ -467,7 +466,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
         __builtin_amdgcn_s_setprio(1);
         __builtin_amdgcn_sched_barrier(0);
         scores(slot);
-        values(slot2, start_load);
+        values(place_of(kRing - 1), start_load);
         feed_matrix();
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(0);
@@ -484,7 +483,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
         for (int j = 0; j < 2 * kLoads; ++j) start_load(j);
         if (from + t * kKeys < high) scores(slot);
       }
-      if (from + (t - 1) * kKeys < high) masked_values(t - 1, slot2);
+      if (from + (t - 1) * kKeys < high) masked_values(t - 1, place_of(kRing - 1));
       if (t == steps) break;
       after_matrix(second);
     }
