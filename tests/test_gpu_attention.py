@@ -292,6 +292,8 @@ def run_decode(seed, lens, prefix_len, Hq, Hkv, D, page, dtype, *, scale=None, q
     ([40, 7, 9], 1500, 12, 4, 64, 16),
     ([9] * 70, 1100, 8, 2, 128, 16),        # 280 rows of the prefix to a key/value head
     ([7] * 33, 600, 8, 1, 64, 32),
+    ([9] * 70 + [0], 10801, 8, 2, 128, 16),   # enough work for the LDS tiles
+    ([3] * 17, 22700, 16, 1, 64, 64),
 ])
 def test_decode(dtype, lens, prefix, Hq, Hkv, D, page):
     run_decode(len(lens) + prefix, lens, prefix, Hq, Hkv, D, page, dtype)

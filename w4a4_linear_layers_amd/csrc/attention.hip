@@ -6,6 +6,15 @@
 // fp32; a larger maximum scales l and o by 2^(m_old - m_new). Parts of the
 // keys are joined the same way.
 //
+// The kernels here keep 16 query rows to a wave and read keys and values
+// straight from the cache into registers, each once: a decode's queries of one
+// key/value head are a group's few heads, so its keys are read at the rate of
+// HBM with matrix cores to spare (32 sequences of 513 to 32000 tokens, 64 query
+// and 8 key/value heads, 1.04 GB: 195 us, 5.3 TB/s). fp32 prompts use the same
+// steps (three of 500 to 2000 tokens, 16 heads of 64: 126 us, 86 TFLOP/s of the
+// 154 that a large fp32 product reaches). bf16 prompts and long prefixes of
+// many sequences go to attn_tile.hip.
+//
 // Both products are taken transposed. S^T = K Q^T leaves each lane with
 // scores of one query (column = lane % 16) and four keys per 16 x 16 tile,
 // so the statistics of a query are one value per lane; and as the index that
@@ -690,6 +699,9 @@ __global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs a, PrefillP
   static_cast<T*>(a.O)[t * a.ldo + static_cast<int64_t>(h) * D + tid] = static_cast<T>(y * inverse(l));
 }
 
+// Which join: 32 sequences of 4096 keys, 256 rows: 26.9 us a call with a
+// workgroup a row against 29.5 with a wave; 2048 rows 192 against 194; 3072
+// rows of 1024 keys 83.8 against 82.1.
 constexpr int64_t kFewRows = 2048;
 
 template <typename T, int D, bool PREFILL>
@@ -739,7 +751,15 @@ inline int cut(int len, int64_t& splits, int unit = 128) {
 }  // namespace
 
 constexpr int kTileRows = 256;       // rows of a workgroup of the tile kernel
-constexpr int kPrefixTileRows = 96;  // rows a key/value head from which the prefix goes there
+
+// Work of a prefix (sequences * query heads * keys) from which it goes to the
+// LDS tiles. They take ~13 us before they gain; the 16-row kernel reads the
+// keys from L2 once for every 16 rows. Over 8 key/value heads of 128, bf16,
+// join included, tiles against rows: 8192 keys, 64 rows a head 22.2 against
+// 21.8 us, 96 rows 24.0 against 29.0, 384 rows 34.0 against 75.7; 2048 keys,
+// 256 rows 30.4 against 22.2, 384 rows 24.3 against 27.5; 512 keys, 384 rows
+// 18.6 against 12.8.
+constexpr int64_t kPrefixTileWork = 6000000;
 
 PrefillPlan plan_prefill(int bf16, int B, int T, int Hq, int Hkv, int D, int max_len) {
   (void)B;
@@ -748,7 +768,11 @@ PrefillPlan plan_prefill(int bf16, int B, int T, int Hq, int Hkv, int D, int max
   p.tiled = bf16;
   p.pack = p.tiled && G % 8 == 0 ? 8 : p.tiled && G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1;
   p.tile_pos = (p.tiled ? kTileRows : kPrefillRows) / p.pack;
-  p.target = p.tiled ? 256 : 768;     // workgroups that run at once: one of the tile kernel's a CU, three of the other
+  // Workgroups that run at once: one of the tile kernel's a CU, three of the
+  // other. Few new tokens over many keys leave CUs idle unless the keys are
+  // cut: 16 tokens of 32 heads over 4096 keys take 21 us with parts and 80
+  // without, 512 over 8192 88 against 164.
+  p.target = p.tiled ? 256 : 768;
   int64_t splits = p.target / (static_cast<int64_t>(ceil_div(T, p.tile_pos)) * (Hq / p.pack));
   if (splits > max_len / 256) splits = max_len / 256;
   if (splits > kMostSplits) splits = kMostSplits;
@@ -778,11 +802,16 @@ DecodePlan plan_decode(int bf16, int B, int Hq, int Hkv, int D, int prefix_len, 
   const int G = Hq / Hkv;
   const int64_t rows = static_cast<int64_t>(B) * G;
   p.tiles = ceil_div(G, 16);
-  int64_t s = ceil_div(8192, static_cast<int64_t>(B) * Hkv * p.tiles);
-  p.chunk = cut(max_len, s, static_cast<int64_t>(B) * Hkv * p.tiles >= 512 ? 256 : 128);
+  // About 8192 parts in all, so that ragged lengths balance (against 2048, 64
+  // sequences of up to 4096 keys: 113 us against 130), of at least 128 keys;
+  // of 256 where there are many sequences and heads (256 sequences of up to
+  // 256 keys: 27 us against 33; one of 4095: 9.4 us against 8.4).
+  const int64_t groups = static_cast<int64_t>(B) * Hkv * p.tiles;
+  int64_t s = ceil_div(8192, groups);
+  p.chunk = cut(max_len, s, groups >= 512 ? 256 : 128);
   p.splits = static_cast<int>(s);
   if (prefix_len > 0) {
-    p.ptiled = bf16 && rows >= kPrefixTileRows;
+    p.ptiled = bf16 && static_cast<int64_t>(B) * Hq * prefix_len >= kPrefixTileWork;
     p.ptiles = ceil_div(rows, p.ptiled ? kTileRows : 16);
     s = ceil_div(p.ptiled ? 256 : 1024, static_cast<int64_t>(Hkv) * p.ptiles);
     p.pchunk = cut(prefix_len, s, p.ptiled ? 64 : 128);

@@ -13,6 +13,13 @@
 // holds (4 h .. 4 h + 3 and 8 + 4 h .. 8 + 4 h + 3). V^T is read from LDS by
 // the transposing reads in the same order. Softmax statistics are one value
 // per lane, and scores never leave the registers.
+//
+// 16384 tokens of 32 query and 8 key/value heads of 128: 1.78 ms, 1.24 PFLOP/s
+// of the visible pairs (a large bf16 product reaches 1.39 here). The matrix
+// cores are busy 69 % of the cycles; under this load the card runs at about
+// 1.7 GHz, so what fewer cycles gain its clock gives back in part. A period of
+// two tiles (one of either wave of a SIMD) takes 2600 cycles, 2048 of them
+// matrix products; a workgroup's start and end another 12000.
 
 #include <type_traits>
 

@@ -4,7 +4,9 @@
 //     y = x * w / sqrt(mean(x^2) + eps),  (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s),
 // queries to Q, keys and the unchanged values to slot[t] of the cache. Every
 // value is read once and written once, so the kernel is bound by HBM for
-// prompts and by latency for single tokens.
+// prompts (8192 tokens of 48 heads of 128 with norms, bf16, 206 MB: 46 us from
+// HBM, 4.5 TB/s; 35 us with the inputs in the last-level cache) and by latency
+// for single tokens (one token 2.4 us, about a launch).
 
 #include "serq_attn.h"
 
@@ -14,7 +16,6 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
-constexpr int kFewTokens = 256;      // below: a workgroup per set of heads
 
 template <typename T>
 struct Elem;
@@ -259,15 +260,24 @@ __global__ __launch_bounds__(64) void rope_append_scalar_kernel(RopeArgs a) {
   }
 }
 
+// A workgroup per set of heads, or per three sets where many tokens are normed:
+// their weights are then loaded once for three heads a lane instead of one.
+// (8192 tokens of 48 heads with norms, bf16: 42 us against 52; 2048 tokens
+// 13.9 against 13.0, 8192 without norms 38.9 against 37.9, one token 3.3
+// against 2.9.)
+constexpr int kManyTokens = 4096;
+
 template <typename T, int D, bool INTER, bool NORM>
 void launch_vector(const RopeArgs& a, hipStream_t st) {
   constexpr int GROUPS = kThreads / (D / Elem<T>::kVec);
   const int sets = (a.Hq + 2 * a.Hkv + GROUPS - 1) / GROUPS;
-  if (a.M < kFewTokens || sets == 1) {
-    rope_append_kernel<T, D, INTER, NORM, 1><<<dim3(a.M, sets), kThreads, 0, st>>>(a);
-  } else {
-    rope_append_kernel<T, D, INTER, NORM, 3><<<dim3(a.M, (sets + 2) / 3), kThreads, 0, st>>>(a);
+  if constexpr (NORM) {
+    if (a.M >= kManyTokens && sets > 1) {
+      rope_append_kernel<T, D, INTER, NORM, 3><<<dim3(a.M, (sets + 2) / 3), kThreads, 0, st>>>(a);
+      return;
+    }
   }
+  rope_append_kernel<T, D, INTER, NORM, 1><<<dim3(a.M, sets), kThreads, 0, st>>>(a);
 }
 
 template <typename T, int D>
