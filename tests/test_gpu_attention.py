@@ -198,6 +198,8 @@ def run_prefill(seed, new, kv, Hq, Hkv, D, page, dtype, *, scale=None, q_pad=0, 
     ([3, 1, 20], [200, 129, 31], 4, 1, 128, 16),
     ([257], [300], 2, 2, 128, 128),
     ([40], [40], 16, 1, 64, 1024),
+    ([500, 301], [500, 511], 8, 1, 128, 16),
+    ([450], [450], 3, 3, 64, 32),
 ])
 def test_prefill(dtype, new, kv, Hq, Hkv, D, page):
     run_prefill(len(new) * 10 + Hq, new, kv, Hq, Hkv, D, page, dtype)
