@@ -314,6 +314,21 @@ def test_decode_without_keys(dtype):
     assert run_decode(1, [0, 0], 0, 4, 2, 128, 16, dtype, max_len=4000).count_nonzero() == 0
 
 
+# Around the bounds where a sequence's keys are cut in parts or taken whole,
+# by four waves or by eight, with few sequences and with many.
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens,Hq,Hkv,D,page", [
+    ([256, 1, 0, 255], 8, 2, 64, 16),
+    ([257, 0, 33, 16], 8, 8, 128, 16),
+    ([512, 511, 1], 20, 1, 64, 32),           # two tiles of query heads
+    ([513, 0, 90], 8, 2, 128, 64),
+    ([1, 0, 700, 16, 1024] + [31] * 27, 16, 8, 64, 16),
+    ([1025, 0, 300] + [5] * 29, 16, 8, 64, 16),
+])
+def test_decode_of_short_caches(dtype, lens, Hq, Hkv, D, page):
+    run_decode(7, lens, 0, Hq, Hkv, D, page, dtype)
+
+
 def test_lengths_beyond_the_bound_are_cut():
     """kv_len above max_len or the table's room counts as that; below 0 as 0."""
     g = gen(9)

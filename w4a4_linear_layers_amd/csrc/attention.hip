@@ -469,14 +469,14 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void attn_prefill_kernel(Att
 
 // ------------------------------------------------------------------- decode
 
-constexpr int kDecodeWaves = 4;
-
 // One workgroup: 16 query rows over one part of the keys, its waves taking
-// steps in turn and joined through LDS. Prefix parts come first: their rows
+// steps in turn and joined through LDS; eight of them where the part is all a
+// sequence has, which is then written as it is. Prefix parts come first: their rows
 // are those of all sequences (row R: sequence R / G, head R % G of the
 // group); a sequence's own parts have its G rows.
-template <typename T, int D>
-__global__ __launch_bounds__(64 * kDecodeWaves, sizeof(T) == 2 ? 3 : 2) void attn_decode_kernel(AttnArgs a, DecodePlan p, Parts parts) {
+template <typename T, int D, int kDecodeWaves>
+__global__ __launch_bounds__(64 * kDecodeWaves, kDecodeWaves == 4 && sizeof(T) == 2 ? 3 : 2) void attn_decode_kernel(
+    AttnArgs a, DecodePlan p, Parts parts) {
   __shared__ float so[kDecodeWaves][16][D + 4];
   __shared__ float sml[kDecodeWaves][2][16];
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
@@ -532,9 +532,9 @@ __global__ __launch_bounds__(64 * kDecodeWaves, sizeof(T) == 2 ? 3 : 2) void att
     sml[wave][1][n] = lw;
   }
   __syncthreads();
-  // the waves' parts joined: 16 threads per row, D / 16 values each
-  constexpr int W = D / 16;
-  const int q = threadIdx.x / 16, d = threadIdx.x % 16 * W;
+  // the waves' parts joined, all threads over the 16 rows
+  constexpr int N = 4 * kDecodeWaves, W = D / N;
+  const int q = threadIdx.x / N, d = threadIdx.x % N * W;
   if (R0 + q >= rows) return;
   float m = kNone;
 #pragma unroll
@@ -548,18 +548,20 @@ __global__ __launch_bounds__(64 * kDecodeWaves, sizeof(T) == 2 ? 3 : 2) void att
     for (int i = 0; i < W; ++i) o[i] = __builtin_fmaf(f, so[w][q][d + i], o[i]);
   }
   const int bq = (R0 + q) / G, hq = kvh * G + (R0 + q) % G;
-  if (p.splits + p.psplits > 1) {
-    const int64_t slot = (static_cast<int64_t>(bq) * a.Hq + hq) * parts.splits + part;
+  if constexpr (kDecodeWaves == 4) {
+    if (p.splits + p.psplits > 1) {
+      const int64_t slot = (static_cast<int64_t>(bq) * a.Hq + hq) * parts.splits + part;
 #pragma unroll
-    for (int i = 0; i < W; i += 4)
-      *reinterpret_cast<f32x4*>(parts.o + slot * D + d + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
-    if (d == 0) parts.ml[slot] = float2{m, l};
-  } else {
-    const float inv = inverse(l);
-    T* out = static_cast<T*>(a.O) + bq * a.ldo + static_cast<int64_t>(hq) * D + d;
-#pragma unroll
-    for (int i = 0; i < W; ++i) out[i] = static_cast<T>(o[i] * inv);
+      for (int i = 0; i < W; i += 4)
+        *reinterpret_cast<f32x4*>(parts.o + slot * D + d + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
+      if (d == 0) parts.ml[slot] = float2{m, l};
+      return;
+    }
   }
+  const float inv = inverse(l);
+  T* out = static_cast<T*>(a.O) + bq * a.ldo + static_cast<int64_t>(hq) * D + d;
+#pragma unroll
+  for (int i = 0; i < W; ++i) out[i] = static_cast<T>(o[i] * inv);
 }
 
 // --------------------------------------------------------------------- join
@@ -726,6 +728,12 @@ void launch_join(const AttnArgs& a, const PrefillPlan& p, int64_t rows, int pspl
   }
 }
 
+template <typename T, int D>
+void launch_decode(const AttnArgs& a, const DecodePlan& p, const Parts& parts, dim3 grid, hipStream_t st) {
+  if (p.waves == 8) attn_decode_kernel<T, D, 8><<<grid, 512, 0, st>>>(a, p, parts);
+  else attn_decode_kernel<T, D, 4><<<grid, 256, 0, st>>>(a, p, parts);
+}
+
 Parts parts_of(void* workspace, int64_t rows, int D, int splits) {
   float* o = static_cast<float*>(workspace);
   return Parts{o, reinterpret_cast<float2*>(o + rows * splits * D), splits};
@@ -804,12 +812,25 @@ DecodePlan plan_decode(int bf16, int B, int Hq, int Hkv, int D, int prefix_len, 
   p.tiles = ceil_div(G, 16);
   // About 8192 parts in all, so that ragged lengths balance (against 2048, 64
   // sequences of up to 4096 keys: 113 us against 130), of at least 128 keys;
-  // of 256 where there are many sequences and heads (256 sequences of up to
-  // 256 keys: 27 us against 33; one of 4095: 9.4 us against 8.4).
+  // of 256 where there are many sequences and heads (96 sequences of 8 heads
+  // after a prefix: 50.6 us against 51.6; one of 4095 keys: 9.4 us against 8.4).
   const int64_t groups = static_cast<int64_t>(B) * Hkv * p.tiles;
   int64_t s = ceil_div(8192, groups);
   p.chunk = cut(max_len, s, groups >= 512 ? 256 : 128);
   p.splits = static_cast<int>(s);
+  p.waves = 4;
+  // Short caches whole: one launch and no join, eight waves a workgroup beyond
+  // 256 keys. Against parts, 32 query heads of 8, up to 512 keys: one sequence
+  // 7.0 us against 7.6 (launched one by one 8.9 against 12.8), 64 19.3 against
+  // 23.8; up to 1024: 96 sequences of 64 heads 53 against 62, 32 of 32 heads
+  // 19 against 20.5, but 8 of them 13.8 against 10.5; up to 2048 keys, 64
+  // sequences: 71 against 67. Four waves up to 256 keys: 256 sequences 38
+  // against 44.
+  if (prefix_len == 0 && max_len <= (groups >= 256 ? 1024 : 512)) {
+    p.splits = 1;
+    p.chunk = max_len > 0 ? max_len : 1;
+    p.waves = max_len > 256 ? 8 : 4;
+  }
   if (prefix_len > 0) {
     p.ptiled = bf16 && static_cast<int64_t>(B) * Hq * prefix_len >= kPrefixTileWork;
     p.ptiles = ceil_div(rows, p.ptiled ? kTileRows : 16);
@@ -830,13 +851,13 @@ hipError_t launch_attn_decode(const AttnArgs& a, const DecodePlan& p, hipStream_
   }
   const int64_t blocks = (p.ptiled ? 0 : static_cast<int64_t>(a.Hkv) * p.ptiles * p.psplits) +
                          static_cast<int64_t>(a.B) * p.tiles * a.Hkv * p.splits;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(64 * kDecodeWaves);
+  const dim3 grid(static_cast<unsigned>(blocks));
   if (a.bf16) {
-    if (a.D == 64) attn_decode_kernel<__bf16, 64><<<grid, block, 0, st>>>(a, p, parts);
-    else attn_decode_kernel<__bf16, 128><<<grid, block, 0, st>>>(a, p, parts);
+    if (a.D == 64) launch_decode<__bf16, 64>(a, p, parts, grid, st);
+    else launch_decode<__bf16, 128>(a, p, parts, grid, st);
   } else {
-    if (a.D == 64) attn_decode_kernel<float, 64><<<grid, block, 0, st>>>(a, p, parts);
-    else attn_decode_kernel<float, 128><<<grid, block, 0, st>>>(a, p, parts);
+    if (a.D == 64) launch_decode<float, 64>(a, p, parts, grid, st);
+    else launch_decode<float, 128>(a, p, parts, grid, st);
   }
   if (p.splits + p.psplits > 1) launch_join<false>(a, PrefillPlan{}, rows, p.psplits, p.chunk, parts, st);
   return hipGetLastError();

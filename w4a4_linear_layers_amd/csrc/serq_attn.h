@@ -62,9 +62,10 @@ struct PrefillPlan {
 };
 
 // How serq_attn_decode is cut: the sequences' own keys in `splits` parts of
-// `chunk`, the prefix in `psplits` parts of `pchunk`; row tiles of 16.
+// `chunk` (one, with no join, where they are few), the prefix in `psplits`
+// parts of `pchunk`; row tiles of 16.
 struct DecodePlan {
-  int splits, chunk, tiles;
+  int splits, chunk, tiles, waves;      // waves of a workgroup
   int psplits, pchunk, ptiles;
   int ptiled;             // the prefix on LDS tiles (attn_tile.hip)
   int64_t bytes;          // workspace
