@@ -108,9 +108,7 @@ struct Rows<__bf16, D> {
     for (int c = 0; c < C; ++c) q[c] = *reinterpret_cast<const u32x4*>(row + 32 * c + 8 * g);
   }
 
-  template <bool CAUSAL>
-  __device__ __forceinline__ void step(const Pages<__bf16, D>& pg, int key0, int limit, int mine, float scale, int n,
-                                       int g) {
+  __device__ __forceinline__ void step(const Pages<__bf16, D>& pg, int key0, int limit, float scale, int n, int g) {
     const int64_t at0 = pg.at(key0), at1 = pg.at(key0 + 16);
     u32x4 k[2][C];
     uint32_t v[8][W / 2];
@@ -151,9 +149,9 @@ struct Rows<__bf16, D> {
     float z[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) z[j] = s[j / 4][j & 3] * scale;
-    if (CAUSAL || key0 + 32 > limit) {
+    if (key0 + 32 > limit) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = key0 + 16 * (j / 4) + 4 * g + (j & 3) < mine ? z[j] : kNone;
+      for (int j = 0; j < 8; ++j) z[j] = key0 + 16 * (j / 4) + 4 * g + (j & 3) < limit ? z[j] : kNone;
     }
     float top = z[0];
 #pragma unroll
@@ -167,41 +165,7 @@ struct Rows<__bf16, D> {
       l += a + b;
       p[j / 2] = pack2(a, b);       // weights in 8 bits each, as the values they multiply
     }
-    const bf16x8 pb = __builtin_bit_cast(bf16x8, u32x4{p[0], p[1], p[2], p[3]});
-    bool odd = false;
-    if constexpr (CAUSAL) odd = __any(key0 + 32 > mine) && __any(!finite(v));
-    if (!odd) {
-      product(v, pb, o);
-    } else {
-      // A value that is not finite lies where some of these queries do not
-      // look, and 0 * inf is not 0: each query takes the product over its own
-      // keys with the others' values cleared.
-      for (int i = 0; i < 16; ++i) {
-        const int lim = __shfl(mine, i, 64);
-        uint32_t u[8][W / 2];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int c = 0; c < W / 2; ++c)
-            u[j][c] = key0 + 16 * (j / 4) + 4 * g + (j & 3) < lim ? v[j][c] : 0;
-        f32x4 t[W];
-#pragma unroll
-        for (int c = 0; c < W; ++c) t[c] = o[c];
-        product(u, pb, t);
-#pragma unroll
-        for (int c = 0; c < W; ++c) o[c] = n == i ? t[c] : o[c];
-      }
-    }
-  }
-
-  static __device__ __forceinline__ bool finite(const uint32_t (&v)[8][W / 2]) {
-    bool ok = true;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int c = 0; c < W / 2; ++c)
-        ok &= (v[j][c] & 0x7F80u) != 0x7F80u && (v[j][c] & 0x7F800000u) != 0x7F800000u;
-    return ok;
+    product(v, __builtin_bit_cast(bf16x8, u32x4{p[0], p[1], p[2], p[3]}), o);
   }
 
   static __device__ __forceinline__ void product(const uint32_t (&v)[8][W / 2], bf16x8 pb, f32x4 (&o)[W]) {
@@ -215,19 +179,7 @@ struct Rows<__bf16, D> {
     }
   }
 
-  // Value index of o[c][j], and how a lane's values lie in memory: for each
-  // j, W consecutive ones from W (4 g + j).
-  __device__ __forceinline__ void store(__bf16* row, int g, float inv) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t w[W / 2];
-#pragma unroll
-      for (int c = 0; c < W; c += 2) w[c / 2] = pack2(o[c][j] * inv, o[c + 1][j] * inv);
-      __bf16* p = row + W * (4 * g + j);
-      if constexpr (W == 8) *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
-      else *reinterpret_cast<u32x2*>(p) = u32x2{w[0], w[1]};
-    }
-  }
+  // O^T as it lies in memory: for each j, W consecutive values from W (4 g + j).
   __device__ __forceinline__ void store_f32(float* row, int g) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -273,81 +225,83 @@ struct Rows<float, D> {
     for (int c = 0; c < C; ++c) q[c] = *reinterpret_cast<const f32x4*>(row + 16 * c + 4 * g);
   }
 
-  struct Keys {
-    f32x4 k[C], v[4][NB];
-  };
-  static __device__ __forceinline__ void fetch(const Pages<float, D>& pg, int64_t at, int n, int g, Keys& x) {
+  static __device__ __forceinline__ void fetch_k(const Pages<float, D>& pg, int64_t at, int n, int g, f32x4 (&k)[C]) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) x.k[c] = *reinterpret_cast<const f32x4*>(pg.k + at + n * D + 16 * c + 4 * g);
+    for (int c = 0; c < C; ++c) k[c] = *reinterpret_cast<const f32x4*>(pg.k + at + n * D + 16 * c + 4 * g);
+  }
+  static __device__ __forceinline__ void fetch_v(const Pages<float, D>& pg, int64_t at, int n, int g,
+                                                 f32x4 (&v)[4][NB]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        x.v[j][b] = *reinterpret_cast<const f32x4*>(pg.v + at + (4 * g + j) * D + 64 * b + 4 * n);
+        v[j][b] = *reinterpret_cast<const f32x4*>(pg.v + at + (4 * g + j) * D + 64 * b + 4 * n);
   }
-
-  template <bool CAUSAL>
-  __device__ __forceinline__ void step(const Pages<float, D>& pg, int key0, int limit, int mine, float scale, int n,
-                                       int g) {
-    Keys x;
-    fetch(pg, pg.at(key0), n, g, x);
-    step<CAUSAL>(x, key0, limit, mine, scale, n, g);
-  }
-
-  template <bool CAUSAL>
-  __device__ __forceinline__ void step(Keys& x, int key0, int limit, int mine, float scale, int n, int g) {
-    auto& k = x.k;
-    auto& v = x.v;
-    if (key0 + 16 > limit) {
+  // Values of keys that are not there: 0, as 0 * inf is not.
+  static __device__ __forceinline__ void clear(f32x4 (&v)[4][NB], int key0, int limit, int g) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = key0 + 4 * g + j < limit;
+    for (int j = 0; j < 4; ++j) {
+      const bool in = key0 + 4 * g + j < limit;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[j][b][e] = in ? v[j][b][e] : 0.0f;
-      }
+        for (int e = 0; e < 4; ++e) v[j][b][e] = in ? v[j][b][e] : 0.0f;
     }
+  }
+
+  __device__ __forceinline__ void step(const Pages<float, D>& pg, int key0, int limit, float scale, int n, int g) {
+    const int64_t at = pg.at(key0);
+    f32x4 k[C], v[4][NB];
+    fetch_k(pg, at, n, g, k);
+    fetch_v(pg, at, n, g, v);
+    __builtin_amdgcn_sched_barrier(0);       // all loads at once (64 sequences of up to 2048: 119 us against 123)
+    float z[4], p[4];
+    scores(k, scale, z);
+    if (key0 + 16 > limit) {
+      clear(v, key0, limit, g);
+      mask(z, key0, limit, g);
+    }
+    weigh(z, p);
+    product(v, p, o);
+  }
+
+  __device__ __forceinline__ void scores(const f32x4 (&k)[C], float scale, float (&z)[4]) const {
     f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[e & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(k[c][e], q[c][e], s[e & 1], 0, 0, 0);
-    float z[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) z[j] = (s[0][j] + s[1][j]) * scale;
-    if (CAUSAL || key0 + 16 > limit) {
+  }
+  static __device__ __forceinline__ void mask(float (&z)[4], int key0, int mine, int g) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) z[j] = key0 + 4 * g + j < mine ? z[j] : kNone;
-    }
-    const float top = max_groups(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
-    grow(top);
+    for (int j = 0; j < 4; ++j) z[j] = key0 + 4 * g + j < mine ? z[j] : kNone;
+  }
+  __device__ __forceinline__ void weigh(const float (&z)[4], float (&p)[4]) {
+    grow(max_groups(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]))));
     const float r = ref(m);
-    float p[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) p[j] = exp2_(z[j] - r);
     l += (p[0] + p[1]) + (p[2] + p[3]);
-    bool odd = false;
-    if constexpr (CAUSAL) odd = __any(key0 + 16 > mine) && __any(!finite(v));
-    if (!odd) {
-      product(v, p, o);
-    } else {                        // as for bf16: each query over its own keys alone
+  }
+
+  // The product where a value that is not finite lies on a key that some of
+  // these queries do not see, and 0 * inf is not 0: each query takes it over
+  // its own keys with the others' values cleared.
+  __device__ __forceinline__ void product_of_own(const f32x4 (&v)[4][NB], const float (&p)[4], int key0, int mine,
+                                                 int n, int g) {
+#pragma unroll
+    for (int c = 0; c < NB * 4; ++c)
+#pragma unroll 1
       for (int i = 0; i < 16; ++i) {
         const int lim = __shfl(mine, i, 64);
-        f32x4 u[4][NB], t[NB * 4];
+        f32x4 t = o[c];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) u[j][b][e] = key0 + 4 * g + j < lim ? v[j][b][e] : 0.0f;
-#pragma unroll
-        for (int c = 0; c < NB * 4; ++c) t[c] = o[c];
-        product(u, p, t);
-#pragma unroll
-        for (int c = 0; c < NB * 4; ++c) o[c] = n == i ? t[c] : o[c];
+          t = __builtin_amdgcn_mfma_f32_16x16x4f32(key0 + 4 * g + j < lim ? v[j][c / 4][c % 4] : 0.0f, p[j], t, 0, 0, 0);
+        o[c] = n == i ? t : o[c];
       }
-    }
   }
 
   static __device__ __forceinline__ bool finite(const f32x4 (&v)[4][NB]) {
@@ -371,15 +325,14 @@ struct Rows<float, D> {
           o[4 * b + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[j][b][e], p[j], o[4 * b + e], 0, 0, 0);
   }
 
-  __device__ __forceinline__ void store(float* row, int g, float inv) const {
+  __device__ __forceinline__ void store_f32(float* row, int g) const {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<f32x4*>(row + 64 * b + 4 * (4 * g + i)) =
-            f32x4{o[4 * b][i] * inv, o[4 * b + 1][i] * inv, o[4 * b + 2][i] * inv, o[4 * b + 3][i] * inv};
+            f32x4{o[4 * b][i], o[4 * b + 1][i], o[4 * b + 2][i], o[4 * b + 3][i]};
   }
-  __device__ __forceinline__ void store_f32(float* row, int g) const { store(row, g, 1.0f); }
 };
 
 // ------------------------------------------------------------------ prefill
@@ -387,17 +340,24 @@ struct Rows<float, D> {
 constexpr int kPrefillWaves = 4, kPrefillRows = 32;
 
 // fp32 (bf16 goes to attn_tile.hip). One workgroup: a tile of positions of one
-// sequence for `pack` heads of a group, 32 rows in all. Two waves to 16 rows,
-// every other 16 keys each, joined through LDS: a chain of steps is half as
-// long as with one, which is what a batch of few long sequences waits for.
+// sequence for `pack` heads of a group, 32 rows in all, which each of its
+// waves holds: a wave takes every fourth 16 keys and uses each loaded value
+// in two products, and the waves are joined through LDS. What bounds it is the
+// matrix cores and, beside them, the cache's path into the registers: with 16
+// rows a wave, and so twice the loads, two prompts of 2000 and 2100 (24 heads
+// of 128) took 586 us against 462 (112 TFLOP/s), three of 500 to 2000 (16
+// heads of 64) 139 against 124; eight of 40 tokens, whose time is the start
+// and the join, 11.7 against 12.9. The loop over keys that all rows see is
+// apart from the one with masks: together the first takes 627 us.
 template <int D>
-__global__ __launch_bounds__(64 * kPrefillWaves, 2) void attn_prefill_kernel(AttnArgs a, PrefillPlan p, Parts parts) {
+__global__ __launch_bounds__(64 * kPrefillWaves, D == 64 ? 3 : 2) void attn_prefill_kernel(AttnArgs a, PrefillPlan p,
+                                                                                      Parts parts) {
   using R = Rows<float, D>;
-  constexpr int NO = R::NB * 4;
-  __shared__ f32x4 so[2][NO][64];
-  __shared__ float sml[2][2][64];
+  constexpr int NO = R::NB * 4, kTurn = 16 * kPrefillWaves;
+  __shared__ float2 so[2][2][kPrefillWaves][NO][64];      // [set of rows][half][wave]
+  __shared__ float sml[2][kPrefillWaves][2][64];
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-  const int wave = uniform(threadIdx.x >> 6), sub = wave & 1, turn = wave >> 1;
+  const int wave = uniform(threadIdx.x >> 6);
   const int units = a.Hq / p.pack;
   const int unit = blockIdx.x % units;
   TileAt at;
@@ -407,63 +367,120 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void attn_prefill_kernel(Att
     count = parts_for(a, p, at.total, chunk);
     if (static_cast<int>(blockIdx.y) >= count) return;
   }
-  const int nq = at.nq, q0 = at.q0, len = at.len;
-  const int h = unit * p.pack + sub % p.pack;
-  const int pos0 = at.tile * p.tile_pos + 16 * (sub / p.pack);
-  const int pos = pos0 + n;
-  const int row = q0 + (pos < nq ? pos : nq - 1);
+  const int nq = at.nq, len = at.len;
   const int64_t first = static_cast<int64_t>(len) - nq + 1;        // keys that position 0 sees
-  int mine = static_cast<int>(first + pos < 0 ? 0 : first + pos);
-  if (mine > len) mine = len;
-  const int top = pos0 + 15 < nq ? pos0 + 15 : nq - 1;
-  int end = pos0 < nq && first + top > 0 ? static_cast<int>(first + top) : 0;
   const int from = static_cast<int>(blockIdx.y) * chunk;
-  if (count > 1 && end > from + chunk) end = from + chunk;
-  R r;
-  r.init();
-  r.load_q(static_cast<const float*>(a.Q) + row * a.ldq + static_cast<int64_t>(h) * D, g);
-  if (from + 16 * turn < end) {
-    Pages<float, D> pg{static_cast<const float*>(a.Kc), static_cast<const float*>(a.Vc),
-                   a.page_table + static_cast<int64_t>(at.b) * a.max_pages, (len - 1) >> a.page_shift,
-                   a.page_shift, a.n_pages, a.Hkv, h / (a.Hq / a.Hkv)};
-    // the next keys are on their way while these are worked on, and the page
-    // of those after them
-    typename R::Keys x[2];
-    int key = from + 16 * turn;
-    int entry = pg.entry(key + 32);
-    r.fetch(pg, pg.at(key), n, g, x[0]);
-    while (true) {
-      r.fetch(pg, pg.at(key + 32, entry), n, g, x[1]);
-      entry = pg.entry(key + 64);
-      r.template step<true>(x[0], key, len, mine, a.scale_log2, n, g);
-      if ((key += 32) >= end) break;
-      r.fetch(pg, pg.at(key + 32, entry), n, g, x[0]);
-      entry = pg.entry(key + 64);
-      r.template step<true>(x[1], key, len, mine, a.scale_log2, n, g);
-      if ((key += 32) >= end) break;
-    }
-  }
-  float l = sum_groups(r.l);
-  if (turn) {
+  R r[2];
+  int pos[2], mine[2], end = 0;
 #pragma unroll
-    for (int c = 0; c < NO; ++c) so[sub][c][lane] = r.o[c];
-    sml[sub][0][lane] = r.m;
-    sml[sub][1][lane] = l;
+  for (int s = 0; s < 2; ++s) {
+    const int h = unit * p.pack + s % p.pack, pos0 = at.tile * p.tile_pos + 16 * (s / p.pack);
+    pos[s] = pos0 + n;
+    mine[s] = static_cast<int>(first + pos[s] < 0 ? 0 : first + pos[s]);
+    if (mine[s] > len) mine[s] = len;
+    const int top = pos0 + 15 < nq ? pos0 + 15 : nq - 1;
+    if (pos0 < nq && first + top > end) end = static_cast<int>(first + top);
+    const int row = at.q0 + (pos[s] < nq ? pos[s] : nq - 1);
+    r[s].init();
+    r[s].load_q(static_cast<const float*>(a.Q) + row * a.ldq + static_cast<int64_t>(h) * D, g);
+  }
+  if (count > 1 && end > from + chunk) end = from + chunk;
+  // keys that every row sees
+  const int64_t low = first + static_cast<int64_t>(at.tile) * p.tile_pos;
+  const int all = static_cast<int>(low < 0 ? 0 : low < len ? low : len);
+  int key = from + 16 * wave;
+  if (key < end) {
+    Pages<float, D> pg{static_cast<const float*>(a.Kc), static_cast<const float*>(a.Vc),
+                       a.page_table + static_cast<int64_t>(at.b) * a.max_pages, (len - 1) >> a.page_shift,
+                       a.page_shift, a.n_pages, a.Hkv, unit * p.pack / (a.Hq / a.Hkv)};
+    f32x4 k[R::C], v[4][R::NB];
+    const int64_t at0 = pg.at(key);
+    R::fetch_k(pg, at0, n, g, k);
+    R::fetch_v(pg, at0, n, g, v);
+    int entry = pg.entry(key + kTurn);
+    // The next keys come while these ones' values are worked on, those values
+    // while the next scores are; the page after them is looked up.
+    auto step = [&](auto masked) __attribute__((always_inline)) {
+      constexpr bool M = decltype(masked)::value;
+      float z[2][4], w[2][4];
+      r[0].scores(k, a.scale_log2, z[0]);
+      r[1].scores(k, a.scale_log2, z[1]);
+      __builtin_amdgcn_sched_barrier(0);
+      const int64_t next = pg.at(key + kTurn, entry);
+      R::fetch_k(pg, next, n, g, k);
+      entry = pg.entry(key + 2 * kTurn);
+      if constexpr (M) {
+        R::mask(z[0], key, mine[0], g);
+        R::mask(z[1], key, mine[1], g);
+      }
+      r[0].weigh(z[0], w[0]);
+      r[1].weigh(z[1], w[1]);
+      if (M && key + 16 > len) R::clear(v, key, len, g);
+      if (M && __any(!R::finite(v))) {
+        r[0].product_of_own(v, w[0], key, mine[0], n, g);
+        r[1].product_of_own(v, w[1], key, mine[1], n, g);
+      } else {
+        R::product(v, w[0], r[0].o);
+        R::product(v, w[1], r[1].o);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      key += kTurn;
+      R::fetch_v(pg, next, n, g, v);
+    };
+    while (key + 16 <= all && key < end) step(std::false_type{});
+    while (key < end) step(std::true_type{});
+  }
+  // Each wave joins one half of the values of one set of rows, of the waves
+  // that had keys.
+  const int waves = end - from >= kTurn ? kPrefillWaves : (end - from + 15) / 16;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    if (wave >= waves) break;
+    const float l = sum_groups(r[s].l);
+#pragma unroll
+    for (int c = 0; c < NO; ++c) {
+      so[s][0][wave][c][lane] = float2{r[s].o[c][0], r[s].o[c][1]};
+      so[s][1][wave][c][lane] = float2{r[s].o[c][2], r[s].o[c][3]};
+    }
+    sml[s][wave][0][lane] = r[s].m;
+    sml[s][wave][1][lane] = l;
   }
   __syncthreads();
-  if (turn || pos >= nq) return;
-  const float m1 = sml[sub][0][lane], m = fmaxf(r.m, m1);
-  const float f0 = exp2_(r.m - ref(m)), f1 = exp2_(m1 - ref(m));
-  l = f0 * l + f1 * sml[sub][1][lane];
+  const int s = wave & 1, half = wave >> 1;
+  const int p0 = s ? pos[1] : pos[0], m0 = s ? mine[1] : mine[0];
+  if (p0 >= nq) return;
+  float m = kNone, l = 0.0f;
 #pragma unroll
-  for (int c = 0; c < NO; ++c) r.o[c] = r.o[c] * f0 + so[sub][c][lane] * f1;
+  for (int w = 0; w < kPrefillWaves; ++w)
+    if (w < waves) m = fmaxf(m, sml[s][w][0][lane]);
+  float2 o[NO] = {};
+#pragma unroll
+  for (int w = 0; w < kPrefillWaves; ++w) {
+    if (w >= waves) break;
+    const float f = exp2_(sml[s][w][0][lane] - ref(m));
+    l = __builtin_fmaf(f, sml[s][w][1][lane], l);
+#pragma unroll
+    for (int c = 0; c < NO; ++c) {
+      const float2 x = so[s][half][w][c][lane];
+      o[c].x = __builtin_fmaf(f, x.x, o[c].x);
+      o[c].y = __builtin_fmaf(f, x.y, o[c].y);
+    }
+  }
+  const int row = at.q0 + p0, h = unit * p.pack + s % p.pack;
+  float* out = static_cast<float*>(a.O) + row * a.ldo + static_cast<int64_t>(h) * D;
+  float inv = inverse(l);
   if (count > 1) {
-    if (from >= mine && from > 0) return;            // the join takes only parts that begin before `mine`
+    if (from >= m0 && from > 0) return;              // the join takes only parts that begin before `mine`
     const int64_t slot = (static_cast<int64_t>(row) * a.Hq + h) * parts.splits + blockIdx.y;
-    r.store_f32(parts.o + slot * D, g);
-    if (g == 0) parts.ml[slot] = float2{m, l};
-  } else {
-    r.store(static_cast<float*>(a.O) + row * a.ldo + static_cast<int64_t>(h) * D, g, inverse(l));
+    out = parts.o + slot * D;
+    inv = 1.0f;
+    if (half == 0 && g == 0) parts.ml[slot] = float2{m, l};
+  }
+#pragma unroll
+  for (int b = 0; b < R::NB; ++b) {
+    float* to = out + 64 * b + 4 * (4 * g + 2 * half);
+    *reinterpret_cast<f32x4*>(to) = f32x4{o[4 * b].x, o[4 * b + 1].x, o[4 * b + 2].x, o[4 * b + 3].x} * inv;
+    *reinterpret_cast<f32x4*>(to + 4) = f32x4{o[4 * b].y, o[4 * b + 1].y, o[4 * b + 2].y, o[4 * b + 3].y} * inv;
   }
 }
 
@@ -523,7 +540,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, kDecodeWaves == 4 && sizeof(T) =
     Pages<T, D> pg{static_cast<const T*>(a.Kc), static_cast<const T*>(a.Vc), table, (len - 1) >> a.page_shift,
                    a.page_shift, a.n_pages, a.Hkv, kvh};
     for (int key = from + wave * r.kStep; key < to; key += kDecodeWaves * r.kStep)
-      r.template step<false>(pg, key, to, to, a.scale_log2, n, g);
+      r.step(pg, key, to, a.scale_log2, n, g);
   }
   const float lw = sum_groups(r.l);
   r.store_f32(&so[wave][n][0], g);
@@ -776,8 +793,9 @@ PrefillPlan plan_prefill(int bf16, int B, int T, int Hq, int Hkv, int D, int max
   p.tiled = bf16;
   p.pack = p.tiled && G % 8 == 0 ? 8 : p.tiled && G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1;
   p.tile_pos = (p.tiled ? kTileRows : kPrefillRows) / p.pack;
-  // Workgroups that run at once: one of the tile kernel's a CU, three of the
-  // other. Few new tokens over many keys leave CUs idle unless the keys are
+  // Workgroups that run at once: one of the tile kernel's a CU, two or three of
+  // the other (with 512 parts 33 and 64 tokens over 4000 keys take 42 us, with
+  // 768 36). Few new tokens over many keys leave CUs idle unless the keys are
   // cut: 16 tokens of 32 heads over 4096 keys take 21 us with parts and 80
   // without, 512 over 8192 88 against 164.
   p.target = p.tiled ? 256 : 768;
