@@ -24,6 +24,7 @@ try:
 except ImportError:  # pragma: no cover - library use without PyTorch
     torch = None
 
+_BF16, _F32, _I32 = (getattr(torch, name, None) for name in ("bfloat16", "float32", "int32"))
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
 
@@ -32,27 +33,39 @@ _SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
 class KvCache:
     """Paged keys and values: two contiguous device tensors, each (pages, kv
     heads, page size, head dim), of one dtype. Slot s is token s % page size
-    of page s // page size."""
+    of page s // page size. They may be replaced, by larger ones say: every
+    call takes the tensors as they are then (a captured graph keeps those of
+    its capture)."""
 
     k: "object"
     v: "object"
 
     def __post_init__(self):
+        self._now()
+
+    def _now(self):
+        """What a call needs of the tensors, checked and read afresh: (k
+        address, v address, pages, kv heads, page size, head dim, torch dtype,
+        library dtype, device index). Kept from an earlier call, an address
+        could be of memory that is another tensor's by now."""
         k, v = self.k, self.v
-        shape = k.shape
-        if len(shape) != 4 or shape != v.shape or k.dtype is not v.dtype or k.device != v.device:
+        shape, dtype, dev = k.shape, k.dtype, k.get_device()
+        if len(shape) != 4 or v.shape != shape or v.dtype is not dtype or v.get_device() != dev:
             raise ValueError("k and v must be (pages, kv heads, page size, head dim) tensors alike")
-        if not k.is_cuda or not k.is_contiguous() or not v.is_contiguous():
+        if dev < 0 or not k.is_contiguous() or not v.is_contiguous():
             raise ValueError("device tensors must be contiguous CUDA tensors")
-        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = shape
-        self.torch_dtype = k.dtype
-        if k.dtype is torch.bfloat16:
-            self.dtype = SERQ_BF16
-        elif k.dtype is torch.float32:
-            self.dtype = SERQ_F32
-        else:
+        if dtype is not _BF16 and dtype is not _F32:
             raise ValueError("the cache must be float32 or bfloat16")
-        self.pointers = k.data_ptr(), v.data_ptr()
+        pages, heads, page, D = shape
+        return k.data_ptr(), v.data_ptr(), pages, heads, page, D, dtype, SERQ_BF16 if dtype is _BF16 else SERQ_F32, dev
+
+    n_pages = property(lambda self: self._now()[2])
+    n_kv_heads = property(lambda self: self._now()[3])
+    page_size = property(lambda self: self._now()[4])
+    head_dim = property(lambda self: self._now()[5])
+    torch_dtype = property(lambda self: self._now()[6])
+    dtype = property(lambda self: self._now()[7])
+    pointers = property(lambda self: self._now()[:2])
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, *, dtype=None, device="cuda"):
@@ -77,31 +90,27 @@ def rope_table(rot_dim: int, max_pos: int, *, theta: float = 10000.0, scaling: s
     return t
 
 
-# The current stream's handle. torch.cuda.current_stream() builds a Stream
-# object around it, which takes longer than the smallest of these kernels.
-_raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
-
-
-def _stream(t):
-    if _raw_stream is not None:
-        return _raw_stream(t.get_device())
-    return torch.cuda.current_stream(t.device).cuda_stream
+# The handle of a device's current stream. torch.cuda.current_stream() builds
+# a Stream object around it, which takes longer than the smallest of these
+# kernels.
+_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 # The checks below run on every call of a decoding step, where a handful of
 # microseconds is what the kernels take: each attribute is read once.
 
 def _ints(t, shape, what):
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not _I32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous CUDA int32 tensor of shape {shape}")
     return t.data_ptr()
 
 
-def _rows(t, shape, cache, what):
+def _rows(t, shape, D, dtype, what):
     """Row stride of a (rows, heads, head dim) tensor whose rows are whole."""
     n, h, d = shape
-    if d != cache.head_dim or t.dtype is not cache.torch_dtype or not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA (rows, heads, {cache.head_dim}) tensor of the cache's dtype")
+    if d != D or t.dtype is not dtype or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA (rows, heads, {D}) tensor of the cache's dtype")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != d and h > 1):
         raise ValueError(f"{what}: heads must lie one after another in a row")
@@ -115,13 +124,11 @@ def _shape3(t, what):
     return shape
 
 
-def _out(out, q, shape, cache):
+def _out(out, shape, dtype):
     """(output, its row stride)"""
-    if out is None:
-        return q.new_empty(shape), shape[1] * shape[2]
     if out.shape != shape:
         raise ValueError(f"out must be of shape {tuple(shape)}")
-    return out, _rows(out, shape, cache, "out")
+    return out, _rows(out, shape, shape[2], dtype, "out")
 
 
 def _space(workspace, need, q):
@@ -139,6 +146,12 @@ def _space(workspace, need, q):
     return workspace, workspace.data_ptr(), size
 
 
+def _norm(w, D):
+    if w.dtype is not _F32 or w.shape != (D,) or not w.is_cuda or not w.is_contiguous():
+        raise ValueError(f"norms must be contiguous CUDA float32 tensors of {D}")
+    return w.data_ptr()
+
+
 def rope_append(qkv, n_heads: int, cache: KvCache, pos, slot, table, *, layout: str = "half", q_norm=None, k_norm=None,
                 eps: float = 1e-6, out=None):
     """Queries of the q/k/v linear's output, with keys and values stored in
@@ -146,44 +159,44 @@ def rope_append(qkv, n_heads: int, cache: KvCache, pos, slot, table, *, layout: 
     (n_heads + 2 kv heads) * head dim (unit column stride), ``pos`` and
     ``slot`` M int32, ``table`` (max_pos, rot_dim) float32 on the device or
     None for no rotation. Returns M x n_heads x head dim."""
+    kc, vc, n_pages, Hkv, page, D, tdt, dt, dev = cache._now()
     shape = qkv.shape
-    if len(shape) != 2 or not qkv.is_cuda or qkv.dtype is not cache.torch_dtype:
+    if len(shape) != 2 or not qkv.is_cuda or qkv.dtype is not tdt:
         raise ValueError("qkv must be a two-dimensional CUDA tensor of the cache's dtype")
     M, width = shape
-    D, Hkv = cache.head_dim, cache.n_kv_heads
     ld, unit = qkv.stride()
     if width != (n_heads + 2 * Hkv) * D or (unit != 1 and M > 0):
         raise ValueError(f"qkv must have {(n_heads + 2 * Hkv) * D} columns of unit stride")
     if M <= 1:
         ld = width
-    if layout not in _LAYOUTS:
+    order = _LAYOUTS.get(layout)
+    if order is None:
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}")
     rot = max_pos = 0
     tp = pp = None
     if table is not None:
-        if table.dtype is not torch.float32 or table.dim() != 2 or not table.is_cuda or not table.is_contiguous():
+        size = table.shape
+        if len(size) != 2 or table.dtype is not _F32 or not table.is_cuda or not table.is_contiguous():
             raise ValueError("table must be a contiguous CUDA (max_pos, rot_dim) float32 tensor")
-        max_pos, rot = table.shape
+        max_pos, rot = size
         if rot:
             tp, pp = table.data_ptr(), _ints(pos, (M,), "pos")
-    wp = [None, None]
-    for i, w in enumerate((q_norm, k_norm)):
-        if w is not None:
-            if w.dtype is not torch.float32 or w.shape != (D,) or not w.is_cuda or not w.is_contiguous():
-                raise ValueError(f"norms must be contiguous CUDA float32 tensors of {D}")
-            wp[i] = w.data_ptr()
+    qw = None if q_norm is None else _norm(q_norm, D)
+    kw = None if k_norm is None else _norm(k_norm, D)
     sp = _ints(slot, (M,), "slot")
-    q, ldq = _out(out, qkv, (M, n_heads, D), cache)
-    kc, vc = cache.pointers
-    check("serq_rope_append", lib.serq_rope_append(
-        qkv.data_ptr(), cache.dtype, ld, M, n_heads, Hkv, D, wp[0], wp[1], eps, tp, rot, max_pos, _LAYOUTS[layout], pp,
-        sp, q.data_ptr(), ldq, kc, vc, cache.n_pages, cache.page_size, _stream(qkv)))
+    q, ldq = (qkv.new_empty((M, n_heads, D)), n_heads * D) if out is None else _out(out, (M, n_heads, D), tdt)
+    status = lib.serq_rope_append(
+        qkv.data_ptr(), dt, ld, M, n_heads, Hkv, D, qw, kw, eps, tp, rot, max_pos, order, pp,
+        sp, q.data_ptr(), ldq, kc, vc, n_pages, page, _stream(dev))
+    if status:
+        check("serq_rope_append", status)
     return q
 
 
 def attn_prefill_workspace(cache: KvCache, B: int, T: int, n_heads: int, max_len: int) -> int:
     """Bytes of workspace attn_prefill needs (serq_attn_prefill_workspace)."""
-    return lib.serq_attn_prefill_workspace(cache.dtype, B, T, n_heads, cache.n_kv_heads, cache.head_dim, max_len)
+    _, _, _, Hkv, _, D, _, dt, _ = cache._now()
+    return lib.serq_attn_prefill_workspace(dt, B, T, n_heads, Hkv, D, max_len)
 
 
 def attn_prefill(q, cu_q, cache: KvCache, page_table, kv_len, *, max_len: int, scale: float | None = None, out=None,
@@ -194,9 +207,10 @@ def attn_prefill(q, cu_q, cache: KvCache, page_table, kv_len, *, max_len: int, s
     device; ``max_len`` bounds kv_len; ``scale`` is head_dim ** -0.5 unless
     given. A workspace is taken from torch's allocator unless given. Returns
     T x heads x head dim."""
+    kc, vc, n_pages, Hkv, page, D, tdt, dt, dev = cache._now()
     shape = _shape3(q, "q")
-    ldq = _rows(q, shape, cache, "q")
-    T, Hq, D = shape
+    ldq = _rows(q, shape, D, tdt, "q")
+    T, Hq, _ = shape
     if page_table.dim() != 2:
         raise ValueError("page_table must be sequences x pages")
     pages = page_table.shape
@@ -204,20 +218,20 @@ def attn_prefill(q, cu_q, cache: KvCache, page_table, kv_len, *, max_len: int, s
     tp = _ints(page_table, pages, "page_table")
     cp = _ints(cu_q, (B + 1,), "cu_q")
     kp = _ints(kv_len, (B,), "kv_len")
-    o, ldo = _out(out, q, shape, cache)
-    Hkv = cache.n_kv_heads
-    kc, vc = cache.pointers
-    hold, wp, size = _space(workspace, lib.serq_attn_prefill_workspace(cache.dtype, B, T, Hq, Hkv, D, max_len), q)
-    check("serq_attn_prefill", lib.serq_attn_prefill(
-        q.data_ptr(), cache.dtype, ldq, cp, B, T, Hq, Hkv, D, kc, vc, cache.n_pages, cache.page_size, tp, pages[1], kp,
-        max_len, D ** -0.5 if scale is None else scale, o.data_ptr(), ldo, wp, size, _stream(q)))
+    o, ldo = (q.new_empty(shape), Hq * D) if out is None else _out(out, shape, tdt)
+    hold, wp, size = _space(workspace, lib.serq_attn_prefill_workspace(dt, B, T, Hq, Hkv, D, max_len), q)
+    status = lib.serq_attn_prefill(
+        q.data_ptr(), dt, ldq, cp, B, T, Hq, Hkv, D, kc, vc, n_pages, page, tp, pages[1], kp,
+        max_len, D ** -0.5 if scale is None else scale, o.data_ptr(), ldo, wp, size, _stream(dev))
+    if status:
+        check("serq_attn_prefill", status)
     return o
 
 
 def attn_decode_workspace(cache: KvCache, B: int, n_heads: int, prefix_len: int, max_len: int) -> int:
     """Bytes of workspace attn_decode needs (serq_attn_decode_workspace)."""
-    return lib.serq_attn_decode_workspace(cache.dtype, B, n_heads, cache.n_kv_heads, cache.head_dim, prefix_len,
-                                          max_len)
+    _, _, _, Hkv, _, D, _, dt, _ = cache._now()
+    return lib.serq_attn_decode_workspace(dt, B, n_heads, Hkv, D, prefix_len, max_len)
 
 
 def attn_decode(q, cache: KvCache, page_table, kv_len, *, max_len: int, prefix=None, prefix_len: int = 0,
@@ -227,9 +241,10 @@ def attn_decode(q, cache: KvCache, page_table, kv_len, *, max_len: int, prefix=N
     and ``kv_len`` B int32 give each sequence's own tokens, ``prefix`` (int32
     page ids) and ``prefix_len`` the tokens that all of them share before
     those. Returns B x heads x head dim."""
+    kc, vc, n_pages, Hkv, page, D, tdt, dt, dev = cache._now()
     shape = _shape3(q, "q")
-    ldq = _rows(q, shape, cache, "q")
-    B, Hq, D = shape
+    ldq = _rows(q, shape, D, tdt, "q")
+    B, Hq, _ = shape
     pages = page_table.shape
     if len(pages) != 2 or pages[0] != B:
         raise ValueError(f"page_table must be {B} x pages")
@@ -237,15 +252,15 @@ def attn_decode(q, cache: KvCache, page_table, kv_len, *, max_len: int, prefix=N
     kp = _ints(kv_len, (B,), "kv_len")
     pp = None
     if prefix_len > 0:
-        need = -(-prefix_len // cache.page_size)
+        need = -(-prefix_len // page)
         if prefix is None or prefix.numel() < need:
             raise ValueError(f"prefix must hold {need} page ids")
         pp = _ints(prefix, (prefix.numel(),), "prefix")
-    o, ldo = _out(out, q, shape, cache)
-    Hkv = cache.n_kv_heads
-    kc, vc = cache.pointers
-    hold, wp, size = _space(workspace, lib.serq_attn_decode_workspace(cache.dtype, B, Hq, Hkv, D, prefix_len, max_len), q)
-    check("serq_attn_decode", lib.serq_attn_decode(
-        q.data_ptr(), cache.dtype, ldq, B, Hq, Hkv, D, kc, vc, cache.n_pages, cache.page_size, pp, prefix_len, tp,
-        pages[1], kp, max_len, D ** -0.5 if scale is None else scale, o.data_ptr(), ldo, wp, size, _stream(q)))
+    o, ldo = (q.new_empty(shape), Hq * D) if out is None else _out(out, shape, tdt)
+    hold, wp, size = _space(workspace, lib.serq_attn_decode_workspace(dt, B, Hq, Hkv, D, prefix_len, max_len), q)
+    status = lib.serq_attn_decode(
+        q.data_ptr(), dt, ldq, B, Hq, Hkv, D, kc, vc, n_pages, page, pp, prefix_len, tp,
+        pages[1], kp, max_len, D ** -0.5 if scale is None else scale, o.data_ptr(), ldo, wp, size, _stream(dev))
+    if status:
+        check("serq_attn_decode", status)
     return o
