@@ -52,15 +52,16 @@ def ints(*shape, device=0):
 
 
 class Recorder:
-    """Stands for the library: keeps the arguments of the last call."""
+    """Stands for the library: keeps the arguments of the last call and the
+    device it was made on."""
 
-    name = None
+    name, current = None, 0
 
     def __getattr__(self, name):
         def call(*args):
             if name.endswith("workspace"):
                 return 64
-            self.name, self.args = name, args
+            self.name, self.args, self.on = name, args, self.current
             return 0
         return call
 
@@ -69,7 +70,20 @@ class Recorder:
 def lib(monkeypatch):
     rec = Recorder()
     monkeypatch.setattr(A, "lib", rec)
-    monkeypatch.setattr(A, "_stream", lambda device: 7)
+    monkeypatch.setattr(A, "_stream", lambda device: 70 + device)
+    monkeypatch.setattr(A, "_current", lambda: rec.current, raising=False)
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, rec.current = rec.current, self.index
+
+        def __exit__(self, *exc):
+            rec.current = self.before
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
     return rec
 
 
@@ -77,22 +91,27 @@ def cache(pages=4, Hkv=2, page=16, D=64, dtype=torch.bfloat16, device=0):
     return S.KvCache(Fake(pages, Hkv, page, D, dtype=dtype, device=device), Fake(pages, Hkv, page, D, dtype=dtype, device=device))
 
 
-def call_append(c, M=3, Hq=4, **kw):
-    w = (Hq + 2 * 2) * 64
-    dev = kw.pop("device", 0)
-    dtype = kw.pop("dtype", torch.bfloat16)
-    return S.rope_append(kw.pop("qkv", Fake(M, w, dtype=dtype, device=dev)), Hq, c, kw.pop("pos", ints(M)), kw.pop("slot", ints(M)),
-                         kw.pop("table", Fake(9, 64, dtype=torch.float32)), **kw)
+def floats(*shape, device=0):
+    return Fake(*shape, dtype=torch.float32, device=device)
 
 
-def call_prefill(c, T=5, B=2, **kw):
-    return S.attn_prefill(kw.pop("q", Fake(T, 4, 64, dtype=kw.pop("dtype", torch.bfloat16))), kw.pop("cu_q", ints(B + 1)), c,
-                          kw.pop("page_table", ints(B, 3)), kw.pop("kv_len", ints(B)), max_len=40, **kw)
+def call_append(c, dtype=torch.bfloat16, d=0, **kw):
+    a = dict(pos=ints(3, device=d), slot=ints(3, device=d), table=floats(9, 64, device=d),
+             qkv=Fake(3, 8 * 64, dtype=dtype, device=d), cache=c, n_heads=4, q_norm=floats(64, device=d),
+             k_norm=floats(64, device=d))
+    return S.rope_append(**{**a, **kw})
 
 
-def call_decode(c, B=2, **kw):
-    return S.attn_decode(kw.pop("q", Fake(B, 4, 64, dtype=kw.pop("dtype", torch.bfloat16))), c, kw.pop("page_table", ints(B, 3)),
-                         kw.pop("kv_len", ints(B)), max_len=40, **kw)
+def call_prefill(c, dtype=torch.bfloat16, d=0, **kw):
+    a = dict(q=Fake(5, 4, 64, dtype=dtype, device=d), cu_q=ints(3, device=d), cache=c, page_table=ints(2, 3, device=d),
+             kv_len=ints(2, device=d), max_len=40)
+    return S.attn_prefill(**{**a, **kw})
+
+
+def call_decode(c, dtype=torch.bfloat16, d=0, **kw):
+    a = dict(q=Fake(2, 4, 64, dtype=dtype, device=d), cache=c, page_table=ints(2, 3, device=d), kv_len=ints(2, device=d),
+             max_len=40, prefix=ints(1, device=d), prefix_len=16)
+    return S.attn_decode(**{**a, **kw})
 
 
 CALLS = [call_append, call_prefill, call_decode]
@@ -133,3 +152,32 @@ def test_a_cache_replaced_in_part_is_refused(lib, call):
         call(c)
     call(c, dtype=torch.float32)
     assert handed(lib)[:2] == (c.k.address, c.v.address)
+
+
+ROWS = dict(qkv=Fake(3, 8 * 64, device=1), pos=ints(3, device=1), slot=ints(3, device=1), table=floats(9, 64, device=1),
+            q_norm=floats(64, device=1), k_norm=floats(64, device=1), out=Fake(3, 4, 64, device=1))
+PROMPT = dict(q=Fake(5, 4, 64, device=1), cu_q=ints(3, device=1), page_table=ints(2, 3, device=1),
+              kv_len=ints(2, device=1), out=Fake(5, 4, 64, device=1), workspace=Fake(64, dtype=torch.uint8, device=1))
+TOKEN = dict(q=Fake(2, 4, 64, device=1), page_table=ints(2, 3, device=1), kv_len=ints(2, device=1),
+             prefix=ints(1, device=1), out=Fake(2, 4, 64, device=1), workspace=Fake(64, dtype=torch.uint8, device=1))
+STRAY = [(c, k, v) for c, kw in zip(CALLS, (ROWS, PROMPT, TOKEN)) for k, v in kw.items()]
+
+
+@pytest.mark.parametrize("call,name,tensor", STRAY, ids=[f"{c.__name__}-{k}" for c, k, _ in STRAY])
+def test_a_tensor_on_another_device_is_refused(lib, call, name, tensor):
+    with pytest.raises(ValueError):
+        call(cache(), **{name: tensor})
+    assert lib.name is None
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("current", [0, 1, 2])
+def test_kernels_are_launched_on_the_cache_s_device(lib, call, current):
+    lib.current = current
+    call(cache(device=1), d=1)
+    assert lib.on == 1 and lib.args[-1] == 71 and lib.current == current
+
+
+def test_a_cache_on_two_devices_is_refused():
+    with pytest.raises(ValueError):
+        S.KvCache(Fake(4, 2, 16, 64), Fake(4, 2, 16, 64, device=1))

@@ -95,22 +95,26 @@ def rope_table(rot_dim: int, max_pos: int, *, theta: float = 10000.0, scaling: s
 # kernels.
 _stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
+# The device that kernels are launched on. A call makes the cache's device the
+# current one where it is not: a stream's handle alone does not say it (the
+# default stream's is 0 on every device).
+_current = getattr(getattr(torch, "_C", None), "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
 
 
 # The checks below run on every call of a decoding step, where a handful of
 # microseconds is what the kernels take: each attribute is read once.
 
-def _ints(t, shape, what):
-    if t.dtype is not _I32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous CUDA int32 tensor of shape {shape}")
+def _ints(t, shape, dev, what):
+    if t.dtype is not _I32 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous CUDA int32 tensor of shape {tuple(shape)} on the cache's device")
     return t.data_ptr()
 
 
-def _rows(t, shape, D, dtype, what):
+def _rows(t, shape, D, dtype, dev, what):
     """Row stride of a (rows, heads, head dim) tensor whose rows are whole."""
     n, h, d = shape
-    if d != D or t.dtype is not dtype or not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA (rows, heads, {D}) tensor of the cache's dtype")
+    if d != D or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{what} must be a CUDA (rows, heads, {D}) tensor of the cache's dtype and device")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != d and h > 1):
         raise ValueError(f"{what}: heads must lie one after another in a row")
@@ -124,14 +128,14 @@ def _shape3(t, what):
     return shape
 
 
-def _out(out, shape, dtype):
+def _out(out, shape, dtype, dev):
     """(output, its row stride)"""
     if out.shape != shape:
         raise ValueError(f"out must be of shape {tuple(shape)}")
-    return out, _rows(out, shape, shape[2], dtype, "out")
+    return out, _rows(out, shape, shape[2], dtype, dev, "out")
 
 
-def _space(workspace, need, q):
+def _space(workspace, need, q, dev):
     """(tensor that holds it, address, bytes)"""
     if need <= 0:
         if need < 0:
@@ -141,14 +145,14 @@ def _space(workspace, need, q):
         workspace = q.new_empty((need + 3) // 2)       # (of q's type: at least two bytes each)
         return workspace, workspace.data_ptr(), need
     size = workspace.numel() * workspace.element_size()
-    if not workspace.is_cuda or not workspace.is_contiguous() or size < need:
-        raise ValueError(f"workspace must be a contiguous CUDA tensor of {need} bytes or more")
+    if workspace.get_device() != dev or not workspace.is_contiguous() or size < need:
+        raise ValueError(f"workspace must be a contiguous CUDA tensor of {need} bytes or more on the cache's device")
     return workspace, workspace.data_ptr(), size
 
 
-def _norm(w, D):
-    if w.dtype is not _F32 or w.shape != (D,) or not w.is_cuda or not w.is_contiguous():
-        raise ValueError(f"norms must be contiguous CUDA float32 tensors of {D}")
+def _norm(w, D, dev):
+    if w.dtype is not _F32 or w.shape != (D,) or w.get_device() != dev or not w.is_contiguous():
+        raise ValueError(f"norms must be contiguous CUDA float32 tensors of {D} on the cache's device")
     return w.data_ptr()
 
 
@@ -160,9 +164,13 @@ def rope_append(qkv, n_heads: int, cache: KvCache, pos, slot, table, *, layout: 
     ``slot`` M int32, ``table`` (max_pos, rot_dim) float32 on the device or
     None for no rotation. Returns M x n_heads x head dim."""
     kc, vc, n_pages, Hkv, page, D, tdt, dt, dev = cache._now()
+    if dev != _current():
+        with torch.cuda.device(dev):
+            return rope_append(qkv, n_heads, cache, pos, slot, table, layout=layout, q_norm=q_norm, k_norm=k_norm,
+                               eps=eps, out=out)
     shape = qkv.shape
-    if len(shape) != 2 or not qkv.is_cuda or qkv.dtype is not tdt:
-        raise ValueError("qkv must be a two-dimensional CUDA tensor of the cache's dtype")
+    if len(shape) != 2 or qkv.get_device() != dev or qkv.dtype is not tdt:
+        raise ValueError("qkv must be a two-dimensional CUDA tensor of the cache's dtype and device")
     M, width = shape
     ld, unit = qkv.stride()
     if width != (n_heads + 2 * Hkv) * D or (unit != 1 and M > 0):
@@ -176,15 +184,15 @@ def rope_append(qkv, n_heads: int, cache: KvCache, pos, slot, table, *, layout: 
     tp = pp = None
     if table is not None:
         size = table.shape
-        if len(size) != 2 or table.dtype is not _F32 or not table.is_cuda or not table.is_contiguous():
-            raise ValueError("table must be a contiguous CUDA (max_pos, rot_dim) float32 tensor")
+        if len(size) != 2 or table.dtype is not _F32 or table.get_device() != dev or not table.is_contiguous():
+            raise ValueError("table must be a contiguous CUDA (max_pos, rot_dim) float32 tensor on the cache's device")
         max_pos, rot = size
         if rot:
-            tp, pp = table.data_ptr(), _ints(pos, (M,), "pos")
-    qw = None if q_norm is None else _norm(q_norm, D)
-    kw = None if k_norm is None else _norm(k_norm, D)
-    sp = _ints(slot, (M,), "slot")
-    q, ldq = (qkv.new_empty((M, n_heads, D)), n_heads * D) if out is None else _out(out, (M, n_heads, D), tdt)
+            tp, pp = table.data_ptr(), _ints(pos, (M,), dev, "pos")
+    qw = None if q_norm is None else _norm(q_norm, D, dev)
+    kw = None if k_norm is None else _norm(k_norm, D, dev)
+    sp = _ints(slot, (M,), dev, "slot")
+    q, ldq = (qkv.new_empty((M, n_heads, D)), n_heads * D) if out is None else _out(out, (M, n_heads, D), tdt, dev)
     status = lib.serq_rope_append(
         qkv.data_ptr(), dt, ld, M, n_heads, Hkv, D, qw, kw, eps, tp, rot, max_pos, order, pp,
         sp, q.data_ptr(), ldq, kc, vc, n_pages, page, _stream(dev))
@@ -208,18 +216,22 @@ def attn_prefill(q, cu_q, cache: KvCache, page_table, kv_len, *, max_len: int, s
     given. A workspace is taken from torch's allocator unless given. Returns
     T x heads x head dim."""
     kc, vc, n_pages, Hkv, page, D, tdt, dt, dev = cache._now()
+    if dev != _current():
+        with torch.cuda.device(dev):
+            return attn_prefill(q, cu_q, cache, page_table, kv_len, max_len=max_len, scale=scale, out=out,
+                                workspace=workspace)
     shape = _shape3(q, "q")
-    ldq = _rows(q, shape, D, tdt, "q")
+    ldq = _rows(q, shape, D, tdt, dev, "q")
     T, Hq, _ = shape
     if page_table.dim() != 2:
         raise ValueError("page_table must be sequences x pages")
     pages = page_table.shape
     B = pages[0]
-    tp = _ints(page_table, pages, "page_table")
-    cp = _ints(cu_q, (B + 1,), "cu_q")
-    kp = _ints(kv_len, (B,), "kv_len")
-    o, ldo = (q.new_empty(shape), Hq * D) if out is None else _out(out, shape, tdt)
-    hold, wp, size = _space(workspace, lib.serq_attn_prefill_workspace(dt, B, T, Hq, Hkv, D, max_len), q)
+    tp = _ints(page_table, pages, dev, "page_table")
+    cp = _ints(cu_q, (B + 1,), dev, "cu_q")
+    kp = _ints(kv_len, (B,), dev, "kv_len")
+    o, ldo = (q.new_empty(shape), Hq * D) if out is None else _out(out, shape, tdt, dev)
+    hold, wp, size = _space(workspace, lib.serq_attn_prefill_workspace(dt, B, T, Hq, Hkv, D, max_len), q, dev)
     status = lib.serq_attn_prefill(
         q.data_ptr(), dt, ldq, cp, B, T, Hq, Hkv, D, kc, vc, n_pages, page, tp, pages[1], kp,
         max_len, D ** -0.5 if scale is None else scale, o.data_ptr(), ldo, wp, size, _stream(dev))
@@ -242,22 +254,26 @@ def attn_decode(q, cache: KvCache, page_table, kv_len, *, max_len: int, prefix=N
     page ids) and ``prefix_len`` the tokens that all of them share before
     those. Returns B x heads x head dim."""
     kc, vc, n_pages, Hkv, page, D, tdt, dt, dev = cache._now()
+    if dev != _current():
+        with torch.cuda.device(dev):
+            return attn_decode(q, cache, page_table, kv_len, max_len=max_len, prefix=prefix, prefix_len=prefix_len,
+                               scale=scale, out=out, workspace=workspace)
     shape = _shape3(q, "q")
-    ldq = _rows(q, shape, D, tdt, "q")
+    ldq = _rows(q, shape, D, tdt, dev, "q")
     B, Hq, _ = shape
     pages = page_table.shape
     if len(pages) != 2 or pages[0] != B:
         raise ValueError(f"page_table must be {B} x pages")
-    tp = _ints(page_table, pages, "page_table")
-    kp = _ints(kv_len, (B,), "kv_len")
+    tp = _ints(page_table, pages, dev, "page_table")
+    kp = _ints(kv_len, (B,), dev, "kv_len")
     pp = None
     if prefix_len > 0:
         need = -(-prefix_len // page)
         if prefix is None or prefix.numel() < need:
             raise ValueError(f"prefix must hold {need} page ids")
-        pp = _ints(prefix, (prefix.numel(),), "prefix")
-    o, ldo = (q.new_empty(shape), Hq * D) if out is None else _out(out, shape, tdt)
-    hold, wp, size = _space(workspace, lib.serq_attn_decode_workspace(dt, B, Hq, Hkv, D, prefix_len, max_len), q)
+        pp = _ints(prefix, (prefix.numel(),), dev, "prefix")
+    o, ldo = (q.new_empty(shape), Hq * D) if out is None else _out(out, shape, tdt, dev)
+    hold, wp, size = _space(workspace, lib.serq_attn_decode_workspace(dt, B, Hq, Hkv, D, prefix_len, max_len), q, dev)
     status = lib.serq_attn_decode(
         q.data_ptr(), dt, ldq, B, Hq, Hkv, D, kc, vc, n_pages, page, pp, prefix_len, tp,
         pages[1], kp, max_len, D ** -0.5 if scale is None else scale, o.data_ptr(), ldo, wp, size, _stream(dev))
