@@ -181,3 +181,34 @@ def test_kernels_are_launched_on_the_cache_s_device(lib, call, current):
 def test_a_cache_on_two_devices_is_refused():
     with pytest.raises(ValueError):
         S.KvCache(Fake(4, 2, 16, 64), Fake(4, 2, 16, 64, device=1))
+
+
+def wants_gradient(t):
+    t.requires_grad = True
+    return t
+
+
+@pytest.mark.parametrize("call,name,tensor", [
+    (call_append, "qkv", lambda: Fake(3, 8 * 64)), (call_append, "q_norm", lambda: floats(64)),
+    (call_append, "k_norm", lambda: floats(64)), (call_prefill, "q", lambda: Fake(5, 4, 64)),
+    (call_decode, "q", lambda: Fake(2, 4, 64))])
+def test_a_gradient_is_not_lost_silently(lib, call, name, tensor):
+    t = wants_gradient(tensor())
+    with pytest.raises(ValueError, match="gradient"):
+        call(cache(), **{name: t})
+    assert lib.name is None
+    with torch.no_grad():
+        call(cache(), **{name: t})
+    assert t.address in lib.args
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_a_cache_s_gradient_is_not_lost_silently(lib, call, which):
+    c = cache()
+    wants_gradient(getattr(c, which))
+    with pytest.raises(ValueError, match="gradient"):
+        call(c)
+    with torch.inference_mode():
+        call(c)
+    assert lib.name is not None

@@ -7,6 +7,10 @@ current torch stream.
     q = rope_append(qkv, n_heads, cache, pos, slot, table)           # queries; keys and values stored
     o = attn_prefill(q, cu_q, cache, pages, kv_len, max_len=...)     # new tokens, packed
     o = attn_decode(q, cache, pages, kv_len, max_len=...)            # one token per sequence
+
+For inference: none of these calls has a backward pass. Where torch records
+gradients, a tensor that requires one is refused rather than its gradient
+lost; under torch.no_grad() it is taken.
 """
 
 from __future__ import annotations
@@ -27,6 +31,11 @@ except ImportError:  # pragma: no cover - library use without PyTorch
 _BF16, _F32, _I32 = (getattr(torch, name, None) for name in ("bfloat16", "float32", "int32"))
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
+
+
+def _no_gradient(what):
+    if torch.is_grad_enabled():
+        raise ValueError(f"{what} requires a gradient, and the attention calls have none: call them under torch.no_grad()")
 
 
 @dataclass
@@ -56,6 +65,8 @@ class KvCache:
             raise ValueError("device tensors must be contiguous CUDA tensors")
         if dtype is not _BF16 and dtype is not _F32:
             raise ValueError("the cache must be float32 or bfloat16")
+        if k.requires_grad or v.requires_grad:
+            _no_gradient("the cache")
         pages, heads, page, D = shape
         return k.data_ptr(), v.data_ptr(), pages, heads, page, D, dtype, SERQ_BF16 if dtype is _BF16 else SERQ_F32, dev
 
@@ -153,6 +164,8 @@ def _space(workspace, need, q, dev):
 def _norm(w, D, dev):
     if w.dtype is not _F32 or w.shape != (D,) or w.get_device() != dev or not w.is_contiguous():
         raise ValueError(f"norms must be contiguous CUDA float32 tensors of {D} on the cache's device")
+    if w.requires_grad:
+        _no_gradient("a norm")
     return w.data_ptr()
 
 
@@ -171,6 +184,8 @@ def rope_append(qkv, n_heads: int, cache: KvCache, pos, slot, table, *, layout: 
     shape = qkv.shape
     if len(shape) != 2 or qkv.get_device() != dev or qkv.dtype is not tdt:
         raise ValueError("qkv must be a two-dimensional CUDA tensor of the cache's dtype and device")
+    if qkv.requires_grad:
+        _no_gradient("qkv")
     M, width = shape
     ld, unit = qkv.stride()
     if width != (n_heads + 2 * Hkv) * D or (unit != 1 and M > 0):
@@ -220,6 +235,8 @@ def attn_prefill(q, cu_q, cache: KvCache, page_table, kv_len, *, max_len: int, s
         with torch.cuda.device(dev):
             return attn_prefill(q, cu_q, cache, page_table, kv_len, max_len=max_len, scale=scale, out=out,
                                 workspace=workspace)
+    if q.requires_grad:
+        _no_gradient("q")
     shape = _shape3(q, "q")
     ldq = _rows(q, shape, D, tdt, dev, "q")
     T, Hq, _ = shape
@@ -258,6 +275,8 @@ def attn_decode(q, cache: KvCache, page_table, kv_len, *, max_len: int, prefix=N
         with torch.cuda.device(dev):
             return attn_decode(q, cache, page_table, kv_len, max_len=max_len, prefix=prefix, prefix_len=prefix_len,
                                scale=scale, out=out, workspace=workspace)
+    if q.requires_grad:
+        _no_gradient("q")
     shape = _shape3(q, "q")
     ldq = _rows(q, shape, D, tdt, dev, "q")
     B, Hq, _ = shape
