@@ -35,7 +35,7 @@ _SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
 
 def _no_gradient(what):
     if torch.is_grad_enabled():
-        raise ValueError(f"{what} requires a gradient, and the attention calls have none: call them under torch.no_grad()")
+        raise ValueError(f"{what} requires a gradient, and the attention calls have none: use torch.no_grad()")
 
 
 @dataclass
