@@ -161,8 +161,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
   if (split && end > from + chunk) end = from + chunk;
 
   u32x4 q[C];              // Q as the second operand: lane (query n, half) holds values 16 c + 8 half .. + 7
-  // (not 0, so that a masked score stays -inf)
-  const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
+  // (Not 0, so that a masked score stays -inf: a scale of 0 becomes the smallest
+  // number there is, which makes less than 2^-20 of any product.)
+  const float scale = fmaxf(fabsf(a.scale_log2), 0x1p-149f);
 
   f32x16 o[DB];
 #pragma unroll
