@@ -45,3 +45,50 @@ def test_scores_of_any_size_under_a_scale_to_match(dtype, scale, size):
     R.check(got, *R.decode(q, k, v, table, lens, prefix, P, scale), f"prefix, scale {scale}")
     got = S.attn_decode(q.to(DEV), cache, table.to(DEV), ints(lens).to(DEV), max_len=40, scale=scale)
     R.check(got, *R.decode(q, k, v, table, lens, None, 0, scale), f"decode, scale {scale}")
+
+
+# ------------------------------------------------------------------ scores of -inf
+
+@TYPES
+@pytest.mark.parametrize("what", [float("inf"), -float("inf"), float("nan")])
+def test_rows_whose_scores_are_all_minus_infinity(dtype, what):
+    """They give zeros, whatever their values hold; other rows come out as
+    they do by themselves."""
+    Hq, Hkv, D, page = 8, 2, 128, 16
+    g = gen(32)
+    new, kv = [40, 33, 3], [40, 90, 2000]
+    k, v, table = filled(g, kv, Hkv, page, D, dtype)
+    q = rnd(g, sum(new), Hq, D, dtype=dtype)
+    q[40:73, :, 7] = 1.0                                   # the second sequence's scores are -inf throughout
+    dead = table[1, :6].long()
+    k[dead, :, :, 7] = -float("inf")
+    v[dead, :, 3, 9] = what
+
+    def prefill():
+        return S.attn_prefill(q.to(DEV), ints([0, 40, 73, 76]).to(DEV), S.KvCache(k.to(DEV), v.to(DEV)), table.to(DEV),
+                              ints(kv).to(DEV), max_len=2000).cpu()
+
+    def decode(max_len, prefix, prefix_len):
+        return S.attn_decode(torch.stack([q[0], q[40], q[73]]).to(DEV), S.KvCache(k.to(DEV), v.to(DEV)),
+                             table.to(DEV), ints([40, 90, 500]).to(DEV), max_len=max_len, prefix=prefix,
+                             prefix_len=prefix_len).cpu()
+
+    runs = [prefill, lambda: decode(500, None, 0), lambda: decode(2000, None, 0)]
+    got = [f() for f in runs]
+    v[dead, :, 3, 9] = 0.0
+    for a, f in zip(got, runs):
+        b = f()
+        at = slice(40, 73) if a.shape[0] == 76 else slice(1, 2)
+        assert a[at].count_nonzero() == 0 and torch.equal(a, b)
+
+    # a prefix of such scores, and nothing after it, by rows and (bf16) by tiles
+    B, P = 20, 40000                                       # 20 x 8 x 40000 = 6.4 million
+    for n in (90, P):
+        k, v, table = filled(g, [n], Hkv, page, D, dtype)
+        k[..., 7] = -float("inf")
+        v[..., 5, 9] = what
+        q = rnd(g, B, Hq, D, dtype=dtype)
+        q[..., 7] = 1.0
+        o = S.attn_decode(q.to(DEV), S.KvCache(k.to(DEV), v.to(DEV)), torch.zeros(B, 1, dtype=torch.int32, device=DEV),
+                          ints([0] * B).to(DEV), max_len=0, prefix=table[0].to(DEV), prefix_len=n)
+        assert o.count_nonzero() == 0

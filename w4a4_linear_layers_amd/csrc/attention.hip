@@ -479,8 +479,14 @@ __global__ __launch_bounds__(64 * kPrefillWaves, D == 64 ? 3 : 2) void attn_pref
 #pragma unroll
   for (int b = 0; b < R::NB; ++b) {
     float* to = out + 64 * b + 4 * (4 * g + 2 * half);
-    *reinterpret_cast<f32x4*>(to) = f32x4{o[4 * b].x, o[4 * b + 1].x, o[4 * b + 2].x, o[4 * b + 3].x} * inv;
-    *reinterpret_cast<f32x4*>(to + 4) = f32x4{o[4 * b].y, o[4 * b + 1].y, o[4 * b + 2].y, o[4 * b + 3].y} * inv;
+    f32x4 x, y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = normed(o[4 * b + i].x, inv);
+      y[i] = normed(o[4 * b + i].y, inv);
+    }
+    *reinterpret_cast<f32x4*>(to) = x;
+    *reinterpret_cast<f32x4*>(to + 4) = y;
   }
 }
 
@@ -578,7 +584,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, kDecodeWaves == 4 && sizeof(T) =
   const float inv = inverse(l);
   T* out = static_cast<T*>(a.O) + bq * a.ldo + static_cast<int64_t>(hq) * D + d;
 #pragma unroll
-  for (int i = 0; i < W; ++i) out[i] = static_cast<T>(o[i] * inv);
+  for (int i = 0; i < W; ++i) out[i] = static_cast<T>(normed(o[i], inv));
 }
 
 // --------------------------------------------------------------------- join
@@ -648,7 +654,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, PrefillPlan 
   const float inv = inverse(l);
   T* out = static_cast<T*>(a.O) + t * a.ldo + static_cast<int64_t>(h) * D + lane * W;
 #pragma unroll
-  for (int i = 0; i < W; ++i) out[i] = static_cast<T>(o[i] * inv);
+  for (int i = 0; i < W; ++i) out[i] = static_cast<T>(normed(o[i], inv));
 }
 
 // Few rows: a workgroup each, D / 8 lanes to a part, so that the whole row is
@@ -715,7 +721,7 @@ __global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs a, PrefillP
   float y = 0.0f;
 #pragma unroll
   for (int k = 0; k < GROUPS; ++k) y += so[k][tid];
-  static_cast<T*>(a.O)[t * a.ldo + static_cast<int64_t>(h) * D + tid] = static_cast<T>(y * inverse(l));
+  static_cast<T*>(a.O)[t * a.ldo + static_cast<int64_t>(h) * D + tid] = static_cast<T>(normed(y, inverse(l)));
 }
 
 // Which join: 32 sequences of 4096 keys, 256 rows: 26.9 us a call with a

@@ -28,8 +28,12 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // score but -inf has been seen (2^(-inf - 0) = 0).
 __device__ __forceinline__ float ref(float m) { return m == kNone ? 0.0f : m; }
 
-// 1 / l, or 0 for a row without keys; NaN stays.
+// 1 / l, or 0 for a row without weights (no keys, or scores of -inf alone);
+// NaN stays.
 __device__ __forceinline__ float inverse(float l) { return l > 0.0f || l != l ? 1.0f / l : 0.0f; }
+// A sum of weighted values by that: 0 for such a row, whose sum may hold NaN
+// (0 * inf).
+__device__ __forceinline__ float normed(float o, float inv) { return inv == 0.0f ? 0.0f : o * inv; }
 
 // Partial results of a row and part, in the caller's workspace: D sums, then
 // (m, l) pairs after all sums.

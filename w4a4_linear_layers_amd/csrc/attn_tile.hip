@@ -538,6 +538,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
     if (wanted && half == 0) parts.ml[slot] = float2{m, l};
   } else {
     const float inv = inverse(l);
+    if (__any(inv == 0.0f)) {                      // (normed(), apart: few waves have such rows)
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = inv == 0.0f ? 0.0f : o[d][i];
+    }
     char* to = valid ? reinterpret_cast<char*>(static_cast<__bf16*>(a.O) + row * a.ldo + static_cast<int64_t>(head) * D)
                      : nullptr;
 #pragma unroll
