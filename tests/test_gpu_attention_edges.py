@@ -92,3 +92,26 @@ def test_rows_whose_scores_are_all_minus_infinity(dtype, what):
         o = S.attn_decode(q.to(DEV), S.KvCache(k.to(DEV), v.to(DEV)), torch.zeros(B, 1, dtype=torch.int32, device=DEV),
                           ints([0] * B).to(DEV), max_len=0, prefix=table[0].to(DEV), prefix_len=n)
         assert o.count_nonzero() == 0
+
+
+# ------------------------------------------------------------------ norms of tiny heads
+
+@TYPES
+@pytest.mark.parametrize("layout,rot", [("half", 128), ("half", 20)])
+def test_norms_of_heads_whose_mean_square_is_denormal(dtype, layout, rot):
+    """Values of about 2^-64 and eps 0: the mean square is below the normal
+    numbers of fp32. A square is then off by 2^-150 at most, D of them by 2^-22
+    of their sum, and so is the mean: 2^-21 more of the result at most."""
+    M, Hq, Hkv, D, page = 5, 4, 2, 128, 16
+    g = gen(33)
+    x = (torch.randn(M, Hq + 2 * Hkv, D, generator=g) * 2.0 ** -64).to(dtype)
+    w = [1 + 0.3 * torch.randn(D, generator=g) for _ in range(2)]
+    table = torch.from_numpy(S.rope_table(rot, 9))
+    pos = ints([0, 8, 3, 5, 1])
+    cache = S.KvCache.empty(1, Hkv, page, D, dtype=dtype)
+    q = S.rope_append(x.view(M, -1).to(DEV), Hq, cache, pos.to(DEV), ints(range(M)).to(DEV), table.to(DEV), layout=layout,
+                      q_norm=w[0].to(DEV), k_norm=w[1].to(DEV), eps=0.0)
+    for got, part, n in ((q, x[:, :Hq], 0), (cache.k[0, :, :M].transpose(0, 1), x[:, Hq:Hq + Hkv], 1)):
+        want, tol = R.rotate(part, w[n], 0.0, table, pos, layout, dtype)
+        size, _ = R.rotate(part.abs(), w[n].abs(), 0.0, table.abs(), pos, layout, dtype)
+        R.check(got, want, tol + 2.0 ** -21 * size.abs().max(), "norm")

@@ -74,6 +74,13 @@ __device__ __forceinline__ void load_floats(const float* p, float (&v)[N]) {
   }
 }
 
+// 1 / sqrt(x). The instruction takes numbers below the normal ones for 0.
+__device__ __forceinline__ float inverse_root(float x) {
+  const bool tiny = x < 0x1p-100f;
+  const float r = __builtin_amdgcn_rsqf(tiny ? x * 0x1p100f : x);
+  return tiny ? r * 0x1p50f : r;
+}
+
 // Where token t's keys and values go: element offset of its slot for head 0
 // (heads are D << page_shift apart), or -1.
 __device__ __forceinline__ int64_t slot_base(const RopeArgs& a, int slot, bool pos_ok) {
@@ -160,7 +167,7 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeArgs a) {
 #pragma unroll
         for (int off = L / 2; off > 0; off >>= 1) ss += __shfl_xor(ss, off, L);
         if (key ? a.k_norm != nullptr : a.q_norm != nullptr) {
-          const float r = __builtin_amdgcn_rsqf(ss * (1.0f / D) + a.eps);
+          const float r = inverse_root(ss * (1.0f / D) + a.eps);
 #pragma unroll
           for (int i = 0; i < V; ++i) x[i] *= r * (key ? wk[i] : wq[i]);
         }
@@ -219,7 +226,7 @@ __global__ __launch_bounds__(64) void rope_append_scalar_kernel(RopeArgs a) {
     if (w) {
 #pragma unroll
       for (int off = 32; off > 0; off >>= 1) ss += __shfl_xor(ss, off, 64);
-      const float r = __builtin_amdgcn_rsqf(ss * (1.0f / D) + a.eps);
+      const float r = inverse_root(ss * (1.0f / D) + a.eps);
 #pragma unroll
       for (int e = 0; e < N; ++e) x[e] *= r * w[lane + 64 * e];
     }
