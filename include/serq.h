@@ -473,8 +473,8 @@ int serq_linear_mx(const uint8_t* Xq, const uint8_t* Xsc,
  *
  * Heads. Hq query heads share Hkv key/value heads (Hq a multiple of Hkv);
  * query head h reads key/value head h / (Hq / Hkv). D is 64 or 128 (others
- * SERQ_EUNSUPPORTED). Bounds: 16384 heads, rows * Hq and the keys of a
- * sequence at most 2^30, n_pages * page_size below 2^31.
+ * SERQ_EUNSUPPORTED). Bounds: 16384 heads, rows * Hq of the two attentions
+ * and the keys of a sequence at most 2^30, n_pages * page_size below 2^31.
  */
 
 typedef enum { SERQ_ROPE_HALF = 0, SERQ_ROPE_INTERLEAVED = 1 } serq_rope_layout;
@@ -576,6 +576,9 @@ int serq_rope_append(const void* QKV, serq_dtype dtype, int64_t ld, int M, int H
  *            NULL if that is 0. Its contents need no preparation and are
  *            free again when the call's work is done; calls that may overlap
  *            need one each.
+ * One launch bounds the rows and sequences of a call further: (T / 256 + B) *
+ * Hq below 2^23 with SERQ_BF16 and (T / 32 + B) * Hq below 2^24 with SERQ_F32
+ * are always taken, and SERQ_EINVAL says where it is more than that.
  * T == 0 or B == 0 is a no-op. Errors: SERQ_EINVAL (NULL pointer, bad size,
  * scale not finite, workspace too small), SERQ_EUNSUPPORTED (D or
  * page_size), SERQ_EALIGN, SERQ_EHIP.

@@ -1,5 +1,5 @@
 """The Python side of the attention calls on stand-in tensors (no GPU needed):
-what it hands to the library, and what it refuses."""
+what it hands to the library, and what it refuses; and the library's bounds."""
 
 from __future__ import annotations
 
@@ -212,3 +212,18 @@ def test_a_cache_s_gradient_is_not_lost_silently(lib, call, which):
     with torch.inference_mode():
         call(c)
     assert lib.name is not None
+
+
+@pytest.mark.parametrize("bf16,B,T,Hq,taken", [
+    (1, 1, 1 << 30, 1, True), (1, 1 << 23, 1 << 23, 1, False), (1, (1 << 23) - (1 << 15) - 1, 1 << 23, 1, True),
+    (1, 1 << 22, 1 << 22, 8, True), (0, 1, 1 << 29, 1, False), (0, 1, 1 << 28, 1, True), (0, 1 << 24, 1 << 24, 1, False),
+    (0, 3, 1 << 24, 64, False)])
+def test_prefills_of_more_than_one_launch_are_refused(bf16, B, T, Hq, taken):
+    """On the host, before anything is launched (the addresses are never used)."""
+    from w4a4_linear_layers_amd import _lib
+    need = _lib.lib.serq_attn_prefill_workspace(bf16, B, T, Hq, 1, 64, 100)
+    assert (need == 0) if taken else (need == -1)
+    if not taken:
+        a = 0x100000
+        assert _lib.lib.serq_attn_prefill(a, bf16, 64 * Hq, a, B, T, Hq, 1, 64, a, a, 4, 16, a, 4, a, 100, 0.1, a, 64 * Hq, None,
+                                          0, None) == _lib.SERQ_EINVAL

@@ -115,3 +115,55 @@ def test_norms_of_heads_whose_mean_square_is_denormal(dtype, layout, rot):
         want, tol = R.rotate(part, w[n], 0.0, table, pos, layout, dtype)
         size, _ = R.rotate(part.abs(), w[n].abs(), 0.0, table.abs(), pos, layout, dtype)
         R.check(got, want, tol + 2.0 ** -21 * size.abs().max(), "norm")
+
+
+# ------------------------------------------------------------------ calls of more than one launch
+
+def test_append_of_more_tokens_than_a_launch_takes():
+    """2^24 + 3 tokens: the last ones, a few in the middle and the first are
+    stored, the rest are padding."""
+    M, D, page = (1 << 24) + 3, 64, 16
+    qkv = torch.zeros(M, 2 * D, dtype=torch.bfloat16, device=DEV)
+    at = [0, 5, (1 << 23) - 1, 1 << 23, (1 << 24) - 1, 1 << 24, M - 1]
+    rows = rnd(gen(34), len(at), 2 * D).to(DEV)
+    qkv[at] = rows
+    slot = torch.full((M,), -1, dtype=torch.int32, device=DEV)
+    slot[at] = torch.arange(len(at), dtype=torch.int32, device=DEV)
+    pos = torch.full((M,), 3, dtype=torch.int32, device=DEV)
+    pos[at] = torch.arange(len(at), dtype=torch.int32, device=DEV)
+    table = torch.from_numpy(S.rope_table(D, 9)).to(DEV)
+    big, small = (S.KvCache(torch.zeros(1, 1, page, D, dtype=torch.bfloat16, device=DEV),
+                            torch.zeros(1, 1, page, D, dtype=torch.bfloat16, device=DEV)) for _ in range(2))
+    S.rope_append(qkv, 0, big, pos, slot, table)
+    S.rope_append(rows, 0, small, pos[at].contiguous(), slot[at].contiguous(), table)
+    assert torch.equal(big.k, small.k) and torch.equal(big.v, small.v) and small.k.count_nonzero() > 0
+
+
+@pytest.mark.parametrize("prefix_len", [0, 40])
+def test_decode_of_more_sequences_than_a_launch_takes(prefix_len):
+    """2^23 + 5 sequences, most of them without tokens of their own: with a
+    prefix every one gives what a call for it alone does."""
+    B, Hq, D, page = (1 << 23) + 5, 1, 64, 16
+    g = gen(35)
+    cache = S.KvCache(rnd(g, 24, 1, page, D).to(DEV), rnd(g, 24, 1, page, D).to(DEV))
+    at = [0, 1, (1 << 22) - 1, 1 << 22, (1 << 23) - 1, 1 << 23, B - 1]
+    q = torch.zeros(B, Hq, D, dtype=torch.bfloat16, device=DEV)
+    q[at] = rnd(g, len(at), Hq, D).to(DEV)
+    kv = torch.zeros(B, dtype=torch.int32, device=DEV)
+    kv[at] = ints([3, 17, 300, 40, 299, 1, 100]).to(DEV)
+    table = torch.zeros(B, 19, dtype=torch.int32, device=DEV)
+    table[at] = torch.stack([torch.randperm(21, generator=g)[:19].to(torch.int32) for _ in at]).to(DEV)
+    prefix = ints([21, 22, 23]).to(DEV) if prefix_len else None
+    call = dict(max_len=300, prefix=prefix, prefix_len=prefix_len)
+    o = S.attn_decode(q, cache, table, kv, **call)
+    for i in at:
+        one = S.attn_decode(q[i:i + 1], cache, table[i:i + 1], kv[i:i + 1], **call)
+        # (parts of the keys are cut otherwise there: two roundings of the same sum)
+        assert (o[i].float() - one[0].float()).abs().max() <= 2.0 ** -7 * cache.v.float().abs().max()
+    rest = torch.ones(B, dtype=torch.bool, device=DEV)
+    rest[at] = False
+    if prefix_len:
+        own = cache.v[21:24].reshape(-1, D)[:prefix_len].double().mean(0).to(torch.bfloat16)
+        assert (o[:, 0][rest].float() - own.float()).abs().max() <= 2.0 ** -7 * cache.v.float().abs().max()
+    else:
+        assert o[rest].count_nonzero() == 0

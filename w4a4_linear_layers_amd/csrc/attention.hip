@@ -793,7 +793,6 @@ constexpr int kTileRows = 256;       // rows of a workgroup of the tile kernel
 constexpr int64_t kPrefixTileWork = 6000000;
 
 PrefillPlan plan_prefill(int bf16, int B, int T, int Hq, int Hkv, int D, int max_len) {
-  (void)B;
   PrefillPlan p{};
   const int G = Hq / Hkv;
   p.tiled = bf16;
@@ -810,6 +809,9 @@ PrefillPlan plan_prefill(int bf16, int B, int T, int Hq, int Hkv, int D, int max
   if (splits > kMostSplits) splits = kMostSplits;
   p.splits = splits < 1 ? 1 : static_cast<int>(splits);
   p.bytes = parts_bytes(static_cast<int64_t>(T) * Hq, D, p.splits);
+  // (a launch takes fewer than 2^32 work items along x)
+  const int64_t blocks = (static_cast<int64_t>(T / p.tile_pos) + B) * (Hq / p.pack);
+  if (blocks * (p.tiled ? 512 : 64 * kPrefillWaves) > UINT32_MAX) p.bytes = -1;
   return p;
 }
 
@@ -866,25 +868,44 @@ DecodePlan plan_decode(int bf16, int B, int Hq, int Hkv, int D, int prefix_len, 
   return p;
 }
 
-hipError_t launch_attn_decode(const AttnArgs& a, const DecodePlan& p, hipStream_t st) {
-  const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
-  const Parts parts = parts_of(a.workspace, rows, a.D, p.splits + p.psplits);
-  if (p.ptiled) {
-    const hipError_t e = launch_attn_prefix_tile(a, p.psplits, p.pchunk, parts, st);
+// Sequences a launch: fewer than 2^32 work items, 512 of them to a sequence and
+// query head at most (beyond this many rows there is one part each).
+constexpr int kRowsOfLaunch = 1 << 22;
+
+hipError_t launch_attn_decode(const AttnArgs& all, const DecodePlan& plan, hipStream_t st) {
+  const int splits = plan.splits + plan.psplits;
+  const Parts all_parts = parts_of(all.workspace, static_cast<int64_t>(all.B) * all.Hq, all.D, splits);
+  const int64_t most = kRowsOfLaunch / all.Hq, bytes = all.bf16 ? 2 : 4;
+  for (int64_t b = 0; b < all.B; b += most) {
+    AttnArgs a = all;
+    a.B = static_cast<int>(all.B - b < most ? all.B - b : most);
+    a.Q = static_cast<const char*>(all.Q) + b * all.ldq * bytes;
+    a.O = static_cast<char*>(all.O) + b * all.ldo * bytes;
+    a.kv_len = all.kv_len + b;
+    if (all.page_table) a.page_table = all.page_table + b * all.max_pages;
+    const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
+    const Parts parts{all_parts.o + b * a.Hq * splits * a.D, all_parts.ml + b * a.Hq * splits, splits};
+    DecodePlan p = plan;
+    if (p.psplits > 0) p.ptiles = ceil_div(rows / a.Hkv, p.ptiled ? kTileRows : 16);
+    if (p.ptiled) {
+      const hipError_t e = launch_attn_prefix_tile(a, p.psplits, p.pchunk, parts, st);
+      if (e != hipSuccess) return e;
+    }
+    const int64_t blocks = (p.ptiled ? 0 : static_cast<int64_t>(a.Hkv) * p.ptiles * p.psplits) +
+                           static_cast<int64_t>(a.B) * p.tiles * a.Hkv * p.splits;
+    const dim3 grid(static_cast<unsigned>(blocks));
+    if (a.bf16) {
+      if (a.D == 64) launch_decode<__bf16, 64>(a, p, parts, grid, st);
+      else launch_decode<__bf16, 128>(a, p, parts, grid, st);
+    } else {
+      if (a.D == 64) launch_decode<float, 64>(a, p, parts, grid, st);
+      else launch_decode<float, 128>(a, p, parts, grid, st);
+    }
+    if (splits > 1) launch_join<false>(a, PrefillPlan{}, rows, p.psplits, p.chunk, parts, st);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const int64_t blocks = (p.ptiled ? 0 : static_cast<int64_t>(a.Hkv) * p.ptiles * p.psplits) +
-                         static_cast<int64_t>(a.B) * p.tiles * a.Hkv * p.splits;
-  const dim3 grid(static_cast<unsigned>(blocks));
-  if (a.bf16) {
-    if (a.D == 64) launch_decode<__bf16, 64>(a, p, parts, grid, st);
-    else launch_decode<__bf16, 128>(a, p, parts, grid, st);
-  } else {
-    if (a.D == 64) launch_decode<float, 64>(a, p, parts, grid, st);
-    else launch_decode<float, 128>(a, p, parts, grid, st);
-  }
-  if (p.splits + p.psplits > 1) launch_join<false>(a, PrefillPlan{}, rows, p.psplits, p.chunk, parts, st);
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace serq

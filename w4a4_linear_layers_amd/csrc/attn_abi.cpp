@@ -28,8 +28,7 @@ inline bool valid_heads(int Hq, int Hkv) {
 
 inline bool valid_dtype(serq_dtype t) { return t == SERQ_F32 || t == SERQ_BF16; }
 
-// Bounds of one call: rows * heads (and with them the workgroups of a launch)
-// and keys of a sequence.
+// Bounds of one call: rows * heads and keys of a sequence.
 inline bool valid_rows(int64_t rows, int Hq) { return rows * Hq <= (int64_t{1} << 30); }
 constexpr int kMaxKeys = 1 << 30;
 
@@ -156,6 +155,7 @@ extern "C" int serq_attn_prefill(const void* Q, serq_dtype dtype, int64_t ldq, c
   if (!page_table && max_pages > 0 && max_len > 0) return SERQ_EINVAL;
   if (!aligned(cu_q, 4) || !aligned(kv_len, 4) || !aligned(page_table, 4)) return SERQ_EALIGN;
   const serq::PrefillPlan plan = serq::plan_prefill(dtype == SERQ_BF16, B, T, Hq, Hkv, D, max_len);
+  if (plan.bytes < 0) return SERQ_EINVAL;
   if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes)) return SERQ_EINVAL;
   if (!aligned(workspace, 16)) return SERQ_EALIGN;
   serq::AttnArgs a = attention_args(Q, dtype, ldq, B, Hq, Hkv, D, Kc, Vc, n_pages, page_size, page_table, max_pages,

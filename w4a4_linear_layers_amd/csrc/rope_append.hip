@@ -306,9 +306,24 @@ hipError_t launch_typed(const RopeArgs& a, hipStream_t st) {
 
 }  // namespace
 
+// A launch takes fewer than 2^32 work items along x, 2^24 tokens of 256.
+constexpr int kTokensOfLaunch = 1 << 23;
+
 hipError_t launch_rope_append(const RopeArgs& a, hipStream_t st) {
-  if (a.bf16) return a.D == 64 ? launch_typed<__bf16, 64>(a, st) : launch_typed<__bf16, 128>(a, st);
-  return a.D == 64 ? launch_typed<float, 64>(a, st) : launch_typed<float, 128>(a, st);
+  const int64_t bytes = a.bf16 ? 2 : 4;
+  for (int64_t t = 0; t < a.M; t += kTokensOfLaunch) {
+    RopeArgs x = a;
+    x.M = static_cast<int>(a.M - t < kTokensOfLaunch ? a.M - t : kTokensOfLaunch);
+    x.QKV = static_cast<const char*>(a.QKV) + t * a.ld * bytes;
+    if (a.Hq > 0) x.Q = static_cast<char*>(a.Q) + t * a.ldq * bytes;
+    if (a.rot > 0) x.pos = a.pos + t;
+    x.slot = a.slot + t;
+    hipError_t e;
+    if (a.bf16) e = a.D == 64 ? launch_typed<__bf16, 64>(x, st) : launch_typed<__bf16, 128>(x, st);
+    else e = a.D == 64 ? launch_typed<float, 64>(x, st) : launch_typed<float, 128>(x, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace serq

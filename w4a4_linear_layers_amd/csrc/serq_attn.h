@@ -58,7 +58,7 @@ struct PrefillPlan {
   int tiled;              // on LDS tiles (attn_tile.hip)
   int pack, tile_pos;
   int splits, target;
-  int64_t bytes;          // workspace
+  int64_t bytes;          // workspace; -1: more than one launch takes
 };
 
 // How serq_attn_decode is cut: the sequences' own keys in `splits` parts of
