@@ -44,7 +44,7 @@ class Fake:
         return self.address
 
     def new_empty(self, shape):
-        return Fake(*(shape if isinstance(shape, (tuple, torch.Size)) else (shape,)), dtype=self.dtype, device=self.index)
+        return Fake(*(shape if isinstance(shape, tuple) else (shape,)), dtype=self.dtype, device=self.index)
 
 
 def ints(*shape, device=0):
@@ -87,8 +87,8 @@ def lib(monkeypatch):
     return rec
 
 
-def cache(pages=4, Hkv=2, page=16, D=64, dtype=torch.bfloat16, device=0):
-    return S.KvCache(Fake(pages, Hkv, page, D, dtype=dtype, device=device), Fake(pages, Hkv, page, D, dtype=dtype, device=device))
+def cache(device=0):
+    return S.KvCache(Fake(4, 2, 16, 64, device=device), Fake(4, 2, 16, 64, device=device))
 
 
 def floats(*shape, device=0):
@@ -109,8 +109,8 @@ def call_prefill(c, dtype=torch.bfloat16, d=0, **kw):
 
 
 def call_decode(c, dtype=torch.bfloat16, d=0, **kw):
-    a = dict(q=Fake(2, 4, 64, dtype=dtype, device=d), cache=c, page_table=ints(2, 3, device=d), kv_len=ints(2, device=d),
-             max_len=40, prefix=ints(1, device=d), prefix_len=16)
+    a = dict(q=Fake(2, 4, 64, dtype=dtype, device=d), cache=c, page_table=ints(2, 3, device=d),
+             kv_len=ints(2, device=d), max_len=40, prefix=ints(1, device=d), prefix_len=16)
     return S.attn_decode(**{**a, **kw})
 
 
@@ -216,8 +216,8 @@ def test_a_cache_s_gradient_is_not_lost_silently(lib, call, which):
 
 @pytest.mark.parametrize("bf16,B,T,Hq,taken", [
     (1, 1, 1 << 30, 1, True), (1, 1 << 23, 1 << 23, 1, False), (1, (1 << 23) - (1 << 15) - 1, 1 << 23, 1, True),
-    (1, 1 << 22, 1 << 22, 8, True), (0, 1, 1 << 29, 1, False), (0, 1, 1 << 28, 1, True), (0, 1 << 24, 1 << 24, 1, False),
-    (0, 3, 1 << 24, 64, False)])
+    (1, 1 << 22, 1 << 22, 8, True), (0, 1, 1 << 29, 1, False), (0, 1, 1 << 28, 1, True),
+    (0, 1 << 24, 1 << 24, 1, False), (0, 3, 1 << 24, 64, False)])
 def test_prefills_of_more_than_one_launch_are_refused(bf16, B, T, Hq, taken):
     """On the host, before anything is launched (the addresses are never used)."""
     from w4a4_linear_layers_amd import _lib
@@ -225,5 +225,5 @@ def test_prefills_of_more_than_one_launch_are_refused(bf16, B, T, Hq, taken):
     assert (need == 0) if taken else (need == -1)
     if not taken:
         a = 0x100000
-        assert _lib.lib.serq_attn_prefill(a, bf16, 64 * Hq, a, B, T, Hq, 1, 64, a, a, 4, 16, a, 4, a, 100, 0.1, a, 64 * Hq, None,
-                                          0, None) == _lib.SERQ_EINVAL
+        assert _lib.lib.serq_attn_prefill(a, bf16, 64 * Hq, a, B, T, Hq, 1, 64, a, a, 4, 16, a, 4, a, 100, 0.1, a,
+                                          64 * Hq, None, 0, None) == _lib.SERQ_EINVAL
