@@ -63,12 +63,16 @@ class KvCache:
             raise ValueError("k and v must be (pages, kv heads, page size, head dim) tensors alike")
         if dev < 0 or not k.is_contiguous() or not v.is_contiguous():
             raise ValueError("device tensors must be contiguous CUDA tensors")
-        if dtype is not _BF16 and dtype is not _F32:
+        if dtype is _BF16:
+            code = SERQ_BF16
+        elif dtype is _F32:
+            code = SERQ_F32
+        else:
             raise ValueError("the cache must be float32 or bfloat16")
         if k.requires_grad or v.requires_grad:
             _no_gradient("the cache")
         pages, heads, page, D = shape
-        return k.data_ptr(), v.data_ptr(), pages, heads, page, D, dtype, SERQ_BF16 if dtype is _BF16 else SERQ_F32, dev
+        return k.data_ptr(), v.data_ptr(), pages, heads, page, D, dtype, code, dev
 
     n_pages = property(lambda self: self._now()[2])
     n_kv_heads = property(lambda self: self._now()[3])
@@ -123,6 +127,8 @@ def _ints(t, shape, dev, what):
 
 def _rows(t, shape, D, dtype, dev, what):
     """Row stride of a (rows, heads, head dim) tensor whose rows are whole."""
+    if len(shape) != 3:
+        raise ValueError(f"{what} must be (rows, heads, head dim)")
     n, h, d = shape
     if d != D or t.dtype is not dtype or t.get_device() != dev:
         raise ValueError(f"{what} must be a CUDA (rows, heads, {D}) tensor of the cache's dtype and device")
@@ -130,13 +136,6 @@ def _rows(t, shape, D, dtype, dev, what):
     if s2 != 1 or (s1 != d and h > 1):
         raise ValueError(f"{what}: heads must lie one after another in a row")
     return s0 if n > 1 else h * d
-
-
-def _shape3(t, what):
-    shape = t.shape
-    if len(shape) != 3:
-        raise ValueError(f"{what} must be (rows, heads, head dim)")
-    return shape
 
 
 def _out(out, shape, dtype, dev):
@@ -147,11 +146,9 @@ def _out(out, shape, dtype, dev):
 
 
 def _space(workspace, need, q, dev):
-    """(tensor that holds it, address, bytes)"""
-    if need <= 0:
-        if need < 0:
-            raise ValueError("sizes that the library does not take")
-        return None, None, 0
+    """(tensor that holds it, address, bytes) of a workspace that is needed"""
+    if need < 0:
+        raise ValueError("sizes that the library does not take")
     if workspace is None:
         workspace = q.new_empty((need + 3) // 2)       # (of q's type: at least two bytes each)
         return workspace, workspace.data_ptr(), need
@@ -237,7 +234,7 @@ def attn_prefill(q, cu_q, cache: KvCache, page_table, kv_len, *, max_len: int, s
                                 workspace=workspace)
     if q.requires_grad:
         _no_gradient("q")
-    shape = _shape3(q, "q")
+    shape = q.shape
     ldq = _rows(q, shape, D, tdt, dev, "q")
     T, Hq, _ = shape
     if page_table.dim() != 2:
@@ -248,7 +245,10 @@ def attn_prefill(q, cu_q, cache: KvCache, page_table, kv_len, *, max_len: int, s
     cp = _ints(cu_q, (B + 1,), dev, "cu_q")
     kp = _ints(kv_len, (B,), dev, "kv_len")
     o, ldo = (q.new_empty(shape), Hq * D) if out is None else _out(out, shape, tdt, dev)
-    hold, wp, size = _space(workspace, lib.serq_attn_prefill_workspace(dt, B, T, Hq, Hkv, D, max_len), q, dev)
+    size = lib.serq_attn_prefill_workspace(dt, B, T, Hq, Hkv, D, max_len)
+    hold = wp = None
+    if size:
+        hold, wp, size = _space(workspace, size, q, dev)
     status = lib.serq_attn_prefill(
         q.data_ptr(), dt, ldq, cp, B, T, Hq, Hkv, D, kc, vc, n_pages, page, tp, pages[1], kp,
         max_len, D ** -0.5 if scale is None else scale, o.data_ptr(), ldo, wp, size, _stream(dev))
@@ -277,7 +277,7 @@ def attn_decode(q, cache: KvCache, page_table, kv_len, *, max_len: int, prefix=N
                                scale=scale, out=out, workspace=workspace)
     if q.requires_grad:
         _no_gradient("q")
-    shape = _shape3(q, "q")
+    shape = q.shape
     ldq = _rows(q, shape, D, tdt, dev, "q")
     B, Hq, _ = shape
     pages = page_table.shape
@@ -292,7 +292,10 @@ def attn_decode(q, cache: KvCache, page_table, kv_len, *, max_len: int, prefix=N
             raise ValueError(f"prefix must hold {need} page ids")
         pp = _ints(prefix, (prefix.numel(),), dev, "prefix")
     o, ldo = (q.new_empty(shape), Hq * D) if out is None else _out(out, shape, tdt, dev)
-    hold, wp, size = _space(workspace, lib.serq_attn_decode_workspace(dt, B, Hq, Hkv, D, prefix_len, max_len), q, dev)
+    size = lib.serq_attn_decode_workspace(dt, B, Hq, Hkv, D, prefix_len, max_len)
+    hold = wp = None
+    if size:
+        hold, wp, size = _space(workspace, size, q, dev)
     status = lib.serq_attn_decode(
         q.data_ptr(), dt, ldq, B, Hq, Hkv, D, kc, vc, n_pages, page, pp, prefix_len, tp,
         pages[1], kp, max_len, D ** -0.5 if scale is None else scale, o.data_ptr(), ldo, wp, size, _stream(dev))
