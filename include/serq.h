@@ -560,7 +560,9 @@ int serq_rope_append(const void* QKV, serq_dtype dtype, int64_t ld, int M, int H
  * of whose scores are -inf. A key or value that a token does not see has no
  * influence on it, NaN and infinities included. Scores, softmax statistics
  * and sums are fp32; with SERQ_BF16 each softmax weight is rounded to bf16
- * for the product with the values.
+ * for the product with the values. Weighted values are summed before they are
+ * divided by the weights' sum, with weights of up to 2^8: a value's magnitude
+ * times the keys it is summed with has to stay below 2^120.
  *   Q        T rows of Hq heads of D, row stride ldq >= Hq D elements; 16-byte
  *            aligned rows.
  *   cu_q     B + 1 int32, cu_q[0] = 0, not decreasing, cu_q[B] = T (values
@@ -569,7 +571,8 @@ int serq_rope_append(const void* QKV, serq_dtype dtype, int64_t ld, int M, int H
  *   page_table  B rows of max_pages page ids;  kv_len  B int32 (taken as at
  *            most min(max_len, max_pages * page_size)).
  *   max_len  bound of kv_len, known to the host; sizes the workspace and
- *            the split of the keys.
+ *            the split of the keys (parts of equal size up to max_len, so a
+ *            bound far above the lengths leaves fewer parts with keys).
  *   O        T rows of Hq heads of D, row stride ldo >= Hq D, 16-byte
  *            aligned rows; must not overlap Q unless it is Q (same stride).
  *   workspace  serq_attn_prefill_workspace(...) bytes, 16-byte aligned, or
@@ -616,7 +619,7 @@ int64_t serq_attn_prefill_workspace(serq_dtype dtype, int B, int T, int Hq, int 
  *            kv_len  B int32, taken as at most min(max_len, max_pages *
  *            page_size), negative as 0.
  *   max_len  bound of kv_len, known to the host: sizes the workspace and the
- *            split of the keys.
+ *            split of the keys, as for serq_attn_prefill.
  *   workspace  serq_attn_decode_workspace(...) bytes, as for
  *            serq_attn_prefill.
  * B == 0 is a no-op. Errors as for serq_attn_prefill.

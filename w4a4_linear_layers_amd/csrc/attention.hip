@@ -6,14 +6,14 @@
 // fp32; a larger maximum scales l and o by 2^(m_old - m_new). Parts of the
 // keys are joined the same way.
 //
-// The kernels here keep 16 query rows to a wave and read keys and values
-// straight from the cache into registers, each once: a decode's queries of one
-// key/value head are a group's few heads, so its keys are read at the rate of
-// HBM with matrix cores to spare (32 sequences of 513 to 32000 tokens, 64 query
-// and 8 key/value heads, 1.04 GB: 195 us, 5.3 TB/s). fp32 prompts use the same
-// steps (three of 500 to 2000 tokens, 16 heads of 64: 126 us, 86 TFLOP/s of the
-// 154 that a large fp32 product reaches). bf16 prompts and long prefixes of
-// many sequences go to attn_tile.hip.
+// The kernels here read keys and values straight from the cache into registers.
+// A decode's waves keep 16 query rows, a group's few heads, and read each key
+// once, at the rate of HBM with matrix cores to spare (32 sequences of 513 to
+// 32000 tokens, 64 query and 8 key/value heads of 128, 1.04 GB: 195 us, 5.3
+// TB/s). fp32 prompts have a loop of their own with 32 rows a wave (three of 500
+// to 2000 tokens, 16 heads of 64: 112 us, 96 TFLOP/s of the 154 that a large
+// fp32 product reaches). bf16 prompts and long prefixes of many sequences go to
+// attn_tile.hip.
 //
 // Both products are taken transposed. S^T = K Q^T leaves each lane with
 // scores of one query (column = lane % 16) and four keys per 16 x 16 tile,
@@ -72,7 +72,11 @@ struct Pages {
 template <typename T, int D>
 struct Rows;
 
-// bf16: 32 keys a step, v_mfma_f32_16x16x32_bf16. Lane (n = lane % 16, g =
+// bf16: 32 keys a step, v_mfma_f32_16x16x32_bf16. That instruction wants both
+// operands in bf16, so each weight is rounded to 8 bits for the product with
+// the values, which have no more; their sum l is of the unrounded ones. Whole
+// outputs are then 0.0018 to 0.0024 from the 64-bit ones (relative norm),
+// 0.0016 to 0.0017 of it their own rounding to bf16. Lane (n = lane % 16, g =
 // lane / 16). Q and K operand c of D / 32: values 32 c + 8 g .. + 7 of row n.
 // V: lane n holds W = D / 16 values W n .. of each of its eight keys; product
 // c takes value W n + c of them as row n of V^T, so O^T register (c, j) is
@@ -163,7 +167,7 @@ struct Rows<__bf16, D> {
     for (int j = 0; j < 8; j += 2) {
       const float a = exp2_(z[j] - r), b = exp2_(z[j + 1] - r);
       l += a + b;
-      p[j / 2] = pack2(a, b);       // weights in 8 bits each, as the values they multiply
+      p[j / 2] = pack2(a, b);       // (see above)
     }
     product(v, __builtin_bit_cast(bf16x8, u32x4{p[0], p[1], p[2], p[3]}), o);
   }
@@ -348,7 +352,9 @@ constexpr int kPrefillWaves = 4, kPrefillRows = 32;
 // of 128) took 586 us against 462 (112 TFLOP/s), three of 500 to 2000 (16
 // heads of 64) 139 against 124; eight of 40 tokens, whose time is the start
 // and the join, 11.7 against 12.9. The loop over keys that all rows see is
-// apart from the one with masks: together the first takes 627 us.
+// apart from the one with masks: together the first takes 627 us. Heads of 128
+// fill all 256 registers and put 38 more in scratch (156 bytes a lane) around
+// the loop with masks, which reads 16 bytes of them a step; the other has none.
 template <int D>
 __global__ __launch_bounds__(64 * kPrefillWaves, D == 64 ? 3 : 2) void attn_prefill_kernel(AttnArgs a, PrefillPlan p,
                                                                                       Parts parts) {
@@ -799,10 +805,10 @@ PrefillPlan plan_prefill(int bf16, int B, int T, int Hq, int Hkv, int D, int max
   p.pack = p.tiled && G % 8 == 0 ? 8 : p.tiled && G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1;
   p.tile_pos = (p.tiled ? kTileRows : kPrefillRows) / p.pack;
   // Workgroups that run at once: one of the tile kernel's a CU, two or three of
-  // the other (with 512 parts 33 and 64 tokens over 4000 keys take 42 us, with
-  // 768 36). Few new tokens over many keys leave CUs idle unless the keys are
-  // cut: 16 tokens of 32 heads over 4096 keys take 21 us with parts and 80
-  // without, 512 over 8192 88 against 164.
+  // the other (two prompts of 33 and 64 tokens over 4000 keys, 16 heads of 64:
+  // 41 us for 512 of them, 35 for 768). Few new tokens over many keys leave CUs
+  // idle unless the keys are cut: 16 tokens of 32 heads over 4096 keys take 20
+  // us with parts and 79 without, 512 over 8192 80 against 153.
   p.target = p.tiled ? 256 : 768;
   int64_t splits = p.target / (static_cast<int64_t>(ceil_div(T, p.tile_pos)) * (Hq / p.pack));
   if (splits > max_len / 256) splits = max_len / 256;

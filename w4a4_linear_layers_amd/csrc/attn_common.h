@@ -78,8 +78,8 @@ struct TileAt {
 // more than idx tiles of class >= c, found by bisection. Otherwise sequence by
 // sequence, the one with the most keys first, each one's longest tile first:
 // sorted by counting, which takes a fifth of the bisection's 2000 cycles. (The
-// fp32 kernel, whose workgroups share a CU, gains from the former, 157 us
-// against 169 for three sequences of 500 to 2000 tokens; on LDS tiles both
+// fp32 kernel, whose workgroups share a CU, gains from the former, 112 us
+// against 122 for three sequences of 500 to 2000 tokens; on LDS tiles both
 // orders run alike.) More sequences than lanes come one after another, each
 // one's longest tile first.
 template <bool BY_KEYS>

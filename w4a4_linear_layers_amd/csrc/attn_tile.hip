@@ -3,7 +3,8 @@
 // One workgroup: eight waves of 32 query rows over the same keys. The rows
 // are `pack` query heads of one group (they share keys and values) times 256
 // / pack positions, so the diagonal wastes little and short sequences fill
-// their tiles. Keys pass in tiles of 64, K and V, through two LDS stages.
+// their tiles. Keys pass in tiles of 64 through four places for K and four for V
+// in LDS.
 //
 // Both products are taken transposed on v_mfma_f32_32x32x16_bf16: S^T = K Q^T
 // leaves each lane with 32 scores of one query (column = lane % 32) per tile,
@@ -12,14 +13,18 @@
 // half h = lane / 32 takes as its eight slots of 16 keys those it already
 // holds (4 h .. 4 h + 3 and 8 + 4 h .. 8 + 4 h + 3). V^T is read from LDS by
 // the transposing reads in the same order. Softmax statistics are one value
-// per lane, and scores never leave the registers.
+// per lane, and scores never leave the registers. Weights are rounded to bf16
+// for the product with the values, which the instruction wants alike; their sum
+// l is of the unrounded ones (outputs 0.0018 to 0.0024 from the 64-bit ones in
+// relative norm, 0.0016 to 0.0017 of it their own rounding to bf16).
 //
-// 16384 tokens of 32 query and 8 key/value heads of 128: 1.78 ms, 1.24 PFLOP/s
-// of the visible pairs (a large bf16 product reaches 1.39 here). The matrix
-// cores are busy 69 % of the cycles; under this load the card runs at about
-// 1.7 GHz, so what fewer cycles gain its clock gives back in part. A period of
-// two tiles (one of either wave of a SIMD) takes 2600 cycles, 2048 of them
-// matrix products; a workgroup's start and end another 12000.
+// 16384 tokens of 32 query and 8 key/value heads of 128: 1.78 to 1.91 ms on
+// several cards, 1.15 to 1.24 PFLOP/s of the visible pairs (a large bf16
+// product reaches 1.39). The matrix cores are busy 69 % of the cycles; under
+// this load the card runs at about 1.7 GHz, so what fewer cycles gain its clock
+// gives back in part. A period of two tiles (one of either wave of a SIMD)
+// takes 2600 cycles, 2048 of them matrix products; a workgroup's start and end
+// another 12000.
 
 #include <type_traits>
 
@@ -246,7 +251,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
   };
 
   f32x16 s[2];                           // scores: register i of block kb is key 32 kb + 8 (i / 4) + 4 half + i % 4
-  u32x4 w[4];                            // weights of 16 keys each, in bf16 as the values they multiply
+  u32x4 w[4];                            // weights of 16 keys each, in bf16
 
   const auto scores = [&](int slot) {
     int base = kbase + slot * kTile;
