@@ -227,3 +227,21 @@ def test_prefills_of_more_than_one_launch_are_refused(bf16, B, T, Hq, taken):
         a = 0x100000
         assert _lib.lib.serq_attn_prefill(a, bf16, 64 * Hq, a, B, T, Hq, 1, 64, a, a, 4, 16, a, 4, a, 100, 0.1, a,
                                           64 * Hq, None, 0, None) == _lib.SERQ_EINVAL
+
+
+@pytest.mark.parametrize("call", [call_prefill, call_decode])
+@pytest.mark.parametrize("max_len", [(1 << 30) + 1, 1 << 31, 1 << 32, (1 << 32) + 40, 1 << 63, -1, -(1 << 32) + 40])
+def test_a_bound_that_no_int_holds_is_refused(lib, call, max_len):
+    """(ctypes would hand on its low 32 bits)"""
+    with pytest.raises(ValueError):
+        call(cache(), max_len=max_len)
+    assert lib.name is None
+    assert S.attn_prefill_workspace(cache(), 2, 5, 4, max_len) == S.attn_decode_workspace(cache(), 2, 4, 0, max_len) == -1
+
+
+def test_a_prefix_that_no_int_holds_is_refused(lib):
+    for n in (-1, -(1 << 32) + 16, (1 << 32) + 16):
+        with pytest.raises(ValueError):
+            call_decode(cache(), prefix_len=n)
+        assert S.attn_decode_workspace(cache(), 2, 4, n, 40) == -1
+    assert lib.name is None

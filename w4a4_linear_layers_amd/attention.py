@@ -29,6 +29,7 @@ except ImportError:  # pragma: no cover - library use without PyTorch
     torch = None
 
 _BF16, _F32, _I32 = (getattr(torch, name, None) for name in ("bfloat16", "float32", "int32"))
+_MOST_KEYS = 1 << 30     # (a larger int would reach the library by its low 32 bits)
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
 
@@ -214,8 +215,11 @@ def rope_append(qkv, n_heads: int, cache: KvCache, pos, slot, table, *, layout: 
 
 
 def attn_prefill_workspace(cache: KvCache, B: int, T: int, n_heads: int, max_len: int) -> int:
-    """Bytes of workspace attn_prefill needs (serq_attn_prefill_workspace)."""
+    """Bytes of workspace attn_prefill needs (serq_attn_prefill_workspace);
+    -1 for sizes that it does not take."""
     _, _, _, Hkv, _, D, _, dt, _ = cache._now()
+    if not 0 <= max_len <= _MOST_KEYS:
+        return -1
     return lib.serq_attn_prefill_workspace(dt, B, T, n_heads, Hkv, D, max_len)
 
 
@@ -237,6 +241,8 @@ def attn_prefill(q, cu_q, cache: KvCache, page_table, kv_len, *, max_len: int, s
     shape = q.shape
     ldq = _rows(q, shape, D, tdt, dev, "q")
     T, Hq, _ = shape
+    if not 0 <= max_len <= _MOST_KEYS:
+        raise ValueError("max_len must be 0 to 2^30")
     if page_table.dim() != 2:
         raise ValueError("page_table must be sequences x pages")
     pages = page_table.shape
@@ -258,8 +264,11 @@ def attn_prefill(q, cu_q, cache: KvCache, page_table, kv_len, *, max_len: int, s
 
 
 def attn_decode_workspace(cache: KvCache, B: int, n_heads: int, prefix_len: int, max_len: int) -> int:
-    """Bytes of workspace attn_decode needs (serq_attn_decode_workspace)."""
+    """Bytes of workspace attn_decode needs (serq_attn_decode_workspace); -1
+    for sizes that it does not take."""
     _, _, _, Hkv, _, D, _, dt, _ = cache._now()
+    if not 0 <= max_len <= _MOST_KEYS or not 0 <= prefix_len <= _MOST_KEYS:
+        return -1
     return lib.serq_attn_decode_workspace(dt, B, n_heads, Hkv, D, prefix_len, max_len)
 
 
@@ -280,6 +289,8 @@ def attn_decode(q, cache: KvCache, page_table, kv_len, *, max_len: int, prefix=N
     shape = q.shape
     ldq = _rows(q, shape, D, tdt, dev, "q")
     B, Hq, _ = shape
+    if not 0 <= max_len <= _MOST_KEYS or not 0 <= prefix_len <= _MOST_KEYS:
+        raise ValueError("max_len and prefix_len must be 0 to 2^30")
     pages = page_table.shape
     if len(pages) != 2 or pages[0] != B:
         raise ValueError(f"page_table must be {B} x pages")
