@@ -548,6 +548,70 @@ int serq_rope_append(const void* QKV, serq_dtype dtype, int64_t ld, int M, int H
                      void* stream);
 
 /*
+ * serq_rope_append_axes -- serq_rope_append for tokens with a position on each
+ * of several axes (time, height and width of a picture's or clip's patches):
+ * pair i of a head is rotated by the position on axis pair_axis[i], by the
+ * table's row for that position as before.
+ *   n_axes     1 to 4.
+ *   pair_axis  host, rot_dim / 2 bytes, each below n_axes; read during the
+ *              call. May be NULL when n_axes is 1.
+ *   pos        n_axes rows of M int32 (axis a of token t at a * M + t). A
+ *              token with a position outside [0, max_pos) on any axis gets NaN
+ *              queries and is not stored.
+ * All else, errors included, as for serq_rope_append; SERQ_EINVAL for n_axes
+ * or an axis outside these ranges.
+ */
+int serq_rope_append_axes(const void* QKV, serq_dtype dtype, int64_t ld, int M, int Hq, int Hkv, int D,
+                          const float* q_norm, const float* k_norm, float eps,
+                          const float* table, int rot_dim, int max_pos, serq_rope_layout layout,
+                          int n_axes, const uint8_t* pair_axis, const int32_t* pos, const int32_t* slot,
+                          void* Q, int64_t ldq, void* Kc, void* Vc, int n_pages, int page_size,
+                          void* stream);
+
+/*
+ * The paged cache in 8 bits. Kc and Vc hold FP8 codes (OCP E4M3, one byte a
+ * value) in the layout above, and each block of 16 tokens of a page and head
+ * has a power of two:
+ *     k_scale[page][kv head][page_size / 16],  v_scale likewise,
+ * bytes e + 127 (OCP E8M0) with -117 <= e <= 120; both arrays 4-byte aligned.
+ * A cache value is code * 2^e. Half the bytes of a bf16 cache and 1 in 16 D
+ * more; a value has 4 significant bits, so it is off by at most 2^-4 of itself
+ * (2^-10 * 2^e near 0).
+ *
+ * Storing a block's token 0 begins it anew: its scale then comes from what that
+ * call stores in it, and the codes of its other tokens stay as they are, to be
+ * stored after it. Later tokens may need a larger scale; the block's other
+ * codes are then multiplied by 2^(old e - new e), exactly but for those that fall below
+ * 2^-6 (rounded to the nearest multiple of 2^-9, ties to even). One call
+ * stores a block's tokens from rows next to one another, in any order; where
+ * rows of other blocks, or rows that are not stored, lie between them, that
+ * block's values are unspecified.
+ *
+ * serq_rope_append_f8 -- serq_rope_append_axes onto such a cache. Keys are
+ * computed in 64 bits (norm, products and sums) and rounded to fp32 once; then
+ * with m the largest finite |y| of a block's new tokens (of one head, of keys or
+ * of values)
+ *     e = the least integer >= -117 with m <= 448 * 2^e, at least the block's
+ *         e of before unless it is begun anew;
+ *     code = y * 2^-e rounded to E4M3 (nearest, ties to even).
+ * NaN and infinities become the code NaN and do not change the scale. Queries
+ * as for serq_rope_append.
+ *   dtype      of QKV and Q.
+ *   Kc, Vc     n_pages * Hkv * page_size * D bytes each, 16-byte aligned.
+ *   k_scale, v_scale  n_pages * Hkv * page_size / 16 bytes each. Bytes outside
+ *              10..247 of a block that is not begun anew are taken as the
+ *              nearest inside.
+ * Errors as for serq_rope_append_axes, SERQ_EINVAL and SERQ_EALIGN (4 bytes)
+ * for the scales too. Uses no scratch memory.
+ */
+int serq_rope_append_f8(const void* QKV, serq_dtype dtype, int64_t ld, int M, int Hq, int Hkv, int D,
+                        const float* q_norm, const float* k_norm, float eps,
+                        const float* table, int rot_dim, int max_pos, serq_rope_layout layout,
+                        int n_axes, const uint8_t* pair_axis, const int32_t* pos, const int32_t* slot,
+                        void* Q, int64_t ldq, uint8_t* Kc, uint8_t* Vc, uint8_t* k_scale, uint8_t* v_scale,
+                        int n_pages, int page_size, void* stream);
+
+/*
  * serq_attn_prefill -- online, device memory, asynchronous on `stream`.
  *
  * Causal attention of the new tokens of B sequences, packed one after
@@ -635,6 +699,32 @@ int serq_attn_decode(const void* Q, serq_dtype dtype, int64_t ldq, int B, int Hq
  * -1 for invalid ones. Host only. */
 int64_t serq_attn_decode_workspace(serq_dtype dtype, int B, int Hq, int Hkv, int D, int prefix_len,
                                    int max_len);
+
+/*
+ * serq_attn_prefill_f8, serq_attn_decode_f8 -- the same attentions over a cache
+ * in 8 bits: keys and values are code * 2^e, exactly (they are bf16 numbers),
+ * and everything else is as for serq_attn_prefill and serq_attn_decode with
+ * `dtype` that of Q and O. A code NaN behaves as a NaN does there. Scales of
+ * blocks that no token of a sequence lies in are never used.
+ * Errors as there; SERQ_EINVAL (NULL) and SERQ_EALIGN (not 4-byte aligned) for
+ * the scales too. Their workspaces are sized by their own functions.
+ */
+int serq_attn_prefill_f8(const void* Q, serq_dtype dtype, int64_t ldq, const int32_t* cu_q, int B, int T,
+                         int Hq, int Hkv, int D, const uint8_t* Kc, const uint8_t* Vc,
+                         const uint8_t* k_scale, const uint8_t* v_scale, int n_pages, int page_size,
+                         const int32_t* page_table, int max_pages, const int32_t* kv_len, int max_len,
+                         float scale, void* O, int64_t ldo, void* workspace, int64_t workspace_bytes,
+                         void* stream);
+int64_t serq_attn_prefill_f8_workspace(serq_dtype dtype, int B, int T, int Hq, int Hkv, int D, int max_len);
+
+int serq_attn_decode_f8(const void* Q, serq_dtype dtype, int64_t ldq, int B, int Hq, int Hkv, int D,
+                        const uint8_t* Kc, const uint8_t* Vc, const uint8_t* k_scale, const uint8_t* v_scale,
+                        int n_pages, int page_size, const int32_t* prefix_table, int prefix_len,
+                        const int32_t* page_table, int max_pages, const int32_t* kv_len, int max_len,
+                        float scale, void* O, int64_t ldo, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+int64_t serq_attn_decode_f8_workspace(serq_dtype dtype, int B, int Hq, int Hkv, int D, int prefix_len,
+                                      int max_len);
 
 #ifdef __cplusplus
 }

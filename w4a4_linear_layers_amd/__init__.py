@@ -19,15 +19,15 @@ import numpy as np
 
 from . import _lib
 from ._lib import SERQ_BF16, SERQ_F32, SerqError, check
-from .attention import (KvCache, attn_decode, attn_decode_workspace, attn_prefill, attn_prefill_workspace, rope_append,
-                        rope_table)
+from .attention import (KvCache, KvCacheF8, attn_decode, attn_decode_workspace, attn_prefill, attn_prefill_workspace,
+                        rope_append, rope_table)
 
 lib = _lib.lib
 
 __all__ = ["SerqLayer", "DeviceLayer", "calibrate", "calibrate_gptq", "permute_outputs", "quant_act", "silu_mul_quant_act",
            "linear", "kernel_name", "rq_row_bytes", "SerqError", "Bf6Layer", "bf6_bytes", "prepack_bf6", "act_bf6",
-           "linear_bf6", "bf6_kernel_name", "MxLayer", "calibrate_mx", "quant_act_mx", "linear_mx", "KvCache", "rope_table",
-           "rope_append", "attn_prefill", "attn_prefill_workspace", "attn_decode", "attn_decode_workspace"]
+           "linear_bf6", "bf6_kernel_name", "MxLayer", "calibrate_mx", "quant_act_mx", "linear_mx", "KvCache", "KvCacheF8",
+           "rope_table", "rope_append", "attn_prefill", "attn_prefill_workspace", "attn_decode", "attn_decode_workspace"]
 
 
 def _ptr(a: np.ndarray):

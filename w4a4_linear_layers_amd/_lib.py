@@ -23,7 +23,9 @@ EXPORTS = ("serq_strerror", "serq_abi_version", "serq_calibrate", "serq_calibrat
            "serq_rq_row_bytes", "serq_bf6_bytes", "serq_prepack_bf6", "serq_act_bf6", "serq_linear_bf6",
            "serq_linear_bf6_kernel_name", "serq_calibrate_mx", "serq_quant_act_mx", "serq_linear_mx",
            "serq_rope_table", "serq_rope_append", "serq_attn_prefill", "serq_attn_prefill_workspace",
-           "serq_attn_decode", "serq_attn_decode_workspace")
+           "serq_attn_decode", "serq_attn_decode_workspace",
+           "serq_rope_append_axes", "serq_rope_append_f8", "serq_attn_prefill_f8", "serq_attn_prefill_f8_workspace",
+           "serq_attn_decode_f8", "serq_attn_decode_f8_workspace")
 
 
 class SerqError(RuntimeError):
@@ -98,6 +100,22 @@ def _load() -> ctypes.CDLL:
     lib.serq_attn_decode.restype = ip
     lib.serq_attn_decode_workspace.argtypes = [i32, ip, ip, ip, ip, ip, ip]
     lib.serq_attn_decode_workspace.restype = i64
+    lib.serq_rope_append_axes.argtypes = [vp, i32, i64, ip, ip, ip, ip, vp, vp, fp, vp, ip, ip, i32, ip, vp, vp, vp, vp,
+                                          i64, vp, vp, ip, ip, vp]
+    lib.serq_rope_append_axes.restype = ip
+    lib.serq_rope_append_f8.argtypes = [vp, i32, i64, ip, ip, ip, ip, vp, vp, fp, vp, ip, ip, i32, ip, vp, vp, vp, vp,
+                                        i64, vp, vp, vp, vp, ip, ip, vp]
+    lib.serq_rope_append_f8.restype = ip
+    lib.serq_attn_prefill_f8.argtypes = [vp, i32, i64, vp, ip, ip, ip, ip, ip, vp, vp, vp, vp, ip, ip, vp, ip, vp, ip, fp,
+                                         vp, i64, vp, i64, vp]
+    lib.serq_attn_prefill_f8.restype = ip
+    lib.serq_attn_prefill_f8_workspace.argtypes = [i32, ip, ip, ip, ip, ip, ip]
+    lib.serq_attn_prefill_f8_workspace.restype = i64
+    lib.serq_attn_decode_f8.argtypes = [vp, i32, i64, ip, ip, ip, ip, vp, vp, vp, vp, ip, ip, vp, ip, vp, ip, vp, ip, fp,
+                                        vp, i64, vp, i64, vp]
+    lib.serq_attn_decode_f8.restype = ip
+    lib.serq_attn_decode_f8_workspace.argtypes = [i32, ip, ip, ip, ip, ip, ip]
+    lib.serq_attn_decode_f8_workspace.restype = i64
     return lib
 
 

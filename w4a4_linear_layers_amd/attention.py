@@ -8,6 +8,8 @@ current torch stream.
     o = attn_prefill(q, cu_q, cache, pages, kv_len, max_len=...)     # new tokens, packed
     o = attn_decode(q, cache, pages, kv_len, max_len=...)            # one token per sequence
 
+KvCacheF8 in place of KvCache holds 8-bit codes; the calls are the same.
+
 For inference: none of these calls has a backward pass. Where torch records
 gradients, a tensor that requires one is refused rather than its gradient
 lost; under torch.no_grad() it is taken.
@@ -28,7 +30,8 @@ try:
 except ImportError:  # pragma: no cover - library use without PyTorch
     torch = None
 
-_BF16, _F32, _I32 = (getattr(torch, name, None) for name in ("bfloat16", "float32", "int32"))
+_BF16, _F32, _I32, _F8, _U8 = (getattr(torch, name, None)
+                               for name in ("bfloat16", "float32", "int32", "float8_e4m3fn", "uint8"))
 _MOST_KEYS = 1 << 30     # (a larger int would reach the library by its low 32 bits)
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
@@ -89,6 +92,67 @@ class KvCache:
         shape = (n_pages, n_kv_heads, page_size, head_dim)
         dtype = torch.bfloat16 if dtype is None else dtype
         return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
+
+
+@dataclass
+class KvCacheF8:
+    """Paged keys and values in 8 bits: ``k`` and ``v`` contiguous
+    float8_e4m3fn device tensors (pages, kv heads, page size, head dim), and
+    ``k_scale`` and ``v_scale`` uint8 ones (pages, kv heads, page size / 16), a
+    power of two 2^(byte - 127) for each block of 16 tokens and head. A value
+    is its code times its block's power. Queries are bfloat16 or float32,
+    whichever a call is given. A block begins with its first token and is
+    filled in order (serq_rope_append_f8 says how its scale follows). Tensors
+    may be replaced, as for KvCache."""
+
+    k: "object"
+    v: "object"
+    k_scale: "object"
+    v_scale: "object"
+
+    def __post_init__(self):
+        self._now()
+
+    def _now(self):
+        """As KvCache._now, with None for the dtypes and the scales' addresses
+        at the end."""
+        k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
+        shape, dev = k.shape, k.get_device()
+        if len(shape) != 4 or v.shape != shape or k.dtype is not _F8 or v.dtype is not _F8 or v.get_device() != dev:
+            raise ValueError("k and v must be float8_e4m3fn (pages, kv heads, page size, head dim) tensors alike")
+        pages, heads, page, D = shape
+        blocks = (pages, heads, page // 16)
+        if (ks.dtype is not _U8 or vs.dtype is not _U8 or ks.shape != blocks or vs.shape != blocks
+                or ks.get_device() != dev or vs.get_device() != dev):
+            raise ValueError("k_scale and v_scale must be uint8 (pages, kv heads, page size / 16) tensors on the device of k")
+        if dev < 0 or not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+            raise ValueError("device tensors must be contiguous CUDA tensors")
+        if k.requires_grad or v.requires_grad:
+            _no_gradient("the cache")
+        return k.data_ptr(), v.data_ptr(), pages, heads, page, D, None, None, dev, ks.data_ptr(), vs.data_ptr()
+
+    n_pages = property(lambda self: self._now()[2])
+    n_kv_heads = property(lambda self: self._now()[3])
+    page_size = property(lambda self: self._now()[4])
+    head_dim = property(lambda self: self._now()[5])
+    pointers = property(lambda self: self._now()[:2])
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, *, device="cuda"):
+        """A cache of uninitialised pages."""
+        shape, blocks = (n_pages, n_kv_heads, page_size, head_dim), (n_pages, n_kv_heads, page_size // 16)
+        k, v = (torch.empty(shape, dtype=_F8, device=device) for _ in range(2))
+        ks, vs = (torch.empty(blocks, dtype=_U8, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+
+def _query_type(t, what):
+    """(dtype, the library's) of queries to a cache of codes."""
+    if t.dtype is _BF16:
+        return _BF16, SERQ_BF16
+    if t.dtype is _F32:
+        return _F32, SERQ_F32
+    raise ValueError(f"{what} must be float32 or bfloat16")
 
 
 def rope_table(rot_dim: int, max_pos: int, *, theta: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
@@ -167,18 +231,25 @@ def _norm(w, D, dev):
     return w.data_ptr()
 
 
-def rope_append(qkv, n_heads: int, cache: KvCache, pos, slot, table, *, layout: str = "half", q_norm=None, k_norm=None,
-                eps: float = 1e-6, out=None):
+def rope_append(qkv, n_heads: int, cache, pos, slot, table, *, layout: str = "half", q_norm=None, k_norm=None,
+                eps: float = 1e-6, pair_axis=None, out=None):
     """Queries of the q/k/v linear's output, with keys and values stored in
-    the cache (serq_rope_append), on the current stream. ``qkv`` is M x
-    (n_heads + 2 kv heads) * head dim (unit column stride), ``pos`` and
-    ``slot`` M int32, ``table`` (max_pos, rot_dim) float32 on the device or
-    None for no rotation. Returns M x n_heads x head dim."""
-    kc, vc, n_pages, Hkv, page, D, tdt, dt, dev = cache._now()
+    the cache (serq_rope_append; serq_rope_append_f8 for a KvCacheF8), on the
+    current stream. ``qkv`` is M x (n_heads + 2 kv heads) * head dim (unit
+    column stride), ``pos`` and ``slot`` M int32, ``table`` (max_pos, rot_dim)
+    float32 on the device or None for no rotation. ``pair_axis`` gives tokens a
+    position on each of several axes (serq_rope_append_axes): rot_dim / 2
+    numbers (bytes, or any sequence), the axis that turns each pair; ``pos`` is
+    then axes x M, with an axis for each number up to the largest at least.
+    Returns M x n_heads x head dim."""
+    now = cache._now()
+    kc, vc, n_pages, Hkv, page, D, tdt, dt, dev = now[:9]
     if dev != _current():
         with torch.cuda.device(dev):
             return rope_append(qkv, n_heads, cache, pos, slot, table, layout=layout, q_norm=q_norm, k_norm=k_norm,
-                               eps=eps, out=out)
+                               eps=eps, pair_axis=pair_axis, out=out)
+    if tdt is None:
+        tdt, dt = _query_type(qkv, "qkv")
     shape = qkv.shape
     if len(shape) != 2 or qkv.get_device() != dev or qkv.dtype is not tdt:
         raise ValueError("qkv must be a two-dimensional CUDA tensor of the cache's dtype and device")
@@ -194,50 +265,74 @@ def rope_append(qkv, n_heads: int, cache: KvCache, pos, slot, table, *, layout: 
     if order is None:
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}")
     rot = max_pos = 0
-    tp = pp = None
+    tp = pp = axes = None
+    n_axes = 1
     if table is not None:
         size = table.shape
         if len(size) != 2 or table.dtype is not _F32 or table.get_device() != dev or not table.is_contiguous():
             raise ValueError("table must be a contiguous CUDA (max_pos, rot_dim) float32 tensor on the cache's device")
         max_pos, rot = size
         if rot:
-            tp, pp = table.data_ptr(), _ints(pos, (M,), dev, "pos")
+            if pair_axis is None:
+                tp, pp = table.data_ptr(), _ints(pos, (M,), dev, "pos")
+            else:
+                axes, n_axes = bytes(pair_axis), pos.shape[0] if pos.dim() == 2 else 0
+                if len(axes) != rot // 2 or not 1 <= n_axes <= 4 or max(axes) >= n_axes:
+                    raise ValueError(f"pair_axis must hold {rot // 2} axes and pos a row of {M} for each (four at most)")
+                tp, pp = table.data_ptr(), _ints(pos, (n_axes, M), dev, "pos")
     qw = None if q_norm is None else _norm(q_norm, D, dev)
     kw = None if k_norm is None else _norm(k_norm, D, dev)
     sp = _ints(slot, (M,), dev, "slot")
     q, ldq = (qkv.new_empty((M, n_heads, D)), n_heads * D) if out is None else _out(out, (M, n_heads, D), tdt, dev)
-    status = lib.serq_rope_append(
-        qkv.data_ptr(), dt, ld, M, n_heads, Hkv, D, qw, kw, eps, tp, rot, max_pos, order, pp,
-        sp, q.data_ptr(), ldq, kc, vc, n_pages, page, _stream(dev))
+    if len(now) > 9:
+        status = lib.serq_rope_append_f8(
+            qkv.data_ptr(), dt, ld, M, n_heads, Hkv, D, qw, kw, eps, tp, rot, max_pos, order, n_axes, axes, pp,
+            sp, q.data_ptr(), ldq, kc, vc, now[9], now[10], n_pages, page, _stream(dev))
+    elif axes is not None:
+        status = lib.serq_rope_append_axes(
+            qkv.data_ptr(), dt, ld, M, n_heads, Hkv, D, qw, kw, eps, tp, rot, max_pos, order, n_axes, axes, pp,
+            sp, q.data_ptr(), ldq, kc, vc, n_pages, page, _stream(dev))
+    else:
+        status = lib.serq_rope_append(
+            qkv.data_ptr(), dt, ld, M, n_heads, Hkv, D, qw, kw, eps, tp, rot, max_pos, order, pp,
+            sp, q.data_ptr(), ldq, kc, vc, n_pages, page, _stream(dev))
     if status:
-        check("serq_rope_append", status)
+        check("serq_rope_append" + ("_f8" if len(now) > 9 else ""), status)
     return q
 
 
-def attn_prefill_workspace(cache: KvCache, B: int, T: int, n_heads: int, max_len: int) -> int:
+def attn_prefill_workspace(cache, B: int, T: int, n_heads: int, max_len: int, *, dtype=None) -> int:
     """Bytes of workspace attn_prefill needs (serq_attn_prefill_workspace);
-    -1 for sizes that it does not take."""
-    _, _, _, Hkv, _, D, _, dt, _ = cache._now()
+    -1 for sizes that it does not take. ``dtype``: of the queries to a
+    KvCacheF8 (bfloat16 unless given)."""
+    now = cache._now()
+    Hkv, D, dt = now[3], now[5], now[7]
     if not 0 <= max_len <= _MOST_KEYS:
         return -1
+    if len(now) > 9:
+        return lib.serq_attn_prefill_f8_workspace(SERQ_F32 if dtype is _F32 else SERQ_BF16, B, T, n_heads, Hkv, D, max_len)
     return lib.serq_attn_prefill_workspace(dt, B, T, n_heads, Hkv, D, max_len)
 
 
-def attn_prefill(q, cu_q, cache: KvCache, page_table, kv_len, *, max_len: int, scale: float | None = None, out=None,
+def attn_prefill(q, cu_q, cache, page_table, kv_len, *, max_len: int, scale: float | None = None, out=None,
                  workspace=None):
     """Causal attention of packed new tokens over the cache
-    (serq_attn_prefill) on the current stream. ``q`` is T x heads x head dim,
+    (serq_attn_prefill; serq_attn_prefill_f8 for a KvCacheF8) on the current
+    stream. ``q`` is T x heads x head dim,
     ``cu_q`` B + 1, ``page_table`` B x pages and ``kv_len`` B int32 on the
     device; ``max_len`` bounds kv_len; ``scale`` is head_dim ** -0.5 unless
     given. A workspace is taken from torch's allocator unless given. Returns
     T x heads x head dim."""
-    kc, vc, n_pages, Hkv, page, D, tdt, dt, dev = cache._now()
+    now = cache._now()
+    kc, vc, n_pages, Hkv, page, D, tdt, dt, dev = now[:9]
     if dev != _current():
         with torch.cuda.device(dev):
             return attn_prefill(q, cu_q, cache, page_table, kv_len, max_len=max_len, scale=scale, out=out,
                                 workspace=workspace)
     if q.requires_grad:
         _no_gradient("q")
+    if tdt is None:
+        tdt, dt = _query_type(q, "q")
     shape = q.shape
     ldq = _rows(q, shape, D, tdt, dev, "q")
     T, Hq, _ = shape
@@ -251,41 +346,56 @@ def attn_prefill(q, cu_q, cache: KvCache, page_table, kv_len, *, max_len: int, s
     cp = _ints(cu_q, (B + 1,), dev, "cu_q")
     kp = _ints(kv_len, (B,), dev, "kv_len")
     o, ldo = (q.new_empty(shape), Hq * D) if out is None else _out(out, shape, tdt, dev)
-    size = lib.serq_attn_prefill_workspace(dt, B, T, Hq, Hkv, D, max_len)
+    codes = len(now) > 9
+    size = (lib.serq_attn_prefill_f8_workspace if codes else lib.serq_attn_prefill_workspace)(dt, B, T, Hq, Hkv, D, max_len)
     hold = wp = None
     if size:
         hold, wp, size = _space(workspace, size, q, dev)
-    status = lib.serq_attn_prefill(
-        q.data_ptr(), dt, ldq, cp, B, T, Hq, Hkv, D, kc, vc, n_pages, page, tp, pages[1], kp,
-        max_len, D ** -0.5 if scale is None else scale, o.data_ptr(), ldo, wp, size, _stream(dev))
+    scale = D ** -0.5 if scale is None else scale
+    if codes:
+        status = lib.serq_attn_prefill_f8(
+            q.data_ptr(), dt, ldq, cp, B, T, Hq, Hkv, D, kc, vc, now[9], now[10], n_pages, page, tp, pages[1], kp,
+            max_len, scale, o.data_ptr(), ldo, wp, size, _stream(dev))
+    else:
+        status = lib.serq_attn_prefill(
+            q.data_ptr(), dt, ldq, cp, B, T, Hq, Hkv, D, kc, vc, n_pages, page, tp, pages[1], kp,
+            max_len, scale, o.data_ptr(), ldo, wp, size, _stream(dev))
     if status:
-        check("serq_attn_prefill", status)
+        check("serq_attn_prefill" + ("_f8" if codes else ""), status)
     return o
 
 
-def attn_decode_workspace(cache: KvCache, B: int, n_heads: int, prefix_len: int, max_len: int) -> int:
+def attn_decode_workspace(cache, B: int, n_heads: int, prefix_len: int, max_len: int, *, dtype=None) -> int:
     """Bytes of workspace attn_decode needs (serq_attn_decode_workspace); -1
-    for sizes that it does not take."""
-    _, _, _, Hkv, _, D, _, dt, _ = cache._now()
+    for sizes that it does not take. ``dtype``: of the queries to a KvCacheF8
+    (bfloat16 unless given)."""
+    now = cache._now()
+    Hkv, D, dt = now[3], now[5], now[7]
     if not 0 <= max_len <= _MOST_KEYS or not 0 <= prefix_len <= _MOST_KEYS:
         return -1
+    if len(now) > 9:
+        return lib.serq_attn_decode_f8_workspace(SERQ_F32 if dtype is _F32 else SERQ_BF16, B, n_heads, Hkv, D, prefix_len,
+                                                 max_len)
     return lib.serq_attn_decode_workspace(dt, B, n_heads, Hkv, D, prefix_len, max_len)
 
 
-def attn_decode(q, cache: KvCache, page_table, kv_len, *, max_len: int, prefix=None, prefix_len: int = 0,
+def attn_decode(q, cache, page_table, kv_len, *, max_len: int, prefix=None, prefix_len: int = 0,
                 scale: float | None = None, out=None, workspace=None):
-    """One new token per sequence over the cache (serq_attn_decode) on the
-    current stream. ``q`` is B x heads x head dim; ``page_table`` B x pages
+    """One new token per sequence over the cache (serq_attn_decode;
+    serq_attn_decode_f8 for a KvCacheF8) on the current stream. ``q`` is B x heads x head dim; ``page_table`` B x pages
     and ``kv_len`` B int32 give each sequence's own tokens, ``prefix`` (int32
     page ids) and ``prefix_len`` the tokens that all of them share before
     those. Returns B x heads x head dim."""
-    kc, vc, n_pages, Hkv, page, D, tdt, dt, dev = cache._now()
+    now = cache._now()
+    kc, vc, n_pages, Hkv, page, D, tdt, dt, dev = now[:9]
     if dev != _current():
         with torch.cuda.device(dev):
             return attn_decode(q, cache, page_table, kv_len, max_len=max_len, prefix=prefix, prefix_len=prefix_len,
                                scale=scale, out=out, workspace=workspace)
     if q.requires_grad:
         _no_gradient("q")
+    if tdt is None:
+        tdt, dt = _query_type(q, "q")
     shape = q.shape
     ldq = _rows(q, shape, D, tdt, dev, "q")
     B, Hq, _ = shape
@@ -303,13 +413,21 @@ def attn_decode(q, cache: KvCache, page_table, kv_len, *, max_len: int, prefix=N
             raise ValueError(f"prefix must hold {need} page ids")
         pp = _ints(prefix, (prefix.numel(),), dev, "prefix")
     o, ldo = (q.new_empty(shape), Hq * D) if out is None else _out(out, shape, tdt, dev)
-    size = lib.serq_attn_decode_workspace(dt, B, Hq, Hkv, D, prefix_len, max_len)
+    codes = len(now) > 9
+    size = (lib.serq_attn_decode_f8_workspace if codes else lib.serq_attn_decode_workspace)(dt, B, Hq, Hkv, D, prefix_len,
+                                                                                            max_len)
     hold = wp = None
     if size:
         hold, wp, size = _space(workspace, size, q, dev)
-    status = lib.serq_attn_decode(
-        q.data_ptr(), dt, ldq, B, Hq, Hkv, D, kc, vc, n_pages, page, pp, prefix_len, tp,
-        pages[1], kp, max_len, D ** -0.5 if scale is None else scale, o.data_ptr(), ldo, wp, size, _stream(dev))
+    scale = D ** -0.5 if scale is None else scale
+    if codes:
+        status = lib.serq_attn_decode_f8(
+            q.data_ptr(), dt, ldq, B, Hq, Hkv, D, kc, vc, now[9], now[10], n_pages, page, pp, prefix_len, tp,
+            pages[1], kp, max_len, scale, o.data_ptr(), ldo, wp, size, _stream(dev))
+    else:
+        status = lib.serq_attn_decode(
+            q.data_ptr(), dt, ldq, B, Hq, Hkv, D, kc, vc, n_pages, page, pp, prefix_len, tp,
+            pages[1], kp, max_len, scale, o.data_ptr(), ldo, wp, size, _stream(dev))
     if status:
-        check("serq_attn_decode", status)
+        check("serq_attn_decode" + ("_f8" if codes else ""), status)
     return o

@@ -24,26 +24,12 @@
 // (4 g .. 4 g + 3 of each tile) as its summation slots, and the values are
 // loaded to match. Scores never pass through LDS.
 
-#include "attn_common.h"
+#include "attn_decode.h"
 
 namespace serq {
 namespace {
 
 using namespace attn;
-
-// Maximum (sum) over the four lane groups that share a query.
-__device__ __forceinline__ float max_groups(float v) {
-  const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
-  const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
-}
-__device__ __forceinline__ float sum_groups(float v) {
-  const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(x[0]) + __uint_as_float(x[1]);
-  const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(y[0]) + __uint_as_float(y[1]);
-}
 
 // One sequence's pages of one key/value head, for one wave.
 template <typename T, int D>
@@ -68,6 +54,11 @@ struct Pages {
   }
 };
 
+template <typename T, int D>
+__device__ __forceinline__ Pages<T, D> pages_of(const AttnArgs& a, const int32_t* table, int last, int kvh) {
+  return {static_cast<const T*>(a.Kc), static_cast<const T*>(a.Vc), table, last, a.page_shift, a.n_pages, a.Hkv, kvh};
+}
+
 // Sixteen query rows of one wave: operands, running statistics, O^T.
 template <typename T, int D>
 struct Rows;
@@ -88,6 +79,9 @@ struct Rows<__bf16, D> {
   f32x4 o[W];
   float m, l;
 
+  static __device__ __forceinline__ Pages<__bf16, D> pages(const AttnArgs& a, const int32_t* table, int last, int kvh) {
+    return pages_of<__bf16, D>(a, table, last, kvh);
+  }
   __device__ __forceinline__ void init() {
     m = kNone;
     l = 0.0f;
@@ -205,6 +199,9 @@ struct Rows<float, D> {
   f32x4 o[NB * 4];
   float m, l;
 
+  static __device__ __forceinline__ Pages<float, D> pages(const AttnArgs& a, const int32_t* table, int last, int kvh) {
+    return pages_of<float, D>(a, table, last, kvh);
+  }
   __device__ __forceinline__ void init() {
     m = kNone;
     l = 0.0f;
@@ -496,103 +493,6 @@ __global__ __launch_bounds__(64 * kPrefillWaves, D == 64 ? 3 : 2) void attn_pref
   }
 }
 
-// ------------------------------------------------------------------- decode
-
-// One workgroup: 16 query rows over one part of the keys, its waves taking
-// steps in turn and joined through LDS; eight of them where the part is all a
-// sequence has, which is then written as it is. Prefix parts come first: their rows
-// are those of all sequences (row R: sequence R / G, head R % G of the
-// group); a sequence's own parts have its G rows.
-template <typename T, int D, int kDecodeWaves>
-__global__ __launch_bounds__(64 * kDecodeWaves, kDecodeWaves == 4 && sizeof(T) == 2 ? 3 : 2) void attn_decode_kernel(
-    AttnArgs a, DecodePlan p, Parts parts) {
-  __shared__ float so[kDecodeWaves][16][D + 4];
-  __shared__ float sml[kDecodeWaves][2][16];
-  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-  const int wave = uniform(threadIdx.x >> 6);
-  const int G = a.Hq / a.Hkv;
-  int x = blockIdx.x;
-  const int nprefix = p.ptiled ? 0 : a.Hkv * p.ptiles * p.psplits;
-  const bool prefix = x < nprefix;
-  int kvh, R0, rows, part, len, from, to;
-  const int32_t* table;
-  if (prefix) {
-    kvh = x % a.Hkv;
-    x /= a.Hkv;
-    part = x % p.psplits;
-    R0 = x / p.psplits * 16;
-    rows = a.B * G;
-    len = a.prefix_len;
-    table = a.prefix_table;
-    from = part * p.pchunk;
-    to = from + p.pchunk;
-  } else {
-    x -= nprefix;
-    kvh = x % a.Hkv;
-    x /= a.Hkv;
-    part = x % p.splits;
-    x /= p.splits;
-    const int b = x / p.tiles;
-    R0 = b * G + x % p.tiles * 16;
-    rows = (b + 1) * G;
-    len = bounded_len(a, b);
-    table = a.page_table + static_cast<int64_t>(b) * a.max_pages;
-    from = part * p.chunk;
-    to = from + p.chunk;
-    if (from >= len && (from > 0 || p.splits + p.psplits > 1)) return;   // nothing here, and the join knows it
-    part += p.psplits;
-  }
-  if (to > len) to = len;
-  const int R = R0 + n < rows ? R0 + n : rows - 1;
-  const int b = R / G, h = kvh * G + R % G;
-  Rows<T, D> r;
-  r.init();
-  r.load_q(static_cast<const T*>(a.Q) + b * a.ldq + static_cast<int64_t>(h) * D, g);
-  if (from < to) {
-    Pages<T, D> pg{static_cast<const T*>(a.Kc), static_cast<const T*>(a.Vc), table, (len - 1) >> a.page_shift,
-                   a.page_shift, a.n_pages, a.Hkv, kvh};
-    for (int key = from + wave * r.kStep; key < to; key += kDecodeWaves * r.kStep)
-      r.step(pg, key, to, a.scale_log2, n, g);
-  }
-  const float lw = sum_groups(r.l);
-  r.store_f32(&so[wave][n][0], g);
-  if (g == 0) {
-    sml[wave][0][n] = r.m;
-    sml[wave][1][n] = lw;
-  }
-  __syncthreads();
-  // the waves' parts joined, all threads over the 16 rows
-  constexpr int N = 4 * kDecodeWaves, W = D / N;
-  const int q = threadIdx.x / N, d = threadIdx.x % N * W;
-  if (R0 + q >= rows) return;
-  float m = kNone;
-#pragma unroll
-  for (int w = 0; w < kDecodeWaves; ++w) m = fmaxf(m, sml[w][0][q]);
-  float l = 0.0f, o[W] = {};
-#pragma unroll
-  for (int w = 0; w < kDecodeWaves; ++w) {
-    const float f = exp2_(sml[w][0][q] - ref(m));
-    l = __builtin_fmaf(f, sml[w][1][q], l);
-#pragma unroll
-    for (int i = 0; i < W; ++i) o[i] = __builtin_fmaf(f, so[w][q][d + i], o[i]);
-  }
-  const int bq = (R0 + q) / G, hq = kvh * G + (R0 + q) % G;
-  if constexpr (kDecodeWaves == 4) {
-    if (p.splits + p.psplits > 1) {
-      const int64_t slot = (static_cast<int64_t>(bq) * a.Hq + hq) * parts.splits + part;
-#pragma unroll
-      for (int i = 0; i < W; i += 4)
-        *reinterpret_cast<f32x4*>(parts.o + slot * D + d + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
-      if (d == 0) parts.ml[slot] = float2{m, l};
-      return;
-    }
-  }
-  const float inv = inverse(l);
-  T* out = static_cast<T*>(a.O) + bq * a.ldo + static_cast<int64_t>(hq) * D + d;
-#pragma unroll
-  for (int i = 0; i < W; ++i) out[i] = static_cast<T>(normed(o[i], inv));
-}
-
 // --------------------------------------------------------------------- join
 
 // The parts of a row's keys joined in their order. Rows of a prefill see parts
@@ -759,8 +659,8 @@ void launch_join(const AttnArgs& a, const PrefillPlan& p, int64_t rows, int pspl
 
 template <typename T, int D>
 void launch_decode(const AttnArgs& a, const DecodePlan& p, const Parts& parts, dim3 grid, hipStream_t st) {
-  if (p.waves == 8) attn_decode_kernel<T, D, 8><<<grid, 512, 0, st>>>(a, p, parts);
-  else attn_decode_kernel<T, D, 4><<<grid, 256, 0, st>>>(a, p, parts);
+  if (p.waves == 8) attn_decode_kernel<Rows<T, D>, T, D, 8><<<grid, 512, 0, st>>>(a, p, parts);
+  else attn_decode_kernel<Rows<T, D>, T, D, 4><<<grid, 256, 0, st>>>(a, p, parts);
 }
 
 Parts parts_of(void* workspace, int64_t rows, int D, int splits) {
@@ -798,10 +698,10 @@ constexpr int kTileRows = 256;       // rows of a workgroup of the tile kernel
 // 18.6 against 12.8.
 constexpr int64_t kPrefixTileWork = 6000000;
 
-PrefillPlan plan_prefill(int bf16, int B, int T, int Hq, int Hkv, int D, int max_len) {
+PrefillPlan plan_prefill(int kind, int B, int T, int Hq, int Hkv, int D, int max_len) {
   PrefillPlan p{};
   const int G = Hq / Hkv;
-  p.tiled = bf16;
+  p.tiled = (kind & kBf16) != 0;
   p.pack = p.tiled && G % 8 == 0 ? 8 : p.tiled && G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1;
   p.tile_pos = (p.tiled ? kTileRows : kPrefillRows) / p.pack;
   // Workgroups that run at once: one of the tile kernel's a CU, two or three of
@@ -830,14 +730,15 @@ hipError_t launch_attn_prefill(const AttnArgs& a, const PrefillPlan& p, hipStrea
   } else {
     const int64_t tiles = static_cast<int64_t>(a.T / p.tile_pos) + a.B;  // at least the sum of the sequences' tiles
     const dim3 grid(static_cast<unsigned>(tiles * (a.Hq / p.pack)), p.splits), block(64 * kPrefillWaves);
-    if (a.D == 64) attn_prefill_kernel<64><<<grid, block, 0, st>>>(a, p, parts);
+    if (a.k_scale) launch_prefill_f8(a, p, parts, grid, st);
+    else if (a.D == 64) attn_prefill_kernel<64><<<grid, block, 0, st>>>(a, p, parts);
     else attn_prefill_kernel<128><<<grid, block, 0, st>>>(a, p, parts);
   }
   if (p.splits > 1) launch_join<true>(a, p, rows, 0, 0, parts, st);
   return hipGetLastError();
 }
 
-DecodePlan plan_decode(int bf16, int B, int Hq, int Hkv, int D, int prefix_len, int max_len) {
+DecodePlan plan_decode(int kind, int B, int Hq, int Hkv, int D, int prefix_len, int max_len) {
   DecodePlan p{};
   const int G = Hq / Hkv;
   const int64_t rows = static_cast<int64_t>(B) * G;
@@ -864,7 +765,7 @@ DecodePlan plan_decode(int bf16, int B, int Hq, int Hkv, int D, int prefix_len, 
     p.waves = max_len > 256 ? 8 : 4;
   }
   if (prefix_len > 0) {
-    p.ptiled = bf16 && static_cast<int64_t>(B) * Hq * prefix_len >= kPrefixTileWork;
+    p.ptiled = (kind & kBf16) && static_cast<int64_t>(B) * Hq * prefix_len >= kPrefixTileWork;
     p.ptiles = ceil_div(rows, p.ptiled ? kTileRows : 16);
     s = ceil_div(p.ptiled ? 256 : 1024, static_cast<int64_t>(Hkv) * p.ptiles);
     p.pchunk = cut(prefix_len, s, p.ptiled ? 64 : 128);
@@ -900,7 +801,9 @@ hipError_t launch_attn_decode(const AttnArgs& all, const DecodePlan& plan, hipSt
     const int64_t blocks = (p.ptiled ? 0 : static_cast<int64_t>(a.Hkv) * p.ptiles * p.psplits) +
                            static_cast<int64_t>(a.B) * p.tiles * a.Hkv * p.splits;
     const dim3 grid(static_cast<unsigned>(blocks));
-    if (a.bf16) {
+    if (a.k_scale) {
+      launch_decode_f8(a, p, parts, grid, st);
+    } else if (a.bf16) {
       if (a.D == 64) launch_decode<__bf16, 64>(a, p, parts, grid, st);
       else launch_decode<__bf16, 128>(a, p, parts, grid, st);
     } else {

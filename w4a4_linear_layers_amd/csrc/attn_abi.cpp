@@ -1,6 +1,6 @@
 // C ABI entry points of the attention half: host-side argument validation and
-// dispatch of serq_rope_append, serq_attn_prefill and serq_attn_decode onto
-// the caller's HIP stream. serq_rope_table (host) lives in rope_table.cpp.
+// dispatch of serq_rope_append, serq_attn_prefill and serq_attn_decode, and of
+// their forms for a cache of FP8 codes, onto the caller's HIP stream. serq_rope_table (host) lives in rope_table.cpp.
 
 #include <hip/hip_runtime.h>
 
@@ -34,10 +34,15 @@ constexpr int kMaxKeys = 1 << 30;
 
 }  // namespace
 
-extern "C" int serq_rope_append(const void* QKV, serq_dtype dtype, int64_t ld, int M, int Hq, int Hkv, int D,
-                                const float* q_norm, const float* k_norm, float eps, const float* table, int rot_dim,
-                                int max_pos, serq_rope_layout layout, const int32_t* pos, const int32_t* slot, void* Q,
-                                int64_t ldq, void* Kc, void* Vc, int n_pages, int page_size, void* stream) {
+namespace {
+
+// serq_rope_append and its forms: with several axes, and onto a cache of codes
+// (scales given).
+int rope_append(const void* QKV, serq_dtype dtype, int64_t ld, int M, int Hq, int Hkv, int D, const float* q_norm,
+                const float* k_norm, float eps, const float* table, int rot_dim, int max_pos, serq_rope_layout layout,
+                int n_axes, const uint8_t* pair_axis, const int32_t* pos, const int32_t* slot, void* Q, int64_t ldq,
+                void* Kc, void* Vc, uint8_t* k_scale, uint8_t* v_scale, bool codes, int n_pages, int page_size,
+                void* stream) {
   if (!valid_dtype(dtype) || (layout != SERQ_ROPE_HALF && layout != SERQ_ROPE_INTERLEAVED)) return SERQ_EINVAL;
   if (M < 0 || Hq < 0 || Hkv <= 0 || Hq > kMaxHeads || Hkv > kMaxHeads || D <= 0 || page_size <= 0 || n_pages <= 0)
     return SERQ_EINVAL;
@@ -50,15 +55,23 @@ extern "C" int serq_rope_append(const void* QKV, serq_dtype dtype, int64_t ld, i
     return SERQ_EINVAL;
   if (rot_dim < 0 || rot_dim > D || (rot_dim % 2) != 0) return SERQ_EINVAL;
   if (rot_dim > 0 && (!table || max_pos <= 0)) return SERQ_EINVAL;
+  if (n_axes < 1 || n_axes > 4 || (n_axes > 1 && rot_dim > 0 && !pair_axis)) return SERQ_EINVAL;
   if ((q_norm || k_norm) && !(std::isfinite(eps) && eps >= 0.0f)) return SERQ_EINVAL;
-  if (!Kc || !Vc) return SERQ_EINVAL;
+  if (!Kc || !Vc || (codes && (!k_scale || !v_scale))) return SERQ_EINVAL;
   if (!aligned(Kc, 16) || !aligned(Vc, 16) || !aligned(table, 16) || !aligned(q_norm, 16) || !aligned(k_norm, 16))
     return SERQ_EALIGN;
+  if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return SERQ_EALIGN;
+  serq::RopeArgs a{};
+  if (pair_axis) {
+    for (int i = 0; i < rot_dim / 2; ++i) {
+      if (pair_axis[i] >= n_axes) return SERQ_EINVAL;
+      a.axis_bits[i / 16] |= static_cast<uint32_t>(pair_axis[i]) << (2 * (i % 16));
+    }
+  }
   if (M == 0) return SERQ_OK;
   if (!QKV || !slot || (rot_dim > 0 && !pos) || (Hq > 0 && !Q)) return SERQ_EINVAL;
   const uintptr_t eb = dtype == SERQ_BF16 ? 2 : 4;
   if (!aligned(QKV, eb) || (Hq > 0 && !aligned(Q, eb)) || !aligned(pos, 4) || !aligned(slot, 4)) return SERQ_EALIGN;
-  serq::RopeArgs a{};
   a.QKV = QKV;
   a.ld = ld;
   a.M = M;
@@ -73,15 +86,48 @@ extern "C" int serq_rope_append(const void* QKV, serq_dtype dtype, int64_t ld, i
   a.max_pos = max_pos;
   a.interleaved = layout == SERQ_ROPE_INTERLEAVED;
   a.pos = pos;
+  a.pos_stride = M;
+  a.n_axes = n_axes;
   a.slot = slot;
   a.Q = Q;
   a.ldq = ldq;
   a.Kc = Kc;
   a.Vc = Vc;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
   a.n_pages = n_pages;
   a.page_shift = shift;
   a.bf16 = dtype == SERQ_BF16;
   return serq::launch_rope_append(a, static_cast<hipStream_t>(stream)) == hipSuccess ? SERQ_OK : SERQ_EHIP;
+}
+
+}  // namespace
+
+extern "C" int serq_rope_append(const void* QKV, serq_dtype dtype, int64_t ld, int M, int Hq, int Hkv, int D,
+                                const float* q_norm, const float* k_norm, float eps, const float* table, int rot_dim,
+                                int max_pos, serq_rope_layout layout, const int32_t* pos, const int32_t* slot, void* Q,
+                                int64_t ldq, void* Kc, void* Vc, int n_pages, int page_size, void* stream) {
+  return rope_append(QKV, dtype, ld, M, Hq, Hkv, D, q_norm, k_norm, eps, table, rot_dim, max_pos, layout, 1, nullptr, pos,
+                     slot, Q, ldq, Kc, Vc, nullptr, nullptr, false, n_pages, page_size, stream);
+}
+
+extern "C" int serq_rope_append_axes(const void* QKV, serq_dtype dtype, int64_t ld, int M, int Hq, int Hkv, int D,
+                                     const float* q_norm, const float* k_norm, float eps, const float* table,
+                                     int rot_dim, int max_pos, serq_rope_layout layout, int n_axes,
+                                     const uint8_t* pair_axis, const int32_t* pos, const int32_t* slot, void* Q,
+                                     int64_t ldq, void* Kc, void* Vc, int n_pages, int page_size, void* stream) {
+  return rope_append(QKV, dtype, ld, M, Hq, Hkv, D, q_norm, k_norm, eps, table, rot_dim, max_pos, layout, n_axes,
+                     pair_axis, pos, slot, Q, ldq, Kc, Vc, nullptr, nullptr, false, n_pages, page_size, stream);
+}
+
+extern "C" int serq_rope_append_f8(const void* QKV, serq_dtype dtype, int64_t ld, int M, int Hq, int Hkv, int D,
+                                   const float* q_norm, const float* k_norm, float eps, const float* table,
+                                   int rot_dim, int max_pos, serq_rope_layout layout, int n_axes,
+                                   const uint8_t* pair_axis, const int32_t* pos, const int32_t* slot, void* Q,
+                                   int64_t ldq, uint8_t* Kc, uint8_t* Vc, uint8_t* k_scale, uint8_t* v_scale,
+                                   int n_pages, int page_size, void* stream) {
+  return rope_append(QKV, dtype, ld, M, Hq, Hkv, D, q_norm, k_norm, eps, table, rot_dim, max_pos, layout, n_axes,
+                     pair_axis, pos, slot, Q, ldq, Kc, Vc, k_scale, v_scale, true, n_pages, page_size, stream);
 }
 
 namespace {
@@ -134,11 +180,96 @@ serq::AttnArgs attention_args(const void* Q, serq_dtype dtype, int64_t ldq, int 
 
 }  // namespace
 
-extern "C" int64_t serq_attn_prefill_workspace(serq_dtype dtype, int B, int T, int Hq, int Hkv, int D, int max_len) {
+namespace {
+
+// The cache's scales, where it holds codes.
+struct Scales {
+  const uint8_t* k;
+  const uint8_t* v;
+  bool codes;
+};
+
+inline int kind_of(serq_dtype dtype, bool codes) {
+  return (dtype == SERQ_BF16 ? serq::kBf16 : 0) | (codes ? serq::kCodes : 0);
+}
+
+int check_scales(const Scales& s) {
+  if (!s.codes) return SERQ_OK;
+  if (!s.k || !s.v) return SERQ_EINVAL;
+  return aligned(s.k, 4) && aligned(s.v, 4) ? SERQ_OK : SERQ_EALIGN;
+}
+
+int64_t prefill_workspace(serq_dtype dtype, bool codes, int B, int T, int Hq, int Hkv, int D, int max_len) {
   if (!valid_dtype(dtype) || B < 0 || T < 0 || !valid_heads(Hq, Hkv) || (D != 64 && D != 128) || max_len < 0 ||
       max_len > kMaxKeys || !valid_rows(T, Hq) || !valid_rows(B, Hq))
     return -1;
-  return B == 0 || T == 0 ? 0 : serq::plan_prefill(dtype == SERQ_BF16, B, T, Hq, Hkv, D, max_len).bytes;
+  return B == 0 || T == 0 ? 0 : serq::plan_prefill(kind_of(dtype, codes), B, T, Hq, Hkv, D, max_len).bytes;
+}
+
+int attn_prefill(const void* Q, serq_dtype dtype, int64_t ldq, const int32_t* cu_q, int B, int T, int Hq, int Hkv, int D,
+                 const void* Kc, const void* Vc, const Scales& scales, int n_pages, int page_size,
+                 const int32_t* page_table, int max_pages, const int32_t* kv_len, int max_len, float scale, void* O,
+                 int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (B < 0 || T < 0 || !valid_rows(B, Hq)) return SERQ_EINVAL;
+  int bad = check_attention(Q, dtype, ldq, T, Hq, Hkv, D, Kc, Vc, n_pages, page_size, max_pages, max_len, scale, O, ldo);
+  if (bad == SERQ_OK) bad = check_scales(scales);
+  if (bad != SERQ_OK) return bad;
+  if (B == 0 || T == 0) return SERQ_OK;
+  if (!Q || !O || !cu_q || !kv_len) return SERQ_EINVAL;
+  if (!page_table && max_pages > 0 && max_len > 0) return SERQ_EINVAL;
+  if (!aligned(cu_q, 4) || !aligned(kv_len, 4) || !aligned(page_table, 4)) return SERQ_EALIGN;
+  const serq::PrefillPlan plan = serq::plan_prefill(kind_of(dtype, scales.codes), B, T, Hq, Hkv, D, max_len);
+  if (plan.bytes < 0) return SERQ_EINVAL;
+  if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes)) return SERQ_EINVAL;
+  if (!aligned(workspace, 16)) return SERQ_EALIGN;
+  serq::AttnArgs a = attention_args(Q, dtype, ldq, B, Hq, Hkv, D, Kc, Vc, n_pages, page_size, page_table, max_pages,
+                                    kv_len, max_len, scale, O, ldo, workspace);
+  a.k_scale = scales.k;
+  a.v_scale = scales.v;
+  a.cu_q = cu_q;
+  a.T = T;
+  return serq::launch_attn_prefill(a, plan, static_cast<hipStream_t>(stream)) == hipSuccess ? SERQ_OK : SERQ_EHIP;
+}
+
+int64_t decode_workspace(serq_dtype dtype, bool codes, int B, int Hq, int Hkv, int D, int prefix_len, int max_len) {
+  if (!valid_dtype(dtype) || B < 0 || !valid_heads(Hq, Hkv) || (D != 64 && D != 128) || prefix_len < 0 ||
+      prefix_len > kMaxKeys || max_len < 0 || max_len > kMaxKeys || !valid_rows(B, Hq))
+    return -1;
+  return B == 0 ? 0 : serq::plan_decode(kind_of(dtype, codes), B, Hq, Hkv, D, prefix_len, max_len).bytes;
+}
+
+int attn_decode(const void* Q, serq_dtype dtype, int64_t ldq, int B, int Hq, int Hkv, int D, const void* Kc,
+                const void* Vc, const Scales& scales, int n_pages, int page_size, const int32_t* prefix_table,
+                int prefix_len, const int32_t* page_table, int max_pages, const int32_t* kv_len, int max_len,
+                float scale, void* O, int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (B < 0 || prefix_len < 0 || prefix_len > kMaxKeys) return SERQ_EINVAL;
+  int bad = check_attention(Q, dtype, ldq, B, Hq, Hkv, D, Kc, Vc, n_pages, page_size, max_pages, max_len, scale, O, ldo);
+  if (bad == SERQ_OK) bad = check_scales(scales);
+  if (bad != SERQ_OK) return bad;
+  if (B == 0) return SERQ_OK;
+  if (!Q || !O || !kv_len || (prefix_len > 0 && !prefix_table)) return SERQ_EINVAL;
+  if (!page_table && max_pages > 0 && max_len > 0) return SERQ_EINVAL;
+  if (!aligned(prefix_table, 4) || !aligned(kv_len, 4) || !aligned(page_table, 4)) return SERQ_EALIGN;
+  const serq::DecodePlan plan = serq::plan_decode(kind_of(dtype, scales.codes), B, Hq, Hkv, D, prefix_len, max_len);
+  if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes)) return SERQ_EINVAL;
+  if (!aligned(workspace, 16)) return SERQ_EALIGN;
+  serq::AttnArgs a = attention_args(Q, dtype, ldq, B, Hq, Hkv, D, Kc, Vc, n_pages, page_size, page_table, max_pages,
+                                    kv_len, max_len, scale, O, ldo, workspace);
+  a.k_scale = scales.k;
+  a.v_scale = scales.v;
+  a.prefix_table = prefix_table;
+  a.prefix_len = prefix_len;
+  return serq::launch_attn_decode(a, plan, static_cast<hipStream_t>(stream)) == hipSuccess ? SERQ_OK : SERQ_EHIP;
+}
+
+}  // namespace
+
+extern "C" int64_t serq_attn_prefill_workspace(serq_dtype dtype, int B, int T, int Hq, int Hkv, int D, int max_len) {
+  return prefill_workspace(dtype, false, B, T, Hq, Hkv, D, max_len);
+}
+
+extern "C" int64_t serq_attn_prefill_f8_workspace(serq_dtype dtype, int B, int T, int Hq, int Hkv, int D, int max_len) {
+  return prefill_workspace(dtype, true, B, T, Hq, Hkv, D, max_len);
 }
 
 extern "C" int serq_attn_prefill(const void* Q, serq_dtype dtype, int64_t ldq, const int32_t* cu_q, int B, int T,
@@ -146,31 +277,27 @@ extern "C" int serq_attn_prefill(const void* Q, serq_dtype dtype, int64_t ldq, c
                                  const int32_t* page_table, int max_pages, const int32_t* kv_len, int max_len,
                                  float scale, void* O, int64_t ldo, void* workspace, int64_t workspace_bytes,
                                  void* stream) {
-  if (B < 0 || T < 0 || !valid_rows(B, Hq)) return SERQ_EINVAL;
-  const int bad = check_attention(Q, dtype, ldq, T, Hq, Hkv, D, Kc, Vc, n_pages, page_size, max_pages, max_len, scale,
-                                  O, ldo);
-  if (bad != SERQ_OK) return bad;
-  if (B == 0 || T == 0) return SERQ_OK;
-  if (!Q || !O || !cu_q || !kv_len) return SERQ_EINVAL;
-  if (!page_table && max_pages > 0 && max_len > 0) return SERQ_EINVAL;
-  if (!aligned(cu_q, 4) || !aligned(kv_len, 4) || !aligned(page_table, 4)) return SERQ_EALIGN;
-  const serq::PrefillPlan plan = serq::plan_prefill(dtype == SERQ_BF16, B, T, Hq, Hkv, D, max_len);
-  if (plan.bytes < 0) return SERQ_EINVAL;
-  if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes)) return SERQ_EINVAL;
-  if (!aligned(workspace, 16)) return SERQ_EALIGN;
-  serq::AttnArgs a = attention_args(Q, dtype, ldq, B, Hq, Hkv, D, Kc, Vc, n_pages, page_size, page_table, max_pages,
-                                    kv_len, max_len, scale, O, ldo, workspace);
-  a.cu_q = cu_q;
-  a.T = T;
-  return serq::launch_attn_prefill(a, plan, static_cast<hipStream_t>(stream)) == hipSuccess ? SERQ_OK : SERQ_EHIP;
+  return attn_prefill(Q, dtype, ldq, cu_q, B, T, Hq, Hkv, D, Kc, Vc, Scales{}, n_pages, page_size, page_table, max_pages,
+                      kv_len, max_len, scale, O, ldo, workspace, workspace_bytes, stream);
+}
+
+extern "C" int serq_attn_prefill_f8(const void* Q, serq_dtype dtype, int64_t ldq, const int32_t* cu_q, int B, int T,
+                                    int Hq, int Hkv, int D, const uint8_t* Kc, const uint8_t* Vc, const uint8_t* k_scale,
+                                    const uint8_t* v_scale, int n_pages, int page_size, const int32_t* page_table,
+                                    int max_pages, const int32_t* kv_len, int max_len, float scale, void* O,
+                                    int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream) {
+  return attn_prefill(Q, dtype, ldq, cu_q, B, T, Hq, Hkv, D, Kc, Vc, Scales{k_scale, v_scale, true}, n_pages, page_size,
+                      page_table, max_pages, kv_len, max_len, scale, O, ldo, workspace, workspace_bytes, stream);
 }
 
 extern "C" int64_t serq_attn_decode_workspace(serq_dtype dtype, int B, int Hq, int Hkv, int D, int prefix_len,
                                               int max_len) {
-  if (!valid_dtype(dtype) || B < 0 || !valid_heads(Hq, Hkv) || (D != 64 && D != 128) || prefix_len < 0 ||
-      prefix_len > kMaxKeys || max_len < 0 || max_len > kMaxKeys || !valid_rows(B, Hq))
-    return -1;
-  return B == 0 ? 0 : serq::plan_decode(dtype == SERQ_BF16, B, Hq, Hkv, D, prefix_len, max_len).bytes;
+  return decode_workspace(dtype, false, B, Hq, Hkv, D, prefix_len, max_len);
+}
+
+extern "C" int64_t serq_attn_decode_f8_workspace(serq_dtype dtype, int B, int Hq, int Hkv, int D, int prefix_len,
+                                                 int max_len) {
+  return decode_workspace(dtype, true, B, Hq, Hkv, D, prefix_len, max_len);
 }
 
 extern "C" int serq_attn_decode(const void* Q, serq_dtype dtype, int64_t ldq, int B, int Hq, int Hkv, int D,
@@ -178,20 +305,17 @@ extern "C" int serq_attn_decode(const void* Q, serq_dtype dtype, int64_t ldq, in
                                 const int32_t* prefix_table, int prefix_len, const int32_t* page_table, int max_pages,
                                 const int32_t* kv_len, int max_len, float scale, void* O, int64_t ldo, void* workspace,
                                 int64_t workspace_bytes, void* stream) {
-  if (B < 0 || prefix_len < 0 || prefix_len > kMaxKeys) return SERQ_EINVAL;
-  const int bad = check_attention(Q, dtype, ldq, B, Hq, Hkv, D, Kc, Vc, n_pages, page_size, max_pages, max_len, scale,
-                                  O, ldo);
-  if (bad != SERQ_OK) return bad;
-  if (B == 0) return SERQ_OK;
-  if (!Q || !O || !kv_len || (prefix_len > 0 && !prefix_table)) return SERQ_EINVAL;
-  if (!page_table && max_pages > 0 && max_len > 0) return SERQ_EINVAL;
-  if (!aligned(prefix_table, 4) || !aligned(kv_len, 4) || !aligned(page_table, 4)) return SERQ_EALIGN;
-  const serq::DecodePlan plan = serq::plan_decode(dtype == SERQ_BF16, B, Hq, Hkv, D, prefix_len, max_len);
-  if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes)) return SERQ_EINVAL;
-  if (!aligned(workspace, 16)) return SERQ_EALIGN;
-  serq::AttnArgs a = attention_args(Q, dtype, ldq, B, Hq, Hkv, D, Kc, Vc, n_pages, page_size, page_table, max_pages,
-                                    kv_len, max_len, scale, O, ldo, workspace);
-  a.prefix_table = prefix_table;
-  a.prefix_len = prefix_len;
-  return serq::launch_attn_decode(a, plan, static_cast<hipStream_t>(stream)) == hipSuccess ? SERQ_OK : SERQ_EHIP;
+  return attn_decode(Q, dtype, ldq, B, Hq, Hkv, D, Kc, Vc, Scales{}, n_pages, page_size, prefix_table, prefix_len,
+                     page_table, max_pages, kv_len, max_len, scale, O, ldo, workspace, workspace_bytes, stream);
+}
+
+extern "C" int serq_attn_decode_f8(const void* Q, serq_dtype dtype, int64_t ldq, int B, int Hq, int Hkv, int D,
+                                   const uint8_t* Kc, const uint8_t* Vc, const uint8_t* k_scale, const uint8_t* v_scale,
+                                   int n_pages, int page_size, const int32_t* prefix_table, int prefix_len,
+                                   const int32_t* page_table, int max_pages, const int32_t* kv_len, int max_len,
+                                   float scale, void* O, int64_t ldo, void* workspace, int64_t workspace_bytes,
+                                   void* stream) {
+  return attn_decode(Q, dtype, ldq, B, Hq, Hkv, D, Kc, Vc, Scales{k_scale, v_scale, true}, n_pages, page_size,
+                     prefix_table, prefix_len, page_table, max_pages, kv_len, max_len, scale, O, ldo, workspace,
+                     workspace_bytes, stream);
 }

@@ -221,6 +221,11 @@ __device__ __forceinline__ int in_cache(int page, int n_pages) {
 
 }  // namespace attn
 
+// Kernels over a cache of FP8 codes (attention_f8.hip): decode parts, and fp32
+// prompts.
+void launch_decode_f8(const AttnArgs& a, const DecodePlan& p, const attn::Parts& parts, dim3 grid, hipStream_t stream);
+void launch_prefill_f8(const AttnArgs& a, const PrefillPlan& p, const attn::Parts& parts, dim3 grid, hipStream_t stream);
+
 hipError_t launch_attn_tile(const AttnArgs& a, const PrefillPlan& p, const attn::Parts& parts, hipStream_t stream);
 // The prefix of a decode in `splits` parts of `chunk` keys.
 hipError_t launch_attn_prefix_tile(const AttnArgs& a, int splits, int chunk, const attn::Parts& parts,

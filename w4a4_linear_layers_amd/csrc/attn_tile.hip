@@ -105,13 +105,18 @@ __device__ __forceinline__ int swizzle_v(int r) { return D == 128 ? (r & 3) << 2
 // PREFIX: the prefix part of serq_attn_decode instead. The rows are those of
 // all sequences (row R: sequence R / G, head R % G of the group), 256 to a
 // workgroup, and all of them see all keys.
-template <int D, bool PREFIX>
+// F8: a cache of FP8 codes. Each thread loads D / 8 codes of one row of the next
+// tile into registers, makes them bf16 a period later (the scale of a block
+// of 16 tokens is a power of two, so the values are exact) and writes them to
+// the tile's place; everything after that is as for a bf16 cache.
+template <int D, bool PREFIX, bool F8>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, PrefillPlan p, int chunk,
                                                                    Parts parts) {
   constexpr int kRow = 2 * D;                    // bytes of a row
   constexpr int kTile = kKeys * kRow;            // bytes of a K or V tile
   constexpr int kRows = 1024 / kRow;             // rows of one wave load
-  constexpr int kLoads = kTile / (1024 * kWaves);
+  constexpr int kLoads = F8 ? 1 : kTile / (1024 * kWaves);
+  constexpr int kPer = F8 ? kKeys / kWaves : kRows;      // consecutive rows of a tile that one load of a wave takes
   constexpr int C = D / 16, DB = D / 32;
   // K tiles, then V tiles, and half a tile per wave counted with them for Q at
   // the start (in K's last place and V's last two, which are loaded only when Q
@@ -190,13 +195,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
     voff[i] = lr * kRow + ((lp ^ swizzle_v<D>(r)) << 4);
   }
   // Byte offsets of a tile's rows in either cache, for this wave's loads.
-  const uint64_t page_bytes = (static_cast<uint64_t>(a.Hkv) << a.page_shift) * kRow;
-  const uint32_t head_bytes = (static_cast<uint32_t>(kvh) << a.page_shift) * kRow;
+  constexpr int kCached = F8 ? D : kRow;         // bytes of a row in the cache
+  const uint64_t page_bytes = (static_cast<uint64_t>(a.Hkv) << a.page_shift) * kCached;
+  const uint32_t head_bytes = (static_cast<uint32_t>(kvh) << a.page_shift) * kCached;
   const uint32_t in_mask = (1u << a.page_shift) - 1;
   const auto look_up = [&](int t, int (&pages)[kLoads]) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int x = (from + t * kKeys + kRows * (wave + kWaves * i)) >> a.page_shift;
+      const int x = (from + t * kKeys + kPer * (wave + kWaves * i)) >> a.page_shift;
       pages[i] = page_entry(table, x < last ? x : last);
     }
   };
@@ -204,7 +210,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       at[i] = static_cast<uint32_t>(in_cache(pages[i], a.n_pages)) * page_bytes +
-              (head_bytes + ((from + t * kKeys + kRows * (wave + kWaves * i)) & in_mask) * kRow);
+              (head_bytes + ((from + t * kKeys + kPer * (wave + kWaves * i)) & in_mask) * kCached);
   };
   // V tile t, which some row of the workgroup does not see whole, has landed:
   // this wave's rows past the end, where the cache may hold anything, are
@@ -225,6 +231,57 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
     }
     const int odd = __any(!ok);
     if (lane == 0) odd_rows[slot][wave] = odd;
+  };
+
+  // F8: this thread's codes of the K and V tile to come, and their scales.
+  constexpr int kWords = F8 ? D / 32 : 2;        // dwords of codes a thread
+  const int cr = kPer * wave + (lane >> 3), cp = lane & 7;
+  uint32_t kc[kWords], vc[kWords];
+  float ks = 1.0f, vs = 1.0f;
+  const auto fetch = [&](const void* cache, const uint8_t* scales, uint64_t at, uint32_t (&codes)[kWords], float& scale) {
+    const uint8_t* p = static_cast<const uint8_t*>(cache) + at + ((lane >> 3) * D + cp * (D / 8));
+    if constexpr (kWords == 4) {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) codes[i] = x[i];
+    } else {
+      const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+      codes[0] = x[0], codes[1] = x[1];
+    }
+    const uint64_t block = at / (16 * D);        // (rows of a wave lie in one block)
+    const uint32_t w = ((const __attribute__((address_space(4))) uint32_t*)scales)[block >> 2];
+    scale = __uint_as_float((w >> (8 * (static_cast<int>(block) & 3)) & 0xFFu) << 23);
+  };
+  // Codes to a place: the 16-byte parts of kWords / 2 of a row.
+  const auto put = [&](uint8_t* tile, int swizzle, const uint32_t (&codes)[kWords], float scale) {
+#pragma unroll
+    for (int i = 0; i < kWords / 2; ++i) {
+      u32x4 x;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        x[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[2 * i + j], scale, false));
+        x[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[2 * i + j], scale, true));
+      }
+      *reinterpret_cast<u32x4*>(tile + cr * kRow + (((kWords / 2 * cp + i) ^ swizzle) << 4)) = x;
+    }
+  };
+  const auto put_k = [&](int at) { put(smem + at * kTile, swizzle_k<D>(cr), kc, ks); };
+  // V tile t: as for look_over, the rows past the end cleared, and noted whether
+  // the others are finite.
+  const auto put_v = [&](int t, int at) {
+    if (from + (t + 1) * kKeys > whole) {
+      const bool past = from + t * kKeys + cr >= len;
+      bool odd = false;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        vc[i] = past ? 0 : vc[i];
+        odd |= (((vc[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+      }
+      if (from + t * kKeys + kPer * wave >= len) vs = 1.0f;       // (a scale that is no number)
+      const int any = __any(odd);
+      if (lane == 0) odd_rows[at][wave] = any;
+    }
+    put(smem + (kRing + at) * kTile, swizzle_v<D>(cr), vc, vs);
   };
 
   // Read addresses. K: part 2 c + half of row n (+ 32): its swizzled place is
@@ -405,6 +462,19 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
             uniform(lds0 + (kRing + at) * kTile + 1024 * (wave + kWaves * i)));
     };
     const auto start_load = [&](int j) {           // of 2 kLoads: V(t + kRing - 2), K(t + kRing - 1)
+      if constexpr (F8) {
+        // V(t) and K(t + 1) to their places, then V(t + 1) and K(t + 2) on their way
+        if (j == 0) {
+          put_v(t, place_of(0));
+          fetch(a.Vc, a.v_scale, vat[0], vc, vs);
+        } else if (j == 1) {
+          put_k(place_of(1));
+          place(pages, t + 2, kat);
+          fetch(a.Kc, a.k_scale, kat[0], kc, ks);
+          vat[0] = kat[0];
+        }
+        return;
+      }
       if (j < kLoads) {
         load_v(j, place_of(kRing - 2));
       } else if (j < 2 * kLoads) {
@@ -414,6 +484,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       }
     };
     const auto finish_loads = [&] {                // K(t + 1), V(t)
+      if constexpr (F8) return;
       wait_loads_but<(kRing - 2) * 2 * kLoads>();
       if (from + (t + 1) * kKeys > whole) look_over(t, slot);
     };
@@ -422,7 +493,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
         finish_loads();
         barrier();
       }
-      look_up(t + kRing, pages);                   // (a scalar load; among LDS reads it would stall them)
+      look_up(t + (F8 ? 3 : kRing), pages);        // (a scalar load; among LDS reads it would stall them)
     };
     const auto after_vector = [&](bool ends) {
       if (ends) {
@@ -433,9 +504,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       ++t;
     };
     int early[kRing - 1][kLoads];
+    constexpr int kEarly = F8 ? 2 : kRing - 1;
 #pragma unroll
-    for (int u = 0; u < kRing - 1; ++u) look_up(u, early[u]);
-    look_up(kRing - 1, pages);
+    for (int u = 0; u < kEarly; ++u) look_up(u, early[u]);
+    look_up(kEarly, pages);
     // Q by whole rows through LDS: read as an operand from memory, each load
     // would touch 32 rows, 4000 cycles for the workgroup's 64.
     const int qplace = wave < 2 ? (kRing - 1) * kTile + wave * (kTile / 2)
@@ -447,17 +519,30 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       const int r = kRows * k + lr;
       dma16(shuffle(qrow, r) + ((lp ^ swizzle_k<D>(r)) << 4), uniform(lds0 + qplace + 1024 * k));
     }
+    if constexpr (F8) {
+      uint32_t k0[kWords];
+      float s0;
+      place(early[0], 0, kat);
+      fetch(a.Kc, a.k_scale, kat[0], k0, s0);
+      fetch(a.Vc, a.v_scale, kat[0], vc, vs);
+      place(early[1], 1, kat);
+      fetch(a.Kc, a.k_scale, kat[0], kc, ks);
+      vat[0] = kat[0];
+      put(smem, swizzle_k<D>(cr), k0, s0);
+      wait_loads();                                // Q
+    } else {
 #pragma unroll
-    for (int u = 0; u < kRing - 1; ++u) {          // K(u) and V(u - 1)
-      place(early[u], u, kat);
+      for (int u = 0; u < kRing - 1; ++u) {          // K(u) and V(u - 1)
+        place(early[u], u, kat);
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        load_k(i, u);
-        if (u > 0) load_v(i, u - 1);
-        vat[i] = kat[i];
+        for (int i = 0; i < kLoads; ++i) {
+          load_k(i, u);
+          if (u > 0) load_v(i, u - 1);
+          vat[i] = kat[i];
+        }
       }
+      wait_loads_but<(kRing - 2) * 2 * kLoads>();    // Q, K(0)
     }
-    wait_loads_but<(kRing - 2) * 2 * kLoads>();    // Q, K(0)
     // A negative scale goes into Q's sign, so that the largest product is the
     // largest score.
     const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
@@ -566,8 +651,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
 hipError_t launch_attn_tile(const AttnArgs& a, const PrefillPlan& p, const Parts& parts, hipStream_t st) {
   const int64_t tiles = static_cast<int64_t>(a.T / p.tile_pos) + a.B;    // at least the sum of the sequences' tiles
   const dim3 grid(static_cast<unsigned>(tiles * (a.Hq / p.pack)), p.splits), block(64 * kWaves);
-  if (a.D == 64) attn_tile_kernel<64, false><<<grid, block, 0, st>>>(a, p, 0, parts);
-  else attn_tile_kernel<128, false><<<grid, block, 0, st>>>(a, p, 0, parts);
+  if (a.k_scale) {
+    if (a.D == 64) attn_tile_kernel<64, false, true><<<grid, block, 0, st>>>(a, p, 0, parts);
+    else attn_tile_kernel<128, false, true><<<grid, block, 0, st>>>(a, p, 0, parts);
+  } else {
+    if (a.D == 64) attn_tile_kernel<64, false, false><<<grid, block, 0, st>>>(a, p, 0, parts);
+    else attn_tile_kernel<128, false, false><<<grid, block, 0, st>>>(a, p, 0, parts);
+  }
   return hipGetLastError();
 }
 
@@ -575,8 +665,13 @@ hipError_t launch_attn_prefix_tile(const AttnArgs& a, int splits, int chunk, con
   const int64_t rows = static_cast<int64_t>(a.B) * (a.Hq / a.Hkv);
   const int64_t tiles = (rows + 32 * kWaves - 1) / (32 * kWaves);
   const dim3 grid(static_cast<unsigned>(tiles * a.Hkv), splits), block(64 * kWaves);
-  if (a.D == 64) attn_tile_kernel<64, true><<<grid, block, 0, st>>>(a, PrefillPlan{}, chunk, parts);
-  else attn_tile_kernel<128, true><<<grid, block, 0, st>>>(a, PrefillPlan{}, chunk, parts);
+  if (a.k_scale) {
+    if (a.D == 64) attn_tile_kernel<64, true, true><<<grid, block, 0, st>>>(a, PrefillPlan{}, chunk, parts);
+    else attn_tile_kernel<128, true, true><<<grid, block, 0, st>>>(a, PrefillPlan{}, chunk, parts);
+  } else {
+    if (a.D == 64) attn_tile_kernel<64, true, false><<<grid, block, 0, st>>>(a, PrefillPlan{}, chunk, parts);
+    else attn_tile_kernel<128, true, false><<<grid, block, 0, st>>>(a, PrefillPlan{}, chunk, parts);
+  }
   return hipGetLastError();
 }
 

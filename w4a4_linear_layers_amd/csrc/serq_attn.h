@@ -18,14 +18,19 @@ struct RopeArgs {
   const float* table;     // max_pos x rot: cosines, then sines (null when rot == 0)
   int rot, max_pos;
   int interleaved;
-  const int32_t* pos;
+  const int32_t* pos;     // axis a of token t at a * pos_stride + t
+  int64_t pos_stride;
+  int n_axes;
+  uint32_t axis_bits[4];  // two bits a pair: its axis
   const int32_t* slot;
   void* Q;
   int64_t ldq;
   void* Kc;
   void* Vc;
+  uint8_t* k_scale;       // of a cache of codes, else null
+  uint8_t* v_scale;
   int n_pages, page_shift;
-  int bf16;
+  int bf16;               // of QKV and Q
 };
 
 // One attention call (device pointers, validated sizes).
@@ -34,6 +39,8 @@ struct AttnArgs {
   int64_t ldq;
   const void* Kc;
   const void* Vc;
+  const uint8_t* k_scale;       // of a cache of FP8 codes, else null
+  const uint8_t* v_scale;
   int n_pages, page_shift;
   const int32_t* page_table;
   int max_pages;
@@ -71,8 +78,10 @@ struct DecodePlan {
   int64_t bytes;          // workspace
 };
 
-PrefillPlan plan_prefill(int bf16, int B, int T, int Hq, int Hkv, int D, int max_len);
-DecodePlan plan_decode(int bf16, int B, int Hq, int Hkv, int D, int prefix_len, int max_len);
+// `kind`: kBf16 for bf16 queries (else fp32), kCodes over a cache of FP8 codes.
+constexpr int kBf16 = 1, kCodes = 2;
+PrefillPlan plan_prefill(int kind, int B, int T, int Hq, int Hkv, int D, int max_len);
+DecodePlan plan_decode(int kind, int B, int Hq, int Hkv, int D, int prefix_len, int max_len);
 
 hipError_t launch_rope_append(const RopeArgs& a, hipStream_t stream);
 hipError_t launch_attn_prefill(const AttnArgs& a, const PrefillPlan& p, hipStream_t stream);
