@@ -456,6 +456,55 @@ int serq_linear_mx(const uint8_t* Xq, const uint8_t* Xsc,
                    void* stream);
 
 /*
+ * The linear in 8-bit integers: for the layers that keep 8 bits where others
+ * take 4 (down projections, output heads),
+ *     Y[m, n] = sx[m] * (sw[n] * sum_k Xq[m, k] Wq[n, k]),
+ * a scale for each token and each channel, no compensator and no permutation.
+ *
+ * serq_calibrate_i8 -- offline, host memory, synchronous, deterministic.
+ *   W, w_dtype, alpha  as for serq_calibrate; act_absmax as there, or NULL for
+ *              no smoothing (s_j = 1).
+ * Outputs: s_hat_inv, K floats fl32(1 / s_j) in channel order, for
+ * serq_quant_act and serq_silu_mul_quant_act with a_bits 8; Wq, N x K int8,
+ * row n the codes of fl32(s_j W[j, n]) (qmax 127); sw, N floats.
+ * Errors: SERQ_EINVAL (NULL W or output, K or N <= 0, alpha outside [0, 1],
+ * bad w_dtype).
+ */
+int serq_calibrate_i8(const void* W, serq_dtype w_dtype, int K, int N, const float* act_absmax, float alpha,
+                      float* s_hat_inv, int8_t* Wq, float* sw);
+
+/*
+ * serq_linear_i8 -- online, device memory, asynchronous on `stream`. The sums
+ * are exact (int32); the formula's products are fp32, in its order, and Y is
+ * stored as y_dtype (bf16 with round to nearest even).
+ *   Xq, sx     M x K int8 and M floats (serq_quant_act, a_bits 8).
+ *   Wq, sw     N x K int8 and N floats (serq_calibrate_i8).
+ *   M, K, N    M >= 0 (0: no-op, the M-sized buffers may then be NULL), 0 < K
+ *              < 2^17, 0 < N <= 2^26, M N <= 2^37. K that is no multiple of
+ *              16 takes a plain kernel.
+ *   Y          M x N of y_dtype.
+ *   acc_dbg    NULL, or device M x N int32 that receive the sums.
+ *   workspace  serq_linear_i8_workspace(M, K, N) bytes, 16-byte aligned, or NULL
+ *              if that is 0 (K is cut in parts where there are few outputs).
+ *              Its contents need no preparation and are free again when the
+ *              call's work is done; calls that may overlap need one each.
+ * Errors: SERQ_EINVAL (NULL pointer, sizes, y_dtype, workspace too small),
+ * SERQ_EALIGN (a pointer not 16-byte aligned), SERQ_EHIP.
+ */
+int serq_linear_i8(const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw, int M, int K, int N,
+                   void* Y, serq_dtype y_dtype, int32_t* acc_dbg, void* workspace, int64_t workspace_bytes,
+                   void* stream);
+
+/* Bytes of workspace serq_linear_i8 needs for these sizes (may be 0), or -1 for
+ * invalid ones. Host only. */
+int64_t serq_linear_i8_workspace(int M, int K, int N);
+
+/* Which kernel serq_linear_i8 launches for these sizes (static string:
+ * "stream", "tile128x128", "tile256x256" or "generic"), or NULL for invalid
+ * sizes. Host only. */
+const char* serq_linear_i8_kernel_name(int M, int K, int N);
+
+/*
  * The attention half of a decoder layer, between the q/k/v linear and the
  * output linear: rotating and storing keys, causal attention of new tokens,
  * and single-token attention of a batch that may share a prefix.

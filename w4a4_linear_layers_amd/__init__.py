@@ -27,7 +27,8 @@ lib = _lib.lib
 __all__ = ["SerqLayer", "DeviceLayer", "calibrate", "calibrate_gptq", "permute_outputs", "quant_act", "silu_mul_quant_act",
            "linear", "kernel_name", "rq_row_bytes", "SerqError", "Bf6Layer", "bf6_bytes", "prepack_bf6", "act_bf6",
            "linear_bf6", "bf6_kernel_name", "MxLayer", "calibrate_mx", "quant_act_mx", "linear_mx", "KvCache", "KvCacheF8",
-           "rope_table", "rope_append", "attn_prefill", "attn_prefill_workspace", "attn_decode", "attn_decode_workspace"]
+           "rope_table", "I8Layer", "calibrate_i8", "linear_i8", "linear_i8_workspace", "i8_kernel_name",
+           "rope_append", "attn_prefill", "attn_prefill_workspace", "attn_decode", "attn_decode_workspace"]
 
 
 def _ptr(a: np.ndarray):
@@ -534,3 +535,97 @@ def linear_mx(xq, xsc, layer: MxLayer, *, out_dtype=None, out=None, debug: bool 
         layer.Rq.data_ptr() if r else None, layer.Rsc.data_ptr() if r else None, M, K, N, r, y.data_ptr(), dt,
         am.data_ptr() if debug else None, ar.data_ptr() if debug else None, _stream()))
     return (y, am, ar) if debug else y
+
+
+# ------------------------------------------------------------------ 8-bit integers
+
+@dataclass
+class I8Layer:
+    """A layer in 8-bit integers (serq_calibrate_i8): host numpy arrays or,
+    after ``to``, device tensors. ``s_hat_inv`` is what quant_act and
+    silu_mul_quant_act (a_bits=8) take; linear_i8 does not use it."""
+
+    K: int
+    N: int
+    s_hat_inv: "object"     # K float32
+    Wq: "object"            # N x K int8
+    sw: "object"            # N float32
+
+    def to(self, device="cuda") -> "I8Layer":
+        import torch
+        t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(device)  # noqa: E731
+        return I8Layer(K=self.K, N=self.N, s_hat_inv=t(self.s_hat_inv), Wq=t(self.Wq), sw=t(self.sw))
+
+
+def calibrate_i8(W, act_absmax=None, *, alpha: float = 0.5, w_dtype: str | None = None) -> I8Layer:
+    """Offline calibration of a layer in 8-bit integers (serq_calibrate_i8);
+    ``W`` as for ``calibrate``, ``act_absmax`` too, or None for no smoothing."""
+    W, wdt = _host_matrix(W, w_dtype)
+    K, N = W.shape
+    amax = None
+    if act_absmax is not None:
+        amax = np.ascontiguousarray(act_absmax, dtype=np.float32)
+        if amax.shape != (K,):
+            raise ValueError("act_absmax must have K entries")
+    shi, Wq, sw = np.empty(K, np.float32), np.empty((N, K), np.int8), np.empty(N, np.float32)
+    check("serq_calibrate_i8", lib.serq_calibrate_i8(_ptr(W), wdt, K, N, _ptr(amax), float(alpha), _ptr(shi), _ptr(Wq), _ptr(sw)))
+    return I8Layer(K=K, N=N, s_hat_inv=shi, Wq=Wq, sw=sw)
+
+
+def linear_i8_workspace(M: int, K: int, N: int) -> int:
+    """Bytes of workspace linear_i8 needs (serq_linear_i8_workspace); -1 for
+    sizes that it does not take."""
+    return lib.serq_linear_i8_workspace(M, K, N)
+
+
+def i8_kernel_name(M: int, K: int, N: int) -> str | None:
+    """The kernel serq_linear_i8 launches for these sizes."""
+    s = lib.serq_linear_i8_kernel_name(M, K, N)
+    return s.decode() if s else None
+
+
+def linear_i8(xq, sx, layer: I8Layer, *, out_dtype=None, out=None, workspace=None, debug: bool = False):
+    """The linear in 8-bit integers (serq_linear_i8) on the current stream of
+    the layer's device: ``xq`` M x K int8 and ``sx`` M float32 (quant_act with
+    a_bits=8). A workspace is taken from torch's allocator unless given. Returns
+    Y (M x N) or, with ``debug=True``, (Y, the int32 sums)."""
+    import torch
+    K, N, Wq, sw = layer.K, layer.N, layer.Wq, layer.sw
+    dev = Wq.get_device()
+    if Wq.dtype != torch.int8 or Wq.shape != (N, K) or sw.dtype != torch.float32 or sw.shape != (N,):
+        raise ValueError("layer buffers do not match its sizes: Wq must be N x K int8 and sw N float32")
+    if xq.dim() != 2 or xq.shape[1] != K or xq.dtype != torch.int8:
+        raise ValueError(f"xq must be M x {K} int8")
+    M = xq.shape[0]
+    if sx.shape != (M,) or sx.dtype != torch.float32:
+        raise ValueError(f"sx must be ({M},) float32")
+    out_dtype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
+    if out_dtype == torch.bfloat16:
+        dt = SERQ_BF16
+    elif out_dtype == torch.float32:
+        dt = SERQ_F32
+    else:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    y = torch.empty((M, N), dtype=out_dtype, device=xq.device) if out is None else out
+    if y.shape != (M, N) or y.dtype != out_dtype:
+        raise ValueError(f"out must be a ({M}, {N}) {out_dtype} tensor")
+    for t in (xq, sx, Wq, sw, y):
+        if t.get_device() != dev or dev < 0 or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous and on one CUDA device")
+    need = lib.serq_linear_i8_workspace(M, K, N)
+    if need < 0:
+        raise ValueError("sizes that the library does not take")
+    with torch.cuda.device(dev):
+        acc = torch.empty((M, N), dtype=torch.int32, device=xq.device) if debug else None
+        size = 0
+        if need:
+            if workspace is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=xq.device)
+            size = workspace.numel() * workspace.element_size()
+            if workspace.get_device() != dev or not workspace.is_contiguous() or size < need:
+                raise ValueError(f"workspace must be a contiguous CUDA tensor of {need} bytes or more on the layer's device")
+        status = lib.serq_linear_i8(xq.data_ptr(), sx.data_ptr(), Wq.data_ptr(), sw.data_ptr(), M, K, N, y.data_ptr(), dt,
+                                    acc.data_ptr() if debug else None, workspace.data_ptr() if need else None, size, _stream())
+    if status:
+        check("serq_linear_i8", status)
+    return (y, acc) if debug else y

@@ -25,7 +25,8 @@ EXPORTS = ("serq_strerror", "serq_abi_version", "serq_calibrate", "serq_calibrat
            "serq_rope_table", "serq_rope_append", "serq_attn_prefill", "serq_attn_prefill_workspace",
            "serq_attn_decode", "serq_attn_decode_workspace",
            "serq_rope_append_axes", "serq_rope_append_f8", "serq_attn_prefill_f8", "serq_attn_prefill_f8_workspace",
-           "serq_attn_decode_f8", "serq_attn_decode_f8_workspace")
+           "serq_attn_decode_f8", "serq_attn_decode_f8_workspace",
+           "serq_calibrate_i8", "serq_linear_i8", "serq_linear_i8_workspace", "serq_linear_i8_kernel_name")
 
 
 class SerqError(RuntimeError):
@@ -116,6 +117,14 @@ def _load() -> ctypes.CDLL:
     lib.serq_attn_decode_f8.restype = ip
     lib.serq_attn_decode_f8_workspace.argtypes = [i32, ip, ip, ip, ip, ip, ip]
     lib.serq_attn_decode_f8_workspace.restype = i64
+    lib.serq_calibrate_i8.argtypes = [vp, i32, ip, ip, vp, fp, vp, vp, vp]
+    lib.serq_calibrate_i8.restype = ip
+    lib.serq_linear_i8.argtypes = [vp, vp, vp, vp, ip, ip, ip, vp, i32, vp, vp, i64, vp]
+    lib.serq_linear_i8.restype = ip
+    lib.serq_linear_i8_workspace.argtypes = [ip, ip, ip]
+    lib.serq_linear_i8_workspace.restype = i64
+    lib.serq_linear_i8_kernel_name.argtypes = [ip, ip, ip]
+    lib.serq_linear_i8_kernel_name.restype = ctypes.c_char_p
     return lib
 
 

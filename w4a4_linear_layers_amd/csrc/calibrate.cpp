@@ -204,6 +204,50 @@ extern "C" int serq_calibrate(const void* W, serq_dtype w_dtype, int K, int N,
   return SERQ_OK;
 }
 
+namespace {
+
+// Output columns [n0, n1) of the layer in 8 bits, rows in their own order.
+void calibrate_i8_columns(const WeightView& W, int K, const float* s, int n0, int n1, int8_t* Wq, float* sw) {
+  const int nb = n1 - n0;
+  if (nb <= 0) return;
+  std::vector<float> cmax(nb, 0.0f);
+  for (int j = 0; j < K; ++j)
+    for (int c = 0; c < nb; ++c) cmax[c] = std::max(cmax[c], std::fabs(s[j] * W.at(j, n0 + c)));
+  std::vector<Quantizer> q;
+  q.reserve(nb);
+  for (int c = 0; c < nb; ++c) {
+    q.emplace_back(cmax[c], 127.0f);
+    sw[n0 + c] = q[c].scale;
+  }
+  for (int j = 0; j < K; ++j)
+    for (int c = 0; c < nb; ++c)
+      Wq[static_cast<size_t>(n0 + c) * K + j] = static_cast<int8_t>(q[c].code(s[j] * W.at(j, n0 + c), -127, 127));
+}
+
+}  // namespace
+
+extern "C" int serq_calibrate_i8(const void* W, serq_dtype w_dtype, int K, int N, const float* act_absmax, float alpha,
+                                 float* s_hat_inv, int8_t* Wq, float* sw) {
+  if (!W || !s_hat_inv || !Wq || !sw) return SERQ_EINVAL;
+  if (w_dtype != SERQ_F32 && w_dtype != SERQ_BF16) return SERQ_EINVAL;
+  if (K <= 0 || N <= 0 || !(alpha >= 0.0f && alpha <= 1.0f)) return SERQ_EINVAL;
+  const WeightView wv{W, w_dtype, N};
+  std::vector<float> s(K, 1.0f);
+  std::fill(s_hat_inv, s_hat_inv + K, 1.0f);
+  if (act_absmax) smoothing_factors(wv, K, N, act_absmax, alpha, s.data(), s_hat_inv);
+  const int T = worker_count(N);
+  const int per = (N + T - 1) / T;
+  std::vector<std::thread> pool;
+  for (int t = 1; t < T; ++t) {
+    const int n0 = t * per, n1 = std::min(N, n0 + per);
+    if (n0 >= n1) break;
+    pool.emplace_back(calibrate_i8_columns, std::cref(wv), K, s.data(), n0, n1, Wq, sw);
+  }
+  calibrate_i8_columns(wv, K, s.data(), 0, std::min(N, per), Wq, sw);
+  for (auto& th : pool) th.join();
+  return SERQ_OK;
+}
+
 extern "C" int serq_permute_outputs(const int32_t* perm_next, int K, int N, int r,
                                     uint8_t* Wq, float* sw, uint8_t* Rq, float* sr) {
   if (!perm_next || !Wq || !sw) return SERQ_EINVAL;

@@ -1,0 +1,543 @@
+// The linear in 8-bit integers for gfx950:
+//     Y[m, n] = sx[m] * (sw[n] * sum_k Xq[m, k] Wq[n, k]),
+// exact int32 sums on v_mfma_i32_*_i8, whose operands are the bytes as they are
+// stored. Three kernels: few tokens stream the weights from HBM straight into
+// registers; prompts take tiles of 256 x 256, or of 128 x 128 where those would
+// leave compute units idle, from LDS; rows that are no whole 16 bytes take one
+// lane an output.
+//
+// The matrix instructions take weights as their first operand, so a lane holds
+// four consecutive channels of one token at a time, which the epilogue scales
+// and stores as one vector.
+
+#include "serq_i8.h"
+
+#include <type_traits>
+#include <utility>
+
+namespace serq {
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v16i __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+#define SERQ_INLINE __attribute__((always_inline))
+
+constexpr int kKTile = 64;          // bytes of a row in a k-tile
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 p = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
+  return __builtin_bit_cast(uint32_t, p);
+}
+
+// Outputs of token m, channels n .. n + 3 (those below N).
+__device__ __forceinline__ void store4(const I8Args& a, v4i acc, int m, int n, float sx, const float* sw) {
+  const int64_t at = static_cast<int64_t>(m) * a.N + n;
+  const bool whole = n + 3 < a.N && (a.N & 3) == 0;
+  if (a.dbg) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.N) a.dbg[at + i] = acc[i];
+  }
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = sx * (sw[i] * static_cast<float>(acc[i]));
+  if (a.y_bf16) {
+    __bf16* out = static_cast<__bf16*>(a.Y) + at;
+    if (whole) {
+      *reinterpret_cast<u32x2*>(out) = u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < a.N) out[i] = static_cast<__bf16>(y[i]);
+    }
+  } else {
+    float* out = static_cast<float*>(a.Y) + at;
+    if (whole) {
+      *reinterpret_cast<f32x4*>(out) = f32x4{y[0], y[1], y[2], y[3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < a.N) out[i] = y[i];
+    }
+  }
+}
+
+__device__ __forceinline__ void load_scales(const I8Args& a, int n, float (&sw)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sw[i] = a.sw[n + i < a.N ? n + i : a.N - 1];
+}
+
+// ---------------------------------------------------------------- few tokens
+
+// One workgroup: RT tiles of 16 weight rows, all tokens (NT tiles of 16), its
+// eight waves taking chunks of 256 bytes of K in turn; their sums meet in LDS.
+// Lane (row or token l = lane % 16, g = lane / 16) of a step holds bytes 64 s +
+// 16 g .. + 15 of the chunk of its row for v_mfma_i32_16x16x64_i8, whichever
+// order of k that makes being the same on both sides. Weights pass once, so
+// the kernel is bound by HBM; the tokens' rows come from L2, a workgroup's
+// whole K of them for RT tiles of weights.
+constexpr int kStreamWaves = 8, kChunk = 256;
+
+template <int RT, int NT>
+__global__ __launch_bounds__(64 * kStreamWaves) void i8_stream_kernel(I8Args a) {
+  __shared__ v4i red[kStreamWaves][RT * NT][64];
+  const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * (16 * RT);
+  const int8_t* w[RT];
+  const int8_t* x[NT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int row = n0 + 16 * r + l;
+    w[r] = a.Wq + static_cast<int64_t>(row < a.N ? row : a.N - 1) * a.K;
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int row = 16 * t + l;
+    x[t] = a.Xq + static_cast<int64_t>(row < a.M ? row : a.M - 1) * a.K;
+  }
+  v4i acc[RT][NT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[r][t] = v4i{0, 0, 0, 0};
+  const int whole = a.K / kChunk;
+  for (int c = wave; c < whole; c += kStreamWaves) {
+    const int k0 = c * kChunk + 16 * g;
+    v4i wv[RT][4], xv[NT][4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) wv[r][s] = *reinterpret_cast<const v4i*>(w[r] + k0 + 64 * s);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) xv[t][s] = *reinterpret_cast<const v4i*>(x[t] + k0 + 64 * s);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[r][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[r][s], xv[t][s], acc[r][t], 0, 0, 0);
+  }
+  if (wave == whole % kStreamWaves) {           // what is left of K, 16 bytes a lane at a time
+    for (int k = whole * kChunk; k < a.K; k += 64) {
+      const bool in = k + 16 * g < a.K;
+      const int at = in ? k + 16 * g : 0;
+      v4i xv[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        xv[t] = *reinterpret_cast<const v4i*>(x[t] + at);
+        if (!in) xv[t] = v4i{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const v4i wv = *reinterpret_cast<const v4i*>(w[r] + at);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[r][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv, xv[t], acc[r][t], 0, 0, 0);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) red[wave][r * NT + t][lane] = acc[r][t];
+  __syncthreads();
+  for (int b = wave; b < RT * NT; b += kStreamWaves) {
+    v4i sum = red[0][b][lane];
+#pragma unroll
+    for (int i = 1; i < kStreamWaves; ++i) sum += red[i][b][lane];
+    const int m = 16 * (b % NT) + l, n = n0 + 16 * (b / NT) + 4 * g;
+    if (m < a.M && n < a.N) {
+      float sw[4];
+      load_scales(a, n, sw);
+      store4(a, sum, m, n, a.sx[m], sw);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- tiles
+
+// One 16-byte direct global->LDS load per lane, from sbase + voff (sbase
+// wave-uniform), into the wave's 1 KB chunk at `lds_chunk`: lane i lands at
+// + 16 i. M0 is written here and declared clobbered. Waits are explicit.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma16(const void* sbase, uint32_t voff, uint32_t lds_chunk) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(voff), "s"(sbase), "s"(lds_chunk) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+
+template <int N, typename F, int... I>
+__device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_impl<N>(f, std::make_integer_sequence<int, N>{});
+}
+
+// A 16-byte part of a 64-byte row lies at part ^ swz64(row), so that the reads
+// of one part of 16 consecutive rows fall on distinct banks.
+__device__ __forceinline__ int swz64(int row) {
+  return (((row >> 1) ^ (row >> 2)) & 1) | ((((row >> 2) ^ (row >> 3)) & 1) << 1);
+}
+
+// Workgroup -> tile. Workgroups go round-robin over the eight XCDs, each with an
+// L2 of its own: each XCD gets a contiguous range of the tile order, which walks
+// groups of eight tile rows, a column of a group after another.
+__device__ __forceinline__ void tile_coords(int b, int nb, int n_tiles, int& tn, int& tm) {
+  constexpr int kXcds = 8, kGroupM = 8;
+  const int each = nb / kXcds, more = nb % kXcds, x = b % kXcds;
+  const int at = x * each + (x < more ? x : more) + b / kXcds;
+  const int m_tiles = nb / n_tiles, per_group = kGroupM * n_tiles;
+  const int grp = at / per_group, first = grp * kGroupM;
+  const int gm = m_tiles - first < kGroupM ? m_tiles - first : kGroupM;
+  const int in = at - grp * per_group;
+  tm = first + in % gm;
+  tn = in / gm;
+}
+
+// One workgroup: a tile of 64 TN channels by 64 TM tokens, 2 x 2 waves of TN x TM
+// blocks of 32 x 32 (v_mfma_i32_32x32x32_i8), over one part of K.
+//
+// K passes in k-tiles of 64 bytes through STAGES places in LDS, by direct
+// global->LDS loads. Lane half h of a block's operands holds bytes 32 h .. + 31
+// of its row, the two matrix steps of a k-tile 16 of them each. A wave reads the
+// second step's operands during the first step's products and the next
+// k-tile's first ones during the second's; between the steps it waits for the
+// next k-tile, and after the barrier there nobody reads the present one any
+// more, whose place the load of k-tile kt + STAGES takes.
+template <int TN, int TM, int STAGES, int OCC>
+__global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles, int per) {
+  constexpr int BN = 64 * TN, BM = 64 * TM;
+  constexpr int kW = BN * kKTile, kStage = (BN + BM) * kKTile, CPW = TN + TM;
+  static_assert(CPW * (STAGES - 1) < 64, "vmcnt range");
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wave >> 1, wm = wave & 1;
+  int tile_n, tile_m;
+  tile_coords(blockIdx.x, gridDim.x, n_tiles, tile_n, tile_m);
+  const int n0 = __builtin_amdgcn_readfirstlane(tile_n * BN), m0 = __builtin_amdgcn_readfirstlane(tile_m * BM);
+  const int all = (a.K + kKTile - 1) / kKTile;
+  const int kt0 = static_cast<int>(blockIdx.y) * per;
+  const int nkt = all - kt0 < per ? all - kt0 : per;          // k-tiles of this part, at least one
+  const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
+  const int8_t* const wsrc = a.Wq + static_cast<int64_t>(n0) * a.K + static_cast<int64_t>(kt0) * kKTile;
+  const int8_t* const xsrc = a.Xq + static_cast<int64_t>(m0) * a.K + static_cast<int64_t>(kt0) * kKTile;
+  // Wave w loads chunks of 16 rows w TN .. of W and w TM .. of X; rows past the
+  // end are the last one again.
+  const int part = (lane & 3) ^ swz64(lane >> 2);
+  uint32_t woff[TN], xoff[TM];
+#pragma unroll
+  for (int i = 0; i < TN; ++i) {
+    const int row = (wave * TN + i) * 16 + (lane >> 2), last = a.N - 1 - n0;
+    woff[i] = static_cast<uint32_t>(row < last ? row : last) * a.K + part * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int row = (wave * TM + i) * 16 + (lane >> 2), last = a.M - 1 - m0;
+    xoff[i] = static_cast<uint32_t>(row < last ? row : last) * a.K + part * 16;
+  }
+  const int ragged = a.K % kKTile;               // bytes of the last k-tile, 0 for all
+  const auto issue_whole = [&](int kt, int stage) SERQ_INLINE {
+    const uint32_t to = lds_base + stage * kStage;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) dma16(wsrc + kt * kKTile, woff[i], to + (wave * TN + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) dma16(xsrc + kt * kKTile, xoff[i], to + kW + (wave * TM + i) * 1024);
+  };
+  // K's ragged end is filled with zeros. (A load that some lanes skip still
+  // counts as one: part 0 of a row is always there.)
+  const auto issue = [&](int kt, int stage) SERQ_INLINE {
+    if (ragged == 0 || kt0 + kt + 1 < all) {
+      issue_whole(kt, stage);
+      return;
+    }
+    const uint32_t to = lds_base + stage * kStage;
+    const bool in = part * 16 < ragged;
+#pragma unroll
+    for (int i = 0; i < TN + TM; ++i) {
+      const int at = i < TN ? (wave * TN + i) * 1024 : kW + (wave * TM + i - TN) * 1024;
+      if (in) dma16(i < TN ? wsrc + kt * kKTile : xsrc + kt * kKTile, i < TN ? woff[i < TN ? i : 0] : xoff[i < TN ? 0 : i - TN], to + at);
+      else *reinterpret_cast<u32x4*>(lds + stage * kStage + at + lane * 16) = u32x4{0, 0, 0, 0};
+    }
+  };
+  v16i acc[TN][TM];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) acc[i][j] = v16i{};
+  int wrd[2], xrd[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    wrd[p] = (wn * 32 * TN + l32) * kKTile + (((2 * h + p) ^ swz64(l32)) * 16);
+    xrd[p] = kW + (wm * 32 * TM + l32) * kKTile + (((2 * h + p) ^ swz64(l32)) * 16);
+  }
+  v4i fw[2][TN], fx[2][TM];
+  const auto read_part = [&](int stage, auto pc) SERQ_INLINE {
+    constexpr int p = decltype(pc)::value;
+    const uint8_t* sb = lds + stage * kStage;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) fw[p][i] = *reinterpret_cast<const v4i*>(sb + wrd[p] + i * 32 * kKTile);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) fx[p][j] = *reinterpret_cast<const v4i*>(sb + xrd[p] + j * 32 * kKTile);
+  };
+  const auto products = [&](auto pc) SERQ_INLINE {
+    constexpr int p = decltype(pc)::value;
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[p][i], fx[p][j], acc[i][j], 0, 0, 0);
+  };
+  // A step: the reads of the next operands among its products.
+  const auto interleave = [&] SERQ_INLINE {
+#pragma unroll
+    for (int q = 0; q < TN + TM; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, TN * TM, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  using P0 = std::integral_constant<int, 0>;
+  using P1 = std::integral_constant<int, 1>;
+  const auto wait_tiles = [&](int n) SERQ_INLINE {            // until at most n k-tiles are under way
+    if (n >= STAGES - 2) {
+      wait_vmcnt<CPW * (STAGES - 2)>();
+      return;
+    }
+    static_for<STAGES>([&](auto kc) {
+      constexpr int k = decltype(kc)::value;
+      if (n == k) wait_vmcnt<CPW * k>();
+    });
+  };
+#pragma unroll
+  for (int st = 0; st < STAGES; ++st)
+    if (st < nkt) issue(st, st);
+  {
+    const int later = (nkt < STAGES ? nkt : STAGES) - 1;
+    if (later == STAGES - 1) wait_vmcnt<CPW * (STAGES - 1)>();
+    else wait_tiles(later);
+  }
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  asm volatile("s_barrier" ::: "memory");
+  read_part(0, P0{});
+  const auto step = [&](int kt, int stage, auto whole) SERQ_INLINE {
+    constexpr bool kWhole = decltype(whole)::value;          // kt + STAGES is there, and a whole k-tile
+    __builtin_amdgcn_sched_barrier(0);
+    read_part(stage, P1{});
+    products(P0{});
+    interleave();
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    const bool more = kWhole || kt + 1 < nkt;
+    if (more) {
+      if constexpr (kWhole) wait_vmcnt<CPW * (STAGES - 2)>();
+      else wait_tiles(nkt - 2 - kt);
+      asm volatile("s_barrier" ::: "memory");
+      if constexpr (kWhole) issue_whole(kt + STAGES, stage);
+      else if (kt + STAGES < nkt) issue(kt + STAGES, stage);
+      __builtin_amdgcn_sched_barrier(0);
+      read_part((stage + 1) % STAGES, P0{});
+    }
+    products(P1{});
+    if constexpr (kWhole) interleave();
+  };
+  int kt = 0;
+  for (; kt + 2 * STAGES < nkt; kt += STAGES)
+    static_for<STAGES>([&](auto ic) { step(kt + decltype(ic)::value, decltype(ic)::value, std::true_type{}); });
+  for (; kt < nkt; kt += STAGES)
+    static_for<STAGES>([&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+      if (kt + i < nkt) step(kt + i, i, std::false_type{});
+    });
+  wait_vmcnt<0>();
+
+  // Register e of block (i, j): channel 32 i + 8 (e / 4) + 4 h + e % 4 of token 32 j + l32.
+  if (a.partial) {
+    int32_t* out = a.partial + static_cast<int64_t>(blockIdx.y) * a.M * a.N;
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int m = m0 + (wm * TM + j) * 32 + l32;
+      if (m >= a.M) continue;
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = n0 + (wn * TN + i) * 32 + 8 * q + 4 * h;
+          int32_t* to = out + static_cast<int64_t>(m) * a.N + n;
+          const v4i x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          if (n + 3 < a.N && (a.N & 3) == 0) {
+            *reinterpret_cast<v4i*>(to) = x;
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (n + c < a.N) to[c] = x[c];
+          }
+        }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < TN; ++i) {
+    const int n = n0 + (wn * TN + i) * 32 + 4 * h;
+    float sw[4][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) load_scales(a, n + 8 * q, sw[q]);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int m = m0 + (wm * TM + j) * 32 + l32;
+      if (m >= a.M) continue;
+      const float sx = a.sx[m];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const v4i x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        if (n + 8 * q < a.N) store4(a, x, m, n + 8 * q, sx, sw[q]);
+      }
+    }
+  }
+}
+
+// The parts of K added up, four channels a lane.
+__global__ __launch_bounds__(256) void i8_join_kernel(I8Args a, int splits) {
+  const int groups = (a.N + 3) / 4;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= static_cast<int64_t>(a.M) * groups) return;
+  const int m = static_cast<int>(at / groups), n = static_cast<int>(at % groups) * 4;
+  const int64_t part = static_cast<int64_t>(a.M) * a.N;
+  const int32_t* from = a.partial + static_cast<int64_t>(m) * a.N + n;
+  v4i sum = {0, 0, 0, 0};
+  for (int s = 0; s < splits; ++s, from += part) {
+    if ((a.N & 3) == 0) {
+      sum += *reinterpret_cast<const v4i*>(from);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] += n + i < a.N ? from[i] : 0;
+    }
+  }
+  float sw[4];
+  load_scales(a, n, sw);
+  store4(a, sum, m, n, a.sx[m], sw);
+}
+
+// ---------------------------------------------------------------- any K
+
+// (a grid of any size: outputs a lane apart)
+__global__ __launch_bounds__(256) void i8_generic_kernel(I8Args a) {
+  const int64_t outputs = static_cast<int64_t>(a.M) * a.N, stride = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < outputs; at += stride) {
+    const int m = static_cast<int>(at / a.N), n = static_cast<int>(at % a.N);
+    const int8_t* x = a.Xq + static_cast<int64_t>(m) * a.K;
+    const int8_t* w = a.Wq + static_cast<int64_t>(n) * a.K;
+    int sum = 0;
+    for (int k = 0; k < a.K; ++k) sum += static_cast<int>(x[k]) * w[k];
+    if (a.dbg) a.dbg[at] = sum;
+    const float y = a.sx[m] * (a.sw[n] * static_cast<float>(sum));
+    if (a.y_bf16) static_cast<__bf16*>(a.Y)[at] = static_cast<__bf16>(y);
+    else static_cast<float*>(a.Y)[at] = y;
+  }
+}
+
+template <int TN, int TM, int STAGES, int OCC>
+hipError_t launch_tile(const I8Args& a, const I8Plan& p, hipStream_t st) {
+  constexpr int kLds = STAGES * 64 * (TN + TM) * kKTile;
+  const int n_tiles = (a.N + 64 * TN - 1) / (64 * TN);
+  const int64_t m_tiles = (a.M + 64 * TM - 1) / (64 * TM);
+  auto* kernel = &i8_tile_kernel<TN, TM, STAGES, OCC>;
+  if (kLds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (e != hipSuccess) return e;
+  }
+  kernel<<<dim3(static_cast<unsigned>(n_tiles * m_tiles), p.splits), 256, kLds, st>>>(a, n_tiles, p.per);
+  if (p.splits > 1) {
+    const int64_t lanes = static_cast<int64_t>(a.M) * ((a.N + 3) / 4);
+    i8_join_kernel<<<dim3(static_cast<unsigned>((lanes + 255) / 256)), 256, 0, st>>>(a, p.splits);
+  }
+  return hipGetLastError();
+}
+
+template <int RT, int NT>
+hipError_t launch_stream(const I8Args& a, hipStream_t st) {
+  i8_stream_kernel<RT, NT><<<dim3((a.N + 16 * RT - 1) / (16 * RT)), 64 * kStreamWaves, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+template <int RT>
+hipError_t launch_stream_tokens(const I8Args& a, int nt, hipStream_t st) {
+  switch (nt) {
+    case 1: return launch_stream<RT, 1>(a, st);
+    case 2: return launch_stream<RT, 2>(a, st);
+    case 3: return launch_stream<RT, 3>(a, st);
+    default: return launch_stream<RT, 4>(a, st);
+  }
+}
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+I8Plan plan_linear_i8(int M, int K, int N) {
+  I8Plan p{};
+  p.splits = 1;
+  const int k_tiles = static_cast<int>(ceil_div(K, kKTile));
+  p.per = k_tiles;
+  if (K % 16 != 0) {
+    p.kind = I8Kernel::kGeneric;
+    p.name = "generic";
+    return p;
+  }
+  if (M <= 64) {
+    p.kind = I8Kernel::kStream;
+    p.nt = static_cast<int>(ceil_div(M, 16));
+    p.rt = N >= 16384 ? 2 : 1;
+    p.name = "stream";
+    return p;
+  }
+  const int64_t big = ceil_div(N, 256) * ceil_div(M, 256);
+  if (big >= 224) {
+    p.kind = I8Kernel::kTile256;
+    p.name = "tile256x256";
+    return p;
+  }
+  const int64_t tiles = ceil_div(N, 128) * ceil_div(M, 128);
+  p.kind = I8Kernel::kTile128;
+  p.name = "tile128x128";
+  if (tiles < 256) {
+    int64_t s = 512 / tiles;
+    if (s > k_tiles / 8) s = k_tiles / 8;
+    if (s > 16) s = 16;
+    if (s > 1) {
+      p.per = static_cast<int>(ceil_div(k_tiles, s));
+      p.splits = static_cast<int>(ceil_div(k_tiles, p.per));
+    }
+  }
+  if (p.splits > 1) p.bytes = static_cast<int64_t>(p.splits) * M * N * 4;
+  return p;
+}
+
+hipError_t launch_linear_i8(const I8Args& a, const I8Plan& p, hipStream_t st) {
+  switch (p.kind) {
+    case I8Kernel::kStream:
+      return p.rt == 2 ? launch_stream_tokens<2>(a, p.nt, st) : launch_stream_tokens<1>(a, p.nt, st);
+    case I8Kernel::kTile256: return launch_tile<4, 4, 4, 1>(a, p, st);
+    case I8Kernel::kTile128: return launch_tile<2, 2, 4, 2>(a, p, st);
+    default: break;
+  }
+  const int64_t blocks = ceil_div(static_cast<int64_t>(a.M) * a.N, 256);
+  i8_generic_kernel<<<dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)), 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace serq
