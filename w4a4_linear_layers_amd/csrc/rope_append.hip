@@ -8,6 +8,9 @@
 // HBM, 4.5 TB/s; 35 us with the inputs in the last-level cache) and by latency
 // for single tokens (one token 2.4 us, about a launch).
 
+#include <type_traits>
+#include <utility>
+
 #include "serq_attn.h"
 
 namespace serq {
@@ -15,6 +18,7 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 
@@ -358,6 +362,18 @@ __device__ __forceinline__ int exponent_for(uint32_t top) {
 }
 __device__ __forceinline__ float two_to(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
+// 1 / sqrt(x) for positive x, by two Newton steps from the instruction's 2^-26 or
+// so (a square root and a division take five times the instructions).
+__device__ __forceinline__ double inverse_root64(double x) {
+  double y = __builtin_amdgcn_rsq(x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const double e = __builtin_fma(-x * y, y, 1.0);
+    y = __builtin_fma(0.5 * e, y, y);
+  }
+  return x > 0.0 && x < static_cast<double>(__builtin_inff()) ? y : __builtin_amdgcn_rsq(x);
+}
+
 __device__ __forceinline__ uint32_t codes4(const float* y) {
   const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
   return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true));
@@ -369,114 +385,67 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float f) {
   return codes4(y);
 }
 
-// One window of 16 rows, one key/value head, keys or values: the runs that
-// begin in it, whose rows are among 31. A row is the L lanes of a vector
-// load; a wave's lanes also hold a row each (lane i + 1: row i) for what is
-// known of rows: their slots, runs and maxima.
+// Sum, and maximum, over the aligned groups of L lanes.
+template <int L, typename X, typename F>
+__device__ __forceinline__ X over_lanes(X v, F&& f) {
+  static_assert(L == 8 || L == 16 || L == 32, "lanes of a head");
+  const auto moved = [](X x, auto ctrl) {
+    constexpr int C = decltype(ctrl)::value;
+    constexpr int N = sizeof(X) / 4;
+    struct Words { int w[N]; } a = __builtin_bit_cast(Words, x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) a.w[i] = __builtin_amdgcn_update_dpp(0, a.w[i], C, 0xf, 0xf, true);
+    return __builtin_bit_cast(X, a);
+  };
+  v = f(v, moved(v, std::integral_constant<int, 0xB1>{}));          // lane ^ 1, lane ^ 2
+  v = f(v, moved(v, std::integral_constant<int, 0x4E>{}));
+  v = f(v, moved(v, std::integral_constant<int, 0x141>{}));         // the other four of eight, the other eight of sixteen
+  if constexpr (L >= 16) v = f(v, moved(v, std::integral_constant<int, 0x140>{}));
+  if constexpr (L == 32) v = f(v, __shfl_xor(v, 16, 32));
+  return v;
+}
+
+// One window of 16 rows, HB * SUB key/value heads from h0 on, keys or values: the
+// runs that begin in the window, whose rows are among 31. A pass is RP rows of
+// L lanes each, for SUB heads side by side; what depends on the row alone
+// serves its HB heads. Which rows go together is found by each wave from the
+// slots (lane i + 1: row i); the rows' maxima and slots meet in LDS, where the
+// lanes of a row read those of its run. Few runs reach past their window:
+// their later rows are computed twice, for the maximum and to be stored,
+// instead of kept.
 // VEC: as for the vector path above; otherwise every value and its partner are
 // loaded one by one.
-template <typename T, int D, bool INTER, bool NORM, bool VEC>
-__device__ __forceinline__ void store_codes(const RopeArgs& a, int window, int kvh, bool value) {
+template <typename T, int D, bool INTER, bool NORM, bool VEC, int HB, bool value>
+__device__ __forceinline__ void store_codes(const RopeArgs& a, int window, int h0) {
   using E = Elem<T>;
-  constexpr int V = E::kVec, L = D / V, GROUPS = kThreads / L, PASSES = GROUPS >= 32 ? 1 : 32 / GROUPS;
-  __shared__ uint32_t tops[PASSES * GROUPS];
-  const int wl = threadIdx.x & 63, mine_row = wl - 1;
-  const int lane = threadIdx.x % L, group = threadIdx.x / L, d0 = lane * V;
+  constexpr int V = E::kVec, L = D / V, RP = kThreads / L < 16 ? kThreads / L : 16, SUB = kThreads / (L * RP), EARLY = 16 / RP;
+  // bf16 values stay as they are: their codes come from pairs of bf16
+  constexpr bool kPairs = value && VEC && V == 8;
+  __shared__ uint32_t tops[HB * SUB][32];
+  __shared__ int slots[32];
+  const int wl = threadIdx.x & 63;
+  const int lane = threadIdx.x % L, group = threadIdx.x / L % RP, sub = threadIdx.x / (L * RP), d0 = lane * V;
   const int row0 = 16 * window;
-  // the rows' slots and runs
-  int slot = -1;
-  if (wl <= 32 && row0 + mine_row >= 0 && row0 + mine_row < a.M) {
-    slot = a.slot[row0 + mine_row];
-    if (slot < 0 || (slot >> a.page_shift) >= a.n_pages || !place_of<true>(a, row0 + mine_row).ok) slot = -1;
-  }
-  const int before = __shfl_up(slot, 1, 64);
-  const bool next = wl > 0 && slot >= 0 && before >= 0 && slot >> 4 == before >> 4;
-  const uint64_t joined = __ballot(next) >> 1;                        // bit i: row i continues row i - 1
-  const uint64_t starts = __ballot(slot >= 0 && !next) >> 1;
-  const uint32_t upto = mine_row < 0 ? 0 : static_cast<uint32_t>(starts) & ((2u << (mine_row & 31)) - 1u);
-  const int start = upto ? 31 - __builtin_clz(upto) : 16;
-  const bool own = wl >= 1 && wl <= 32 && slot >= 0 && start < 16;
-  const uint64_t rows = __ballot(own) >> 1;
-  if (rows == 0) return;
-  const int end = own ? mine_row + __builtin_ctzll(~(joined >> wl)) : 0;          // (bit 63 of a shifted mask is 0)
-  uint8_t* scales = value ? a.v_scale : a.k_scale;
-  const int per = a.page_shift - 4;                                               // blocks of a page: 1 << per
-  const int64_t at_scale =
-      own ? (((static_cast<int64_t>(slot >> a.page_shift) * a.Hkv + kvh) << per) + ((slot >> 4) & ((1 << per) - 1))) : 0;
-  int old = kLeast;
-  if (own && mine_row == start) {
-    old = static_cast<int>(scales[at_scale]) - 127;
-    old = old < kLeast ? kLeast : old > kMost ? kMost : old;
-  }
   const bool norm = NORM && !value && a.k_norm;
   const bool turned = !value && d0 < a.rot;
   const int half = a.rot / 2;
-  float y[PASSES][V];
+  const auto partner = [&](int d) { return d >= a.rot ? d : INTER ? d ^ 1 : d < half ? d + half : d - half; };
+
+  // y = r (x (w A) + z (w' B)), z and w' the partner's: w A and w' B are exact.
+  struct Factors { double wa[V], wb[V]; };
+  const auto load_row = [&](int t, bool in, Factors& f) __attribute__((always_inline)) {
+    float A[V], B[V], wx[V], wz[V];
 #pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
-    const int i = group + GROUPS * p, t = row0 + i;
-    const bool in = i < 32 && (rows >> i & 1) != 0;
-#pragma unroll
-    for (int j = 0; j < V; ++j) y[p][j] = 0.0f;
-    const T* src = static_cast<const T*>(a.QKV) + (in ? t : row0) * a.ld +
-                   static_cast<int64_t>(a.Hq + (value ? a.Hkv : 0) + kvh) * D;
-    if (in) {
-      if constexpr (VEC) {
-        E::unpack(*reinterpret_cast<const u32x4*>(src + d0), y[p]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) y[p][j] = E::load(src + d0 + j);
-      }
-    }
-    if (!value) {
-      double x[V], z[V];
-      if constexpr (NORM) {
-        double ss = 0.0;
-#pragma unroll
-        for (int j = 0; j < V; ++j) ss += static_cast<double>(y[p][j]) * y[p][j];
-#pragma unroll
-        for (int off = L / 2; off > 0; off >>= 1) ss += __shfl_xor(ss, off, L);
-        const double r = norm ? 1.0 / sqrt(ss * (1.0 / D) + static_cast<double>(a.eps)) : 1.0;
-#pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = y[p][j] * r * (norm ? static_cast<double>(a.k_norm[d0 + j]) : 1.0);
-        if constexpr (!VEC) {                 // the partner, normed alike
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const int d = d0 + j, m = d >= a.rot ? d : INTER ? d ^ 1 : d < half ? d + half : d - half;
-            z[j] = in ? static_cast<double>(E::load(src + m)) * r * (norm ? static_cast<double>(a.k_norm[m]) : 1.0) : 0.0;
-          }
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = y[p][j];
-        if constexpr (!VEC) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const int d = d0 + j, m = d >= a.rot ? d : INTER ? d ^ 1 : d < half ? d + half : d - half;
-            z[j] = in ? E::load(src + m) : 0.0f;
-          }
-        }
-      }
-      if constexpr (VEC) {
-        if constexpr (INTER) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) z[j] = x[j ^ 1];
-        } else {
-          const int step = half / V, mate = !turned ? lane : d0 < half ? lane + step : lane - step;
-#pragma unroll
-          for (int j = 0; j < V; ++j) z[j] = __shfl(x[j], mate, L);
-        }
-      }
-      if (in && turned) {
-        const Place at = place_of<true>(a, t);
-        float A[V], B[V];
+    for (int j = 0; j < V; ++j) A[j] = wx[j] = wz[j] = 1.0f, B[j] = 0.0f;
+    if (in && turned) {
+      const Place at = place_of<true>(a, t);
+      if (at.ok) {
         if constexpr (VEC) {
           load_factors<V, INTER, true>(a, at, d0, A, B);
         } else {
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             const int d = d0 + j;
-            A[j] = 1.0f, B[j] = 0.0f;
             if (d < a.rot) {
               const bool second = INTER ? (d & 1) : d >= half;
               const int pair = INTER ? d / 2 : second ? d - half : d;
@@ -486,102 +455,293 @@ __device__ __forceinline__ void store_codes(const RopeArgs& a, int window, int k
             }
           }
         }
+      }
+    }
+    if (norm) {
+      load_floats<V>(a.k_norm + d0, wx);
+      if constexpr (VEC) {
+        if constexpr (INTER) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = x[j] * A[j] + z[j] * B[j];
+          for (int j = 0; j < V; ++j) wz[j] = wx[j ^ 1];
+        } else {
+          load_floats<V>(a.k_norm + partner(d0), wz);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) wz[j] = a.k_norm[partner(d0 + j)];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      f.wa[j] = static_cast<double>(wx[j]) * A[j];
+      f.wb[j] = static_cast<double>(wz[j]) * B[j];
+    }
+  };
+  struct Raw {
+    u32x4 w;                    // kPairs
+    float y[V], z[V];
+  };
+  const auto load_raw = [&](int t, int h, bool in, Raw& r) __attribute__((always_inline)) {
+    r.w = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < V; ++j) r.y[j] = r.z[j] = 0.0f;
+    if (!in) return;
+    const T* src = static_cast<const T*>(a.QKV) + t * a.ld + static_cast<int64_t>(a.Hq + (value ? a.Hkv : 0) + h) * D;
+    if constexpr (kPairs) {
+      r.w = *reinterpret_cast<const u32x4*>(src + d0);
+    } else if constexpr (VEC) {
+      E::unpack(*reinterpret_cast<const u32x4*>(src + d0), r.y);
+      if (!INTER && turned) E::unpack(*reinterpret_cast<const u32x4*>(src + partner(d0)), r.z);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        r.y[j] = E::load(src + d0 + j);
+        if (turned) r.z[j] = E::load(src + partner(d0 + j));
+      }
+    }
+  };
+  // The keys themselves in r.y (all lanes take part).
+  const auto finish = [&](Raw& r, const Factors& f) __attribute__((always_inline)) {
+    if constexpr (!value) {
+      double x[V], s = 1.0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[j] = r.y[j];
+      if constexpr (NORM) {
+        double ss = 0.0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) ss = __builtin_fma(x[j], x[j], ss);
+        ss = over_lanes<L>(ss, [](double u, double v) { return u + v; });
+        if (norm) s = inverse_root64(ss * (1.0 / D) + static_cast<double>(a.eps));
       }
 #pragma unroll
-      for (int j = 0; j < V; ++j) y[p][j] = static_cast<float>(x[j]);
+      for (int j = 0; j < V; ++j) {
+        double u = x[j] * f.wa[j];
+        if (VEC ? turned : d0 + j < a.rot) u = __builtin_fma(INTER && VEC ? x[j ^ 1] : static_cast<double>(r.z[j]), f.wb[j], u);
+        r.y[j] = static_cast<float>(NORM ? u * s : u);
+      }
     }
+  };
+  // Largest finite magnitude of a row, as the bits of an fp32 number. (NaN and
+  // infinities, which become NaN codes, make the lane look at each value.)
+  const auto top_of = [&](const Raw& r) __attribute__((always_inline)) {
     uint32_t top = 0;
+    if constexpr (kPairs) {
+      typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+      const auto mag = [&](int j) { return __builtin_bit_cast(u16x2, r.w[j] & 0x7FFF7FFFu); };
+      const u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(mag(0), mag(1)), __builtin_elementwise_max(mag(2), mag(3)));
+      top = static_cast<uint32_t>(m[0] > m[1] ? m[0] : m[1]) << 16;
+      if (top >= 0x7F800000u) {
+        top = 0;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const uint32_t b = __float_as_uint(y[p][j]) & 0x7FFFFFFFu;
-      top = b < 0x7F800000u && b > top ? b : top;                     // (NaN and infinities become NaN codes)
-    }
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t b = (r.w[j / 2] >> (16 * (j & 1)) & 0x7FFFu) << 16;
+          top = b < 0x7F800000u && b > top ? b : top;
+        }
+      }
+    } else {
 #pragma unroll
-    for (int off = L / 2; off > 0; off >>= 1) {
-      const uint32_t o = __shfl_xor(top, off, L);
-      top = o > top ? o : top;
+      for (int j = 0; j < V; ++j) {
+        const uint32_t b = __float_as_uint(r.y[j]) & 0x7FFFFFFFu;
+        top = b > top ? b : top;
+      }
+      if (top >= 0x7F800000u) {
+        top = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const uint32_t b = __float_as_uint(r.y[j]) & 0x7FFFFFFFu;
+          top = b < 0x7F800000u && b > top ? b : top;
+        }
+      }
     }
-    if (lane == 0) tops[i] = in ? top : 0;
+    return over_lanes<L>(top, [](uint32_t u, uint32_t v) { return u > v ? u : v; });
+  };
+  const auto head = [&](int k) { return h0 + k * SUB + sub; };
+
+  // The window's own rows are loaded before it is known which of them are stored.
+  Raw raw[EARLY][HB];
+  Factors fac[EARLY];
+#pragma unroll
+  for (int p = 0; p < EARLY; ++p) {
+    const int t = row0 + group + RP * p;
+#pragma unroll
+    for (int k = 0; k < HB; ++k) load_raw(t, head(k), t < a.M && head(k) < a.Hkv, raw[p][k]);
+    if constexpr (!value) load_row(t, t < a.M, fac[p]);
   }
+  // the rows' slots and runs
+  int slot = -1;
+  if (wl <= 32 && row0 + wl - 1 >= 0 && row0 + wl - 1 < a.M) {
+    const int s = a.slot[row0 + wl - 1];
+    const bool ok = place_of<true>(a, row0 + wl - 1).ok;
+    slot = ok && s >= 0 && (s >> a.page_shift) < a.n_pages ? s : -1;
+  }
+  const int before = __shfl_up(slot, 1, 64);
+  const bool next = wl > 0 && wl <= 32 && slot >= 0 && before >= 0 && slot >> 4 == before >> 4;
+  const uint64_t joined = __ballot(next) >> 1;                        // bit i: row i continues row i - 1
+  const uint32_t starts = static_cast<uint32_t>(__ballot(slot >= 0 && !next) >> 1);
+  // the run that row i is of: its first and last row
+  const auto start_of = [&](int i) {
+    const uint32_t upto = starts & ((2u << i) - 1u);
+    return upto ? 31 - __builtin_clz(upto) : 16;
+  };
+  const auto end_of = [&](int i) { return i + __builtin_ctzll(~(joined >> (i + 1))); };
+  const uint32_t rows = static_cast<uint32_t>(__ballot(wl > 0 && slot >= 0 && start_of((wl - 1) & 31) < 16) >> 1);
+  if (rows == 0) return;
+  if (threadIdx.x - 1u < 32u) slots[threadIdx.x - 1] = slot;
+  const int past = rows >> 16 ? 32 - __builtin_clz(rows) : 16;         // rows past the window to look at: 16 .. past - 1
+#pragma unroll
+  for (int p = 0; p < EARLY; ++p)
+#pragma unroll
+    for (int k = 0; k < HB; ++k) {
+      const int i = group + RP * p;
+      finish(raw[p][k], fac[p]);
+      const uint32_t top = top_of(raw[p][k]);
+      if (lane == 0) tops[k * SUB + sub][i] = (rows >> i & 1) ? top : 0;
+    }
+  const auto later = [&](auto&& use) __attribute__((always_inline)) {  // use(row, head's number, values)
+#pragma unroll 1
+    for (int i0 = 16; i0 < past; i0 += RP) {
+      const int i = i0 + group;
+      const bool in = (rows >> i & 1) != 0;
+      Factors f;
+      if constexpr (!value) load_row(row0 + i, in, f);
+#pragma unroll
+      for (int k = 0; k < HB; ++k) {
+        Raw r;
+        load_raw(row0 + i, head(k), in && head(k) < a.Hkv, r);
+        finish(r, f);
+        use(i, k, r);
+      }
+    }
+  };
+  later([&](int i, int k, const Raw& r) __attribute__((always_inline)) {
+    const uint32_t top = top_of(r);
+    if (lane == 0) tops[k * SUB + sub][i] = (rows >> i & 1) ? top : 0;
+  });
   __syncthreads();
-  // the runs' maxima, exponents and blocks
-  uint32_t top = own ? tops[mine_row] : 0, tokens = own ? 1u << (slot & 15) : 0;
+
+  uint8_t* const scales = value ? a.v_scale : a.k_scale;
+  uint8_t* const cache = static_cast<uint8_t*>(value ? a.Vc : a.Kc);
+  const int per = a.page_shift - 4;                                    // blocks of a page: 1 << per
+  constexpr auto most = [](uint32_t u, uint32_t v) { return u > v ? u : v; };
+  // Row i's codes of head k; the run's first row writes the scale and takes care
+  // of the block's other codes. (All lanes take part.)
+  const auto store = [&](int i, int k, const Raw& r) __attribute__((always_inline)) {
+    const bool mine = (rows >> i & 1) != 0;
+    const int start = mine ? start_of(i) : i, end = mine ? end_of(i) : i;
+    // the run's tokens (a bit each) and maximum: a row of it a lane
+    uint32_t tokens = 0, top = 0;
 #pragma unroll
-  for (int off = 1; off < 16; off <<= 1) {
-    const uint32_t o = __shfl_up(top, off, 64), s = __shfl_up(tokens, off, 64);
-    if (own && mine_row - off >= start) {
-      top = o > top ? o : top;
-      tokens |= s;
+    for (int n = 0; n < 16; n += (L < 16 ? L : 16)) {
+      const int j = start + (lane & 15) + n;
+      if (j <= end) {
+        tokens |= 1u << (slots[j] & 15);
+        top = most(top, tops[k * SUB + sub][j]);
+      }
     }
-  }
-  top = __shfl(top, end + 1, 64);
-  tokens = __shfl(tokens, end + 1, 64);                               // of the block: those of this run
-  const int was = __shfl(old, (own ? start : 0) + 1, 64);
-  const int now = exponent_for(top);
-  const int e = (tokens & 1) == 0 && was > now ? was : now;             // (token 0 begins the block anew)
-  if (threadIdx.x < 64 && own && mine_row == start) scales[at_scale] = static_cast<uint8_t>(e + 127);
-  uint8_t* cache = static_cast<uint8_t*>(value ? a.Vc : a.Kc);
-#pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
-    const int i = group + GROUPS * p;
-    const int li = (i < 32 ? i : 31) + 1;                             // (all lanes take part in the shuffles)
-    const int se = __shfl(e, li, 64), sw = __shfl(was, li, 64), ss = __shfl(slot, li, 64), st = __shfl(start, li, 64);
-    const uint32_t tk = __shfl(tokens, li, 64);
-    if (!(i < 32 && (rows >> i & 1) != 0)) continue;
-    const float f = two_to(-se);
-    const int64_t at = slot_base(a, ss, true) + (static_cast<int64_t>(kvh) << a.page_shift) * D + d0;
-    float z[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const bool finite = (__float_as_uint(y[p][j]) & 0x7F800000u) != 0x7F800000u;
-      z[j] = finite ? y[p][j] * f : __builtin_nanf("");
+    tokens = over_lanes<L>(tokens, [](uint32_t u, uint32_t v) { return u | v; });
+    top = over_lanes<L>(top, most);
+    if (!mine || head(k) >= a.Hkv) return;
+    const int s = slots[i];
+    const int64_t block = ((static_cast<int64_t>(s >> a.page_shift) * a.Hkv + head(k)) << per) + ((s >> 4) & ((1 << per) - 1));
+    int e = exponent_for(top), was = kLeast;
+    if ((tokens & 1) == 0) {                                          // (token 0 begins the block anew)
+      was = static_cast<int>(scales[block]) - 127;
+      was = was < kLeast ? kLeast : was > kMost ? kMost : was;
+      e = e > was ? e : was;
     }
+    uint8_t* const to = cache + block * (16 * D) + d0;                // the lane's codes of the block's tokens, D apart
     uint32_t w[V / 4];
+    if constexpr (kPairs) {
+      typedef short s16x2 __attribute__((ext_vector_type(2)));
+      u32x4 x = r.w;
+      if (__any((x[0] & 0x7F80u) == 0x7F80u || (x[0] & 0x7F800000u) == 0x7F800000u || (x[1] & 0x7F80u) == 0x7F80u ||
+                (x[1] & 0x7F800000u) == 0x7F800000u || (x[2] & 0x7F80u) == 0x7F80u || (x[2] & 0x7F800000u) == 0x7F800000u ||
+                (x[3] & 0x7F80u) == 0x7F80u || (x[3] & 0x7F800000u) == 0x7F800000u)) {
 #pragma unroll
-    for (int j = 0; j < V / 4; ++j) w[j] = codes4(z + 4 * j);
-    if constexpr (V == 8) *reinterpret_cast<u32x2*>(cache + at) = u32x2{w[0], w[1]};
-    else *reinterpret_cast<uint32_t*>(cache + at) = w[0];
-    if (i == st && (tk & 1) == 0 && se > sw) {                              // the block's other tokens, by 2^(old - new)
-      const float g = two_to(sw - se < -30 ? -30 : sw - se);
-      uint8_t* block = cache + at - static_cast<int64_t>(ss & 15) * D;
+        for (int j = 0; j < 4; ++j) {                                 // infinities to NaN
+          if ((x[j] & 0x7F80u) == 0x7F80u) x[j] |= 0x7FFFu;
+          if ((x[j] & 0x7F800000u) == 0x7F800000u) x[j] |= 0x7FFF0000u;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t x0 = x[2 * j], x1 = x[2 * j + 1];
+        const s16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(s16x2{0, 0}, __builtin_bit_cast(bf16x2, x0), two_to(e), false);
+        w[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(lo, __builtin_bit_cast(bf16x2, x1), two_to(e), true));
+      }
+    } else {
+      const float f = two_to(-e);
+      float z[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const bool finite = (__float_as_uint(r.y[j]) & 0x7F800000u) != 0x7F800000u;
+        z[j] = finite ? r.y[j] * f : __builtin_nanf("");
+      }
+#pragma unroll
+      for (int j = 0; j < V / 4; ++j) w[j] = codes4(z + 4 * j);
+    }
+    if constexpr (V == 8) *reinterpret_cast<u32x2*>(to + (s & 15) * D) = u32x2{w[0], w[1]};
+    else *reinterpret_cast<uint32_t*>(to + (s & 15) * D) = w[0];
+    if (i != start) return;
+    if (lane == 0) scales[block] = static_cast<uint8_t>(e + 127);
+    if ((tokens & 1) == 0 && e > was) {                               // by 2^(old - new)
+      const float g = two_to(was - e < -30 ? -30 : was - e);
       uint32_t c[16][V / 4];
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if ((tk >> k & 1) == 0) {
+      for (int n = 0; n < 16; ++n)
+        if ((tokens >> n & 1) == 0) {
           if constexpr (V == 8) {
-            const u32x2 x = *reinterpret_cast<const u32x2*>(block + k * D);
-            c[k][0] = x[0], c[k][1] = x[1];
+            const u32x2 v = *reinterpret_cast<const u32x2*>(to + n * D);
+            c[n][0] = v[0], c[n][1] = v[1];
           } else {
-            c[k][0] = *reinterpret_cast<const uint32_t*>(block + k * D);
+            c[n][0] = *reinterpret_cast<const uint32_t*>(to + n * D);
           }
         }
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if ((tk >> k & 1) == 0) {
-          if constexpr (V == 8) *reinterpret_cast<u32x2*>(block + k * D) = u32x2{recode4(c[k][0], g), recode4(c[k][1], g)};
-          else *reinterpret_cast<uint32_t*>(block + k * D) = recode4(c[k][0], g);
+      for (int n = 0; n < 16; ++n)
+        if ((tokens >> n & 1) == 0) {
+          if constexpr (V == 8) *reinterpret_cast<u32x2*>(to + n * D) = u32x2{recode4(c[n][0], g), recode4(c[n][1], g)};
+          else *reinterpret_cast<uint32_t*>(to + n * D) = recode4(c[n][0], g);
         }
     }
-  }
+  };
+#pragma unroll
+  for (int p = 0; p < EARLY; ++p)
+#pragma unroll
+    for (int k = 0; k < HB; ++k) store(group + RP * p, k, raw[p][k]);
+  later(store);
 }
 
 // Workgroups for the windows' keys and values (of one window side by side),
-// then, with QUERIES, sets of query heads as above. `first`: the first token
-// of this launch, a multiple of 16.
+// then, with sets, sets of query heads as above. `first`: the first token of
+// this launch, a multiple of 16.
+template <typename T, int D>
+constexpr int heads_side_by_side() {
+  return kThreads / (D / Elem<T>::kVec) <= 16 ? 1 : kThreads / (D / Elem<T>::kVec) / 16;
+}
 template <typename T, int D, bool INTER, bool NORM, bool VEC>
 __global__ __launch_bounds__(kThreads) void rope_append_f8_kernel(RopeArgs a, int first, int tokens, int sets) {
-  const int windows = (tokens + 15) / 16;
-  const int stores = windows * 2 * a.Hkv;
+  constexpr int HB = 1, EACH = heads_side_by_side<T, D>();
+  const int windows = (tokens + 15) / 16, parts = (a.Hkv + EACH - 1) / EACH;
+  const int stores = windows * 2 * parts;
   const int b = blockIdx.x;
   if (b < stores) {
-    const int h = b % (2 * a.Hkv);
-    store_codes<T, D, INTER, NORM, VEC>(a, first / 16 + b / (2 * a.Hkv), h % a.Hkv, h >= a.Hkv);
+    const int h = b % (2 * parts);
+    const int window = first / 16 + b / (2 * parts), h0 = h % parts * EACH;
+    if (h >= parts) store_codes<T, D, false, false, VEC, HB, true>(a, window, h0);
+    else store_codes<T, D, INTER, NORM, VEC, HB, false>(a, window, h0);
   } else if constexpr (VEC) {
     const int x = b - stores;
     rope_heads<T, D, INTER, NORM, true, 1>(a, first + x / sets, x % sets, a.Hq);
   }
+}
+
+// Keys alone, or values alone: each with the registers that it needs.
+template <typename T, int D, bool INTER, bool NORM, int HB, bool VALUE>
+__global__ __launch_bounds__(kThreads) void store_f8_kernel(RopeArgs a, int first) {
+  constexpr int EACH = HB * heads_side_by_side<T, D>();
+  const int parts = (a.Hkv + EACH - 1) / EACH;
+  store_codes<T, D, INTER, NORM, true, HB, VALUE>(a, first / 16 + blockIdx.x / parts, blockIdx.x % parts * EACH);
 }
 
 // A workgroup per set of heads, or per three sets where many tokens are normed:
@@ -631,28 +791,45 @@ hipError_t launch_by_dim(const RopeArgs& a, hipStream_t st) {
   return a.D == 64 ? launch_typed<T, 64, AXES>(a, st) : launch_typed<T, 128, AXES>(a, st);
 }
 
-// Tokens [first, first + tokens) of a call onto a cache of codes.
+// Tokens [first, first + tokens) of a call onto a cache of codes: keys, values
+// and queries in one launch, or in two where many tokens make that cost little
+// and each its own registers and sets of heads gain more.
 template <typename T, int D, bool INTER, bool NORM>
 hipError_t launch_f8(const RopeArgs& a, int first, int tokens, hipStream_t st) {
-  constexpr int GROUPS = kThreads / (D / Elem<T>::kVec);
+  constexpr int GROUPS = kThreads / (D / Elem<T>::kVec), KB = 2, VB = 4;
   const int sets = (a.Hq + GROUPS - 1) / GROUPS;
-  const int64_t stores = static_cast<int64_t>((tokens + 15) / 16) * 2 * a.Hkv;
-  if (vector_path<T>(a)) {
+  const auto stores = [&](int heads) {                     // workgroups of so many heads each
+    const int64_t each = heads * heads_side_by_side<T, D>();
+    return static_cast<int64_t>((tokens + 15) / 16) * ((a.Hkv + each - 1) / each);
+  };
+  const auto queries = [&] {                               // of these tokens alone
+    RopeArgs x = a;
+    x.QKV = static_cast<const T*>(a.QKV) + first * a.ld;
+    x.Q = static_cast<T*>(a.Q) + first * a.ldq;
+    if (a.rot > 0) x.pos = a.pos + first;
+    x.slot = a.slot + first;
+    x.M = tokens;
+    x.Hkv = 0;
+    return x;
+  };
+  const bool vector = vector_path<T>(a), many = tokens >= kManyTokens;
+  if (vector && !many) {
     rope_append_f8_kernel<T, D, INTER, NORM, true>
-        <<<dim3(static_cast<unsigned>(stores + static_cast<int64_t>(tokens) * sets)), kThreads, 0, st>>>(a, first, tokens, sets);
-  } else {
-    rope_append_f8_kernel<T, D, INTER, NORM, false><<<dim3(static_cast<unsigned>(stores)), kThreads, 0, st>>>(a, first, tokens, 0);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (a.Hq > 0) {                                        // (the keys first: Q may lie in QKV's query part alone)
-      RopeArgs x = a;
-      x.QKV = static_cast<const T*>(a.QKV) + first * a.ld;
-      x.Q = static_cast<T*>(a.Q) + first * a.ldq;
-      if (a.rot > 0) x.pos = a.pos + first;
-      x.slot = a.slot + first;
-      rope_append_scalar_kernel<T, D, true><<<dim3(tokens, a.Hq), 64, 0, st>>>(x);
-    }
+        <<<dim3(static_cast<unsigned>(2 * stores(1) + static_cast<int64_t>(tokens) * sets)), kThreads, 0, st>>>(a, first, tokens, sets);
+    return hipGetLastError();
   }
+  if (vector) {
+    store_f8_kernel<T, D, INTER, NORM, KB, false><<<dim3(static_cast<unsigned>(stores(KB))), kThreads, 0, st>>>(a, first);
+    store_f8_kernel<T, D, false, false, VB, true><<<dim3(static_cast<unsigned>(stores(VB))), kThreads, 0, st>>>(a, first);
+  } else {
+    rope_append_f8_kernel<T, D, INTER, NORM, false><<<dim3(static_cast<unsigned>(2 * stores(1))), kThreads, 0, st>>>(a, first, tokens, 0);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.Hq == 0) return e;
+  const RopeArgs x = queries();                            // (the keys first: Q may lie in QKV's query part alone)
+  if (!vector) rope_append_scalar_kernel<T, D, true><<<dim3(tokens, a.Hq), 64, 0, st>>>(x);
+  else if (a.n_axes > 1) launch_vector<T, D, INTER, NORM, true>(x, st);
+  else launch_vector<T, D, INTER, NORM, false>(x, st);
   return hipGetLastError();
 }
 
