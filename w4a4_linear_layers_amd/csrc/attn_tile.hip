@@ -238,7 +238,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
   const int cr = kPer * wave + (lane >> 3), cp = lane & 7;
   uint32_t kc[kWords], vc[kWords];
   float ks = 1.0f, vs = 1.0f;
-  const auto fetch = [&](const void* cache, const uint8_t* scales, uint64_t at, uint32_t (&codes)[kWords], float& scale) {
+  uint32_t ks_word = 0, vs_word = 0;             // dwords that hold the scales, and the bits to shift them by
+  int ks_bit = 0, vs_bit = 0;
+  const auto fetch = [&](const void* cache, uint64_t at, uint32_t (&codes)[kWords]) {
     const uint8_t* p = static_cast<const uint8_t*>(cache) + at + ((lane >> 3) * D + cp * (D / 8));
     if constexpr (kWords == 4) {
       const u32x4 x = *reinterpret_cast<const u32x4*>(p);
@@ -248,10 +250,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       const u32x2 x = *reinterpret_cast<const u32x2*>(p);
       codes[0] = x[0], codes[1] = x[1];
     }
-    const uint64_t block = at / (16 * D);        // (rows of a wave lie in one block)
-    const uint32_t w = ((const __attribute__((address_space(4))) uint32_t*)scales)[block >> 2];
-    scale = __uint_as_float((w >> (8 * (static_cast<int>(block) & 3)) & 0xFFu) << 23);
   };
+  const auto fetch_scale = [&](const uint8_t* scales, uint64_t at, uint32_t& word, int& bit) {
+    const uint64_t block = at / (16 * D);        // (rows of a wave lie in one block)
+    word = ((const __attribute__((address_space(4))) uint32_t*)scales)[block >> 2];
+    bit = 8 * (static_cast<int>(block) & 3);
+  };
+  const auto to_scale = [&](uint32_t word, int bit) { return __uint_as_float((word >> bit & 0xFFu) << 23); };
   // Codes to a place: the 16-byte parts of kWords / 2 of a row.
   const auto put = [&](uint8_t* tile, int swizzle, const uint32_t (&codes)[kWords], float scale) {
 #pragma unroll
@@ -266,9 +271,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
     }
   };
   const auto put_k = [&](int at) { put(smem + at * kTile, swizzle_k<D>(cr), kc, ks); };
-  // V tile t: as for look_over, the rows past the end cleared, and noted whether
+  const auto put_v = [&](int at) { put(smem + (kRing + at) * kTile, swizzle_v<D>(cr), vc, vs); };
+  // The scales of the codes that go to their places next: K tile t + 1, V tile t.
+  // As for look_over, V's rows past the end are cleared, and it is noted whether
   // the others are finite.
-  const auto put_v = [&](int t, int at) {
+  const auto make_ready = [&](int t, int at) {
+    ks = to_scale(ks_word, ks_bit);
+    vs = to_scale(vs_word, vs_bit);
     if (from + (t + 1) * kKeys > whole) {
       const bool past = from + t * kKeys + cr >= len;
       bool odd = false;
@@ -281,7 +290,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       const int any = __any(odd);
       if (lane == 0) odd_rows[at][wave] = any;
     }
-    put(smem + (kRing + at) * kTile, swizzle_v<D>(cr), vc, vs);
   };
 
   // Read addresses. K: part 2 c + half of row n (+ 32): its swizzled place is
@@ -465,13 +473,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       if constexpr (F8) {
         // V(t) and K(t + 1) to their places, then V(t + 1) and K(t + 2) on their way
         if (j == 0) {
-          put_v(t, place_of(0));
-          fetch(a.Vc, a.v_scale, vat[0], vc, vs);
+          put_v(place_of(0));
+          fetch(a.Vc, vat[0], vc);
         } else if (j == 1) {
           put_k(place_of(1));
           place(pages, t + 2, kat);
-          fetch(a.Kc, a.k_scale, kat[0], kc, ks);
-          vat[0] = kat[0];
+          fetch(a.Kc, kat[0], kc);
         }
         return;
       }
@@ -493,7 +500,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
         finish_loads();
         barrier();
       }
-      look_up(t + (F8 ? 3 : kRing), pages);        // (a scalar load; among LDS reads it would stall them)
+      if constexpr (F8) {                          // (scalar loads; among LDS reads they would stall them)
+        fetch_scale(a.v_scale, vat[0], vs_word, vs_bit);
+        fetch_scale(a.k_scale, kat[0], ks_word, ks_bit);
+        vat[0] = kat[0];
+      }
+      look_up(t + (F8 ? 3 : kRing), pages);
     };
     const auto after_vector = [&](bool ends) {
       if (ends) {
@@ -502,6 +514,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       }
       slot = place_of(1);
       ++t;
+      if constexpr (F8) make_ready(t, slot);
     };
     int early[kRing - 1][kLoads];
     constexpr int kEarly = F8 ? 2 : kRing - 1;
@@ -520,15 +533,19 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       dma16(shuffle(qrow, r) + ((lp ^ swizzle_k<D>(r)) << 4), uniform(lds0 + qplace + 1024 * k));
     }
     if constexpr (F8) {
-      uint32_t k0[kWords];
-      float s0;
+      uint32_t k0[kWords], word;
+      int bit;
       place(early[0], 0, kat);
-      fetch(a.Kc, a.k_scale, kat[0], k0, s0);
-      fetch(a.Vc, a.v_scale, kat[0], vc, vs);
+      fetch(a.Kc, kat[0], k0);
+      fetch(a.Vc, kat[0], vc);
+      fetch_scale(a.k_scale, kat[0], word, bit);
+      fetch_scale(a.v_scale, kat[0], vs_word, vs_bit);
       place(early[1], 1, kat);
-      fetch(a.Kc, a.k_scale, kat[0], kc, ks);
+      fetch(a.Kc, kat[0], kc);
+      fetch_scale(a.k_scale, kat[0], ks_word, ks_bit);
       vat[0] = kat[0];
-      put(smem, swizzle_k<D>(cr), k0, s0);
+      put(smem, swizzle_k<D>(cr), k0, to_scale(word, bit));
+      make_ready(0, 0);
       wait_loads();                                // Q
     } else {
 #pragma unroll
