@@ -27,6 +27,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 #define SERQ_INLINE __attribute__((always_inline))
 
 constexpr int kKTile = 64;          // bytes of a row in a k-tile
+constexpr int kCUs = 256;           // compute units of an MI355X
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -164,12 +165,14 @@ __global__ __launch_bounds__(64 * kStreamWaves) void i8_stream_kernel(I8Args a) 
 
 // One 16-byte direct global->LDS load per lane, from sbase + voff (sbase
 // wave-uniform), into the wave's 1 KB chunk at `lds_chunk`: lane i lands at
-// + 16 i. M0 is written here and declared clobbered. Waits are explicit.
+// + 16 i. M0 is written here and declared clobbered. Waits are explicit; LDS
+// reads are not ordered with it, as it writes where no wave reads until the
+// barrier after the wait for it.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(const void* sbase, uint32_t voff, uint32_t lds_chunk) {
   asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
-               :: "v"(voff), "s"(sbase), "s"(lds_chunk) : "memory", "m0");
+               :: "v"(voff), "s"(sbase), "s"(lds_chunk) : "m0");
 }
 #pragma clang diagnostic pop
 
@@ -209,8 +212,18 @@ __device__ __forceinline__ void tile_coords(int b, int nb, int n_tiles, int& tn,
   tn = in / gm;
 }
 
-// One workgroup: a tile of 64 TN channels by 64 TM tokens, 2 x 2 waves of TN x TM
-// blocks of 32 x 32 (v_mfma_i32_32x32x32_i8), over one part of K.
+// One 4-byte direct global->LDS load per lane, likewise: lane i lands at + 4 i.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma4(const void* sbase, uint32_t voff, uint32_t lds_dst) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1"
+               :: "v"(voff), "s"(sbase), "s"(lds_dst) : "m0");
+}
+#pragma clang diagnostic pop
+
+// A tile of 64 TN channels by 64 TM tokens: 2 x 2 waves of TN x TM blocks of 32 x 32
+// (v_mfma_i32_32x32x32_i8), over one part of K. A workgroup takes tiles one
+// after another.
 //
 // K passes in k-tiles of 64 bytes through STAGES places in LDS, by direct
 // global->LDS loads. Lane half h of a block's operands holds bytes 32 h .. + 31
@@ -218,52 +231,66 @@ __device__ __forceinline__ void tile_coords(int b, int nb, int n_tiles, int& tn,
 // second step's operands during the first step's products and the next
 // k-tile's first ones during the second's; between the steps it waits for the
 // next k-tile, and after the barrier there nobody reads the present one any
-// more, whose place the load of k-tile kt + STAGES takes.
+// more, whose place the load of k-tile kt + STAGES takes. The loads stand
+// between products: issued at once, they would hold up the products until the
+// last is taken.
+//
+// A tile's outputs are stored while the next tile's first k-tiles and its
+// scales are under way (the waits count loads, and stores after them make
+// them wait for a little more, never for less).
 template <int TN, int TM, int STAGES, int OCC>
-__global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles, int per) {
+__global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles, int tiles, int per) {
   constexpr int BN = 64 * TN, BM = 64 * TM;
   constexpr int kW = BN * kKTile, kStage = (BN + BM) * kKTile, CPW = TN + TM;
+  constexpr int kScales = STAGES * kStage, kScaleBytes = 4 * (BN + BM);        // two sets of scales after the places
   static_assert(CPW * (STAGES - 1) < 64, "vmcnt range");
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave >> 1, wm = wave & 1;
-  int tile_n, tile_m;
-  tile_coords(blockIdx.x, gridDim.x, n_tiles, tile_n, tile_m);
-  const int n0 = __builtin_amdgcn_readfirstlane(tile_n * BN), m0 = __builtin_amdgcn_readfirstlane(tile_m * BM);
   const int all = (a.K + kKTile - 1) / kKTile;
   const int kt0 = static_cast<int>(blockIdx.y) * per;
   const int nkt = all - kt0 < per ? all - kt0 : per;          // k-tiles of this part, at least one
-  const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
-  const int8_t* const wsrc = a.Wq + static_cast<int64_t>(n0) * a.K + static_cast<int64_t>(kt0) * kKTile;
-  const int8_t* const xsrc = a.Xq + static_cast<int64_t>(m0) * a.K + static_cast<int64_t>(kt0) * kKTile;
-  // Wave w loads chunks of 16 rows w TN .. of W and w TM .. of X; rows past the
-  // end are the last one again.
-  const int part = (lane & 3) ^ swz64(lane >> 2);
-  uint32_t woff[TN], xoff[TM];
-#pragma unroll
-  for (int i = 0; i < TN; ++i) {
-    const int row = (wave * TN + i) * 16 + (lane >> 2), last = a.N - 1 - n0;
-    woff[i] = static_cast<uint32_t>(row < last ? row : last) * a.K + part * 16;
-  }
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int row = (wave * TM + i) * 16 + (lane >> 2), last = a.M - 1 - m0;
-    xoff[i] = static_cast<uint32_t>(row < last ? row : last) * a.K + part * 16;
-  }
   const int ragged = a.K % kKTile;               // bytes of the last k-tile, 0 for all
-  const auto issue_whole = [&](int kt, int stage) SERQ_INLINE {
+  const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
+  const int part = (lane & 3) ^ swz64(lane >> 2);
+
+  // The tile whose loads are issued: its first rows, and each lane's rows in the
+  // wave's chunks of 16 (w TN .. of W, w TM .. of X; rows past the end are the
+  // last one again).
+  int n0 = 0, m0 = 0;
+  const int8_t* wsrc = nullptr;
+  const int8_t* xsrc = nullptr;
+  uint32_t woff[TN], xoff[TM];
+  const auto take = [&](int tile) SERQ_INLINE {
+    int tn, tm;
+    tile_coords(tile, tiles, n_tiles, tn, tm);
+    n0 = __builtin_amdgcn_readfirstlane(tn * BN);
+    m0 = __builtin_amdgcn_readfirstlane(tm * BM);
+    wsrc = a.Wq + static_cast<int64_t>(n0) * a.K + static_cast<int64_t>(kt0) * kKTile;
+    xsrc = a.Xq + static_cast<int64_t>(m0) * a.K + static_cast<int64_t>(kt0) * kKTile;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      const int row = (wave * TN + i) * 16 + (lane >> 2), last = a.N - 1 - n0;
+      woff[i] = static_cast<uint32_t>(row < last ? row : last) * a.K + part * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int row = (wave * TM + i) * 16 + (lane >> 2), last = a.M - 1 - m0;
+      xoff[i] = static_cast<uint32_t>(row < last ? row : last) * a.K + part * 16;
+    }
+  };
+  const auto issue_one = [&](int kt, int stage, int i) SERQ_INLINE {          // chunk i of TN + TM
     const uint32_t to = lds_base + stage * kStage;
-#pragma unroll
-    for (int i = 0; i < TN; ++i) dma16(wsrc + kt * kKTile, woff[i], to + (wave * TN + i) * 1024);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) dma16(xsrc + kt * kKTile, xoff[i], to + kW + (wave * TM + i) * 1024);
+    if (i < TN) dma16(wsrc + kt * kKTile, woff[i < TN ? i : 0], to + (wave * TN + i) * 1024);
+    else dma16(xsrc + kt * kKTile, xoff[i < TN ? 0 : i - TN], to + kW + (wave * TM + i - TN) * 1024);
   };
   // K's ragged end is filled with zeros. (A load that some lanes skip still
   // counts as one: part 0 of a row is always there.)
   const auto issue = [&](int kt, int stage) SERQ_INLINE {
     if (ragged == 0 || kt0 + kt + 1 < all) {
-      issue_whole(kt, stage);
+#pragma unroll
+      for (int i = 0; i < TN + TM; ++i) issue_one(kt, stage, i);
       return;
     }
     const uint32_t to = lds_base + stage * kStage;
@@ -275,11 +302,25 @@ __global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles
       else *reinterpret_cast<u32x4*>(lds + stage * kStage + at + lane * 16) = u32x4{0, 0, 0, 0};
     }
   };
+  // The scales of the tile (of channels and tokens that are there) into set
+  // `set`, then its first k-tiles.
+  const auto begin = [&](int set) SERQ_INLINE {
+    const uint32_t to = lds_base + kScales + set * kScaleBytes;
+    if (wave == 0) {
+#pragma unroll
+      for (int c = 0; c < TN; ++c)
+        if (n0 + 64 * c + lane < a.N) dma4(a.sw + n0 + 64 * c, 4 * lane, to + 256 * c);
+    } else if (wave == 1) {
+#pragma unroll
+      for (int c = 0; c < TM; ++c)
+        if (m0 + 64 * c + lane < a.M) dma4(a.sx + m0 + 64 * c, 4 * lane, to + 4 * BN + 256 * c);
+    }
+#pragma unroll
+    for (int st = 0; st < STAGES; ++st)
+      if (st < nkt) issue(st, st);
+  };
+
   v16i acc[TN][TM];
-#pragma unroll
-  for (int i = 0; i < TN; ++i)
-#pragma unroll
-    for (int j = 0; j < TM; ++j) acc[i][j] = v16i{};
   int wrd[2], xrd[2];
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
@@ -287,31 +328,30 @@ __global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles
     xrd[p] = kW + (wm * 32 * TM + l32) * kKTile + (((2 * h + p) ^ swz64(l32)) * 16);
   }
   v4i fw[2][TN], fx[2][TM];
-  const auto read_part = [&](int stage, auto pc) SERQ_INLINE {
+  const auto read_one = [&](int stage, auto pc, int i) SERQ_INLINE {           // operand i of TN + TM of a step
     constexpr int p = decltype(pc)::value;
     const uint8_t* sb = lds + stage * kStage;
-#pragma unroll
-    for (int i = 0; i < TN; ++i) fw[p][i] = *reinterpret_cast<const v4i*>(sb + wrd[p] + i * 32 * kKTile);
-#pragma unroll
-    for (int j = 0; j < TM; ++j) fx[p][j] = *reinterpret_cast<const v4i*>(sb + xrd[p] + j * 32 * kKTile);
+    if (i < TN) fw[p][i < TN ? i : 0] = *reinterpret_cast<const v4i*>(sb + wrd[p] + i * 32 * kKTile);
+    else fx[p][i < TN ? 0 : i - TN] = *reinterpret_cast<const v4i*>(sb + xrd[p] + (i - TN) * 32 * kKTile);
   };
-  const auto products = [&](auto pc) SERQ_INLINE {
+  const auto read_part = [&](int stage, auto pc) SERQ_INLINE {
+#pragma unroll
+    for (int i = 0; i < TN + TM; ++i) read_one(stage, pc, i);
+  };
+  // A step's products, with what else is to be issued between them: `with(q)`
+  // after product q. The order is kept as it stands here.
+  const auto products = [&](auto pc, auto&& with) SERQ_INLINE {
     constexpr int p = decltype(pc)::value;
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
-      for (int j = 0; j < TM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[p][i], fx[p][j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < TM; ++j) {
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[p][i], fx[p][j], acc[i][j], 0, 0, 0);
+        with(i * TM + j);
+        __builtin_amdgcn_sched_barrier(0);
+      }
   };
-  // A step: the reads of the next operands among its products.
-  const auto interleave = [&] SERQ_INLINE {
-#pragma unroll
-    for (int q = 0; q < TN + TM; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x008, TN * TM, 0);
-    __builtin_amdgcn_sched_barrier(0);
-  };
+  constexpr int kP = TN * TM, kEvery = kP / (TN + TM) > 0 ? kP / (TN + TM) : 1;      // products to a load
   using P0 = std::integral_constant<int, 0>;
   using P1 = std::integral_constant<int, 1>;
   const auto wait_tiles = [&](int n) SERQ_INLINE {            // until at most n k-tiles are under way
@@ -324,61 +364,57 @@ __global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles
       if (n == k) wait_vmcnt<CPW * k>();
     });
   };
-#pragma unroll
-  for (int st = 0; st < STAGES; ++st)
-    if (st < nkt) issue(st, st);
-  {
-    const int later = (nkt < STAGES ? nkt : STAGES) - 1;
-    if (later == STAGES - 1) wait_vmcnt<CPW * (STAGES - 1)>();
-    else wait_tiles(later);
-  }
-  __builtin_amdgcn_s_waitcnt(0xC07F);
-  asm volatile("s_barrier" ::: "memory");
-  read_part(0, P0{});
   const auto step = [&](int kt, int stage, auto whole) SERQ_INLINE {
     constexpr bool kWhole = decltype(whole)::value;          // kt + STAGES is there, and a whole k-tile
+    // (a read after each product, the rest after the last)
+    const auto reads = [&](int s, auto pc, int q) SERQ_INLINE {
+      if (q < TN + TM) read_one(s, pc, q);
+      if (q == kP - 1)
+#pragma unroll
+        for (int i = kP; i < TN + TM; ++i) read_one(s, pc, i);
+    };
     __builtin_amdgcn_sched_barrier(0);
-    read_part(stage, P1{});
-    products(P0{});
-    interleave();
+    products(P0{}, [&](int q) SERQ_INLINE { reads(stage, P1{}, q); });
     __builtin_amdgcn_s_waitcnt(0xC07F);
     const bool more = kWhole || kt + 1 < nkt;
     if (more) {
       if constexpr (kWhole) wait_vmcnt<CPW * (STAGES - 2)>();
       else wait_tiles(nkt - 2 - kt);
       asm volatile("s_barrier" ::: "memory");
-      if constexpr (kWhole) issue_whole(kt + STAGES, stage);
-      else if (kt + STAGES < nkt) issue(kt + STAGES, stage);
-      __builtin_amdgcn_sched_barrier(0);
-      read_part((stage + 1) % STAGES, P0{});
     }
-    products(P1{});
-    if constexpr (kWhole) interleave();
+    if constexpr (kWhole) {
+      products(P1{}, [&](int q) SERQ_INLINE {
+        reads((stage + 1) % STAGES, P0{}, q);
+        if (q % kEvery == kEvery - 1 && q / kEvery < TN + TM) issue_one(kt + STAGES, stage, q / kEvery);
+        if (q == kP - 1)
+#pragma unroll
+          for (int i = kP / kEvery; i < TN + TM; ++i) issue_one(kt + STAGES, stage, i);
+      });
+    } else {
+      if (kt + STAGES < nkt) issue(kt + STAGES, stage);
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) read_part((stage + 1) % STAGES, P0{});
+      products(P1{}, [](int) {});
+    }
   };
-  int kt = 0;
-  for (; kt + 2 * STAGES < nkt; kt += STAGES)
-    static_for<STAGES>([&](auto ic) { step(kt + decltype(ic)::value, decltype(ic)::value, std::true_type{}); });
-  for (; kt < nkt; kt += STAGES)
-    static_for<STAGES>([&](auto ic) {
-      constexpr int i = decltype(ic)::value;
-      if (kt + i < nkt) step(kt + i, i, std::false_type{});
-    });
-  wait_vmcnt<0>();
 
-  // Register e of block (i, j): channel 32 i + 8 (e / 4) + 4 h + e % 4 of token 32 j + l32.
-  if (a.partial) {
+  // Outputs: register e of block (i, j) is channel 32 i + 8 (e / 4) + 4 h + e % 4 of token 32 j + l32.
+  const auto four = [&](int i, int j, int q) SERQ_INLINE {
+    return v4i{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+  };
+  const auto store_parts = [&](int nn, int mm) SERQ_INLINE {
     int32_t* out = a.partial + static_cast<int64_t>(blockIdx.y) * a.M * a.N;
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      const int m = m0 + (wm * TM + j) * 32 + l32;
+      const int m = mm + (wm * TM + j) * 32 + l32;
       if (m >= a.M) continue;
 #pragma unroll
       for (int i = 0; i < TN; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int n = n0 + (wn * TN + i) * 32 + 8 * q + 4 * h;
+          const int n = nn + (wn * TN + i) * 32 + 8 * q + 4 * h;
           int32_t* to = out + static_cast<int64_t>(m) * a.N + n;
-          const v4i x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          const v4i x = four(i, j, q);
           if (n + 3 < a.N && (a.N & 3) == 0) {
             *reinterpret_cast<v4i*>(to) = x;
           } else {
@@ -388,25 +424,98 @@ __global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles
           }
         }
     }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < TN; ++i) {
-    const int n = n0 + (wn * TN + i) * 32 + 4 * h;
-    float sw[4][4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) load_scales(a, n + 8 * q, sw[q]);
+  };
+  const auto store_tile = [&](int nn, int mm, int set) SERQ_INLINE {
+    const float* ssw = reinterpret_cast<const float*>(lds + kScales + set * kScaleBytes);
+    const float* ssx = ssw + BN;
+    float sx[TM];
+    int m[TM];
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      const int m = m0 + (wm * TM + j) * 32 + l32;
-      if (m >= a.M) continue;
-      const float sx = a.sx[m];
+      const int row = (wm * TM + j) * 32 + l32;
+      sx[j] = ssx[row];
+      m[j] = mm + row;
+    }
+    const bool pairs = a.y_bf16 && (a.N & 7) == 0 && !a.dbg;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const v4i x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        if (n + 8 * q < a.N) store4(a, x, m, n + 8 * q, sx, sw[q]);
+    for (int i = 0; i < TN; ++i) {
+      const int c0 = (wn * TN + i) * 32;
+      f32x4 sw[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sw[q] = *reinterpret_cast<const f32x4*>(ssw + c0 + 8 * q + 4 * h);
+      if (pairs) {
+        // Lane half h holds channels 8 q + 4 h .. + 3: with the halves of two q
+        // exchanged, each lane has eight channels side by side.
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+          __bf16* row = static_cast<__bf16*>(a.Y) + static_cast<int64_t>(m[j]) * a.N + nn + c0;
+#pragma unroll
+          for (int q = 0; q < 4; q += 2) {
+            uint32_t w[2][2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float y[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) y[c] = sx[j] * (sw[q + u][c] * static_cast<float>(acc[i][j][4 * (q + u) + c]));
+              w[u][0] = pack_bf16x2(y[0], y[1]);
+              w[u][1] = pack_bf16x2(y[2], y[3]);
+            }
+            const auto lo = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+            const auto hi = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+            const int c = 8 * q + 8 * h;
+            if (m[j] < a.M && nn + c0 + c < a.N) *reinterpret_cast<u32x4*>(row + c) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+          }
+        }
+        continue;
+      }
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        if (m[j] >= a.M) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = nn + c0 + 8 * q + 4 * h;
+          const float s4[4] = {sw[q][0], sw[q][1], sw[q][2], sw[q][3]};
+          if (n < a.N) store4(a, four(i, j, q), m[j], n, sx[j], s4);
+        }
       }
     }
+  };
+
+  int tile = blockIdx.x, set = 0;
+  take(tile);
+  begin(set);
+  while (true) {
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = v16i{};
+    const int later = (nkt < STAGES ? nkt : STAGES) - 1;
+    if (later == STAGES - 1) wait_vmcnt<CPW * (STAGES - 1)>();
+    else wait_tiles(later);
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("s_barrier" ::: "memory");
+    read_part(0, P0{});
+    int kt = 0;
+    for (; kt + 2 * STAGES < nkt; kt += STAGES)
+      static_for<STAGES>([&](auto ic) { step(kt + decltype(ic)::value, decltype(ic)::value, std::true_type{}); });
+    for (; kt < nkt; kt += STAGES)
+      static_for<STAGES>([&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        if (kt + i < nkt) step(kt + i, i, std::false_type{});
+      });
+    const int nn = n0, mm = m0;
+    const int now = set;
+    tile += gridDim.x;
+    const bool more = tile < tiles;
+    asm volatile("s_barrier" ::: "memory");      // (every read of the places has landed: its products are issued)
+    if (more) {
+      take(tile);
+      set ^= 1;
+      begin(set);
+    }
+    if (a.partial) store_parts(nn, mm);
+    else store_tile(nn, mm, now);
+    if (!more) break;
   }
 }
 
@@ -452,15 +561,16 @@ __global__ __launch_bounds__(256) void i8_generic_kernel(I8Args a) {
 
 template <int TN, int TM, int STAGES, int OCC>
 hipError_t launch_tile(const I8Args& a, const I8Plan& p, hipStream_t st) {
-  constexpr int kLds = STAGES * 64 * (TN + TM) * kKTile;
+  constexpr int kLds = 64 * (TN + TM) * (STAGES * kKTile + 8);
   const int n_tiles = (a.N + 64 * TN - 1) / (64 * TN);
-  const int64_t m_tiles = (a.M + 64 * TM - 1) / (64 * TM);
+  const int tiles = n_tiles * ((a.M + 64 * TM - 1) / (64 * TM));
   auto* kernel = &i8_tile_kernel<TN, TM, STAGES, OCC>;
   if (kLds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (e != hipSuccess) return e;
   }
-  kernel<<<dim3(static_cast<unsigned>(n_tiles * m_tiles), p.splits), 256, kLds, st>>>(a, n_tiles, p.per);
+  const int groups = tiles < OCC * kCUs ? tiles : OCC * kCUs;
+  kernel<<<dim3(groups, p.splits), 256, kLds, st>>>(a, n_tiles, tiles, p.per);
   if (p.splits > 1) {
     const int64_t lanes = static_cast<int64_t>(a.M) * ((a.N + 3) / 4);
     i8_join_kernel<<<dim3(static_cast<unsigned>((lanes + 255) / 256)), 256, 0, st>>>(a, p.splits);
