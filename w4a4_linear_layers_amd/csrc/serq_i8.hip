@@ -73,96 +73,6 @@ __device__ __forceinline__ void load_scales(const I8Args& a, int n, float (&sw)[
   for (int i = 0; i < 4; ++i) sw[i] = a.sw[n + i < a.N ? n + i : a.N - 1];
 }
 
-// ---------------------------------------------------------------- few tokens
-
-// One workgroup: RT tiles of 16 weight rows, all tokens (NT tiles of 16), its
-// eight waves taking chunks of 256 bytes of K in turn; their sums meet in LDS.
-// Lane (row or token l = lane % 16, g = lane / 16) of a step holds bytes 64 s +
-// 16 g .. + 15 of the chunk of its row for v_mfma_i32_16x16x64_i8, whichever
-// order of k that makes being the same on both sides. Weights pass once, so
-// the kernel is bound by HBM; the tokens' rows come from L2, a workgroup's
-// whole K of them for RT tiles of weights.
-constexpr int kStreamWaves = 8, kChunk = 256;
-
-template <int RT, int NT>
-__global__ __launch_bounds__(64 * kStreamWaves) void i8_stream_kernel(I8Args a) {
-  __shared__ v4i red[kStreamWaves][RT * NT][64];
-  const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * (16 * RT);
-  const int8_t* w[RT];
-  const int8_t* x[NT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int row = n0 + 16 * r + l;
-    w[r] = a.Wq + static_cast<int64_t>(row < a.N ? row : a.N - 1) * a.K;
-  }
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int row = 16 * t + l;
-    x[t] = a.Xq + static_cast<int64_t>(row < a.M ? row : a.M - 1) * a.K;
-  }
-  v4i acc[RT][NT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[r][t] = v4i{0, 0, 0, 0};
-  const int whole = a.K / kChunk;
-  for (int c = wave; c < whole; c += kStreamWaves) {
-    const int k0 = c * kChunk + 16 * g;
-    v4i wv[RT][4], xv[NT][4];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-#pragma unroll
-      for (int r = 0; r < RT; ++r) wv[r][s] = *reinterpret_cast<const v4i*>(w[r] + k0 + 64 * s);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) xv[t][s] = *reinterpret_cast<const v4i*>(x[t] + k0 + 64 * s);
-    }
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[r][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[r][s], xv[t][s], acc[r][t], 0, 0, 0);
-  }
-  if (wave == whole % kStreamWaves) {           // what is left of K, 16 bytes a lane at a time
-    for (int k = whole * kChunk; k < a.K; k += 64) {
-      const bool in = k + 16 * g < a.K;
-      const int at = in ? k + 16 * g : 0;
-      v4i xv[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        xv[t] = *reinterpret_cast<const v4i*>(x[t] + at);
-        if (!in) xv[t] = v4i{0, 0, 0, 0};
-      }
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const v4i wv = *reinterpret_cast<const v4i*>(w[r] + at);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[r][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv, xv[t], acc[r][t], 0, 0, 0);
-      }
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) red[wave][r * NT + t][lane] = acc[r][t];
-  __syncthreads();
-  for (int b = wave; b < RT * NT; b += kStreamWaves) {
-    v4i sum = red[0][b][lane];
-#pragma unroll
-    for (int i = 1; i < kStreamWaves; ++i) sum += red[i][b][lane];
-    const int m = 16 * (b % NT) + l, n = n0 + 16 * (b / NT) + 4 * g;
-    if (m < a.M && n < a.N) {
-      float sw[4];
-      load_scales(a, n, sw);
-      store4(a, sum, m, n, a.sx[m], sw);
-    }
-  }
-}
-
-// ---------------------------------------------------------------- tiles
-
 // One 16-byte direct global->LDS load per lane, from sbase + voff (sbase
 // wave-uniform), into the wave's 1 KB chunk at `lds_chunk`: lane i lands at
 // + 16 i. M0 is written here and declared clobbered. Waits are explicit; LDS
@@ -190,6 +100,115 @@ template <int N, typename F>
 __device__ __forceinline__ void static_for(F&& f) {
   static_for_impl<N>(f, std::make_integer_sequence<int, N>{});
 }
+
+// ---------------------------------------------------------------- few tokens
+
+// One workgroup: RT tiles of 16 weight rows, all tokens (NT tiles of 16). K
+// passes in windows of 512 bytes through STAGES places in LDS, by direct
+// global->LDS loads of two rows' 512 bytes each: whole lines, where an operand
+// loaded straight into registers takes 64 bytes of each of 16 rows and so half
+// of the rate into a compute unit (45 tokens, 14336 x 4096: 26 us). Wave w
+// multiplies bytes 64 w .. of each window, lane (row or token l = lane % 16, g =
+// lane / 16) with bytes 16 g of those, by v_mfma_i32_16x16x64_i8; the waves' sums
+// meet in LDS.
+constexpr int kStreamWaves = 8, kWindow = 64 * kStreamWaves;
+
+template <int RT, int NT, int STAGES, int OCC>
+__global__ __launch_bounds__(64 * kStreamWaves, OCC) void i8_stream_kernel(I8Args a) {
+  constexpr int CPW = RT + NT, kStage = CPW * 16 * kWindow;       // a window: CPW loads of a wave
+  static_assert(CPW * (STAGES - 1) < 64, "vmcnt range");
+  static_assert(kStreamWaves * RT * NT * 1024 <= STAGES * kStage, "the sums take the windows' place");
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * (16 * RT);
+  const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
+  // Rows of a window: RT * 16 of W, then NT * 16 of X. Load i of wave w: rows 16 i +
+  // 2 w and the next. A 16-byte part of a row lies at part ^ (row % 16), so that
+  // one part of 16 rows falls on distinct banks.
+  const int row = 2 * wave + (lane >> 5), part = (lane & 31) ^ row;
+  const int8_t* const wsrc = a.Wq + static_cast<int64_t>(n0) * a.K;
+  uint32_t off[CPW];
+#pragma unroll
+  for (int i = 0; i < CPW; ++i) {
+    const int r = 16 * (i < RT ? i : i - RT) + row, last = (i < RT ? a.N - n0 : a.M) - 1;
+    off[i] = static_cast<uint32_t>(r < last ? r : last) * a.K + 16 * part;
+  }
+  const int all = (a.K + kWindow - 1) / kWindow, ragged = a.K % kWindow;
+  // (K's ragged end is filled with zeros; part 0 of a row is always there, so
+  // every load is issued)
+  // Each workgroup of an XCD begins at another window: rows a multiple of 2 KB
+  // apart lie in few of its L2's channels, and all workgroups read the tokens.
+  const int turn = static_cast<int>(blockIdx.x >> 3) % all;
+  const auto issue = [&](int step, int stage) SERQ_INLINE {
+    int k = step + turn;
+    k -= k >= all ? all : 0;
+    const uint32_t to = lds_base + stage * kStage + wave * 1024;
+    const bool whole = ragged == 0 || k + 1 < all, in = whole || 16 * part < ragged;
+#pragma unroll
+    for (int i = 0; i < CPW; ++i) {
+      const int8_t* src = (i < RT ? wsrc : a.Xq) + k * kWindow;
+      if (whole) dma16(src, off[i], to + i * 8192);
+      else if (in) dma16(src, off[i], to + i * 8192);
+      else *reinterpret_cast<u32x4*>(lds + stage * kStage + wave * 1024 + i * 8192 + lane * 16) = u32x4{0, 0, 0, 0};
+    }
+  };
+  v4i acc[RT][NT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[r][t] = v4i{0, 0, 0, 0};
+  const int at = l * kWindow + (((4 * wave + g) ^ l) << 4);
+#pragma unroll
+  for (int st = 0; st < STAGES - 1; ++st)
+    if (st < all) issue(st, st);
+  const auto step = [&](int k, auto sc) SERQ_INLINE {
+    constexpr int stage = decltype(sc)::value;
+    const int later = all - 1 - k < STAGES - 2 ? all - 1 - k : STAGES - 2;       // windows under way after this one
+    static_for<STAGES - 1>([&](auto nc) {
+      constexpr int n = decltype(nc)::value;
+      if (later == n) wait_vmcnt<CPW * n>();
+    });
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("s_barrier" ::: "memory");      // window k is there, and nobody reads the one before it any more
+    if (k + STAGES - 1 < all) issue(k + STAGES - 1, (stage + STAGES - 1) % STAGES);
+    const uint8_t* from = lds + stage * kStage + at;
+    v4i w[RT], x[NT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) w[r] = *reinterpret_cast<const v4i*>(from + r * 8192);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) x[t] = *reinterpret_cast<const v4i*>(from + (RT + t) * 8192);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[r][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[r], x[t], acc[r][t], 0, 0, 0);
+  };
+  for (int k = 0; k < all; k += STAGES)
+    static_for<STAGES>([&](auto sc) {
+      if (k + decltype(sc)::value < all) step(k + decltype(sc)::value, sc);
+    });
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  asm volatile("s_barrier" ::: "memory");
+  v4i* red = reinterpret_cast<v4i*>(lds);        // [wave][tile][lane]
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) red[(wave * RT * NT + r * NT + t) * 64 + lane] = acc[r][t];
+  __syncthreads();
+  for (int b = wave; b < RT * NT; b += kStreamWaves) {
+    v4i sum = red[b * 64 + lane];
+#pragma unroll
+    for (int i = 1; i < kStreamWaves; ++i) sum += red[(i * RT * NT + b) * 64 + lane];
+    const int m = 16 * (b % NT) + l, n = n0 + 16 * (b / NT) + 4 * g;
+    if (m < a.M && n < a.N) {
+      float sw[4];
+      load_scales(a, n, sw);
+      store4(a, sum, m, n, a.sx[m], sw);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- tiles
 
 // A 16-byte part of a 64-byte row lies at part ^ swz64(row), so that the reads
 // of one part of 16 consecutive rows fall on distinct banks.
@@ -578,19 +597,35 @@ hipError_t launch_tile(const I8Args& a, const I8Plan& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int RT, int NT>
+template <int RT, int NT, int STAGES, int OCC>
 hipError_t launch_stream(const I8Args& a, hipStream_t st) {
-  i8_stream_kernel<RT, NT><<<dim3((a.N + 16 * RT - 1) / (16 * RT)), 64 * kStreamWaves, 0, st>>>(a);
+  constexpr int kLds = STAGES * (RT + NT) * 16 * kWindow;
+  static_assert(kLds * (OCC / 2) <= 160 * 1024, "LDS");
+  auto* kernel = &i8_stream_kernel<RT, NT, STAGES, OCC>;
+  if (kLds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (e != hipSuccess) return e;
+  }
+  kernel<<<dim3((a.N + 16 * RT - 1) / (16 * RT)), 64 * kStreamWaves, kLds, st>>>(a);
   return hipGetLastError();
 }
 
-template <int RT>
-hipError_t launch_stream_tokens(const I8Args& a, int nt, hipStream_t st) {
+// Places: as many as two workgroups a compute unit leave room for, or one
+// workgroup where that would be fewer than three.
+hipError_t launch_stream_tokens(const I8Args& a, int rt, int nt, hipStream_t st) {
+  if (rt == 2) {
+    switch (nt) {
+      case 1: return launch_stream<2, 1, 3, 4>(a, st);
+      case 2: return launch_stream<2, 2, 5, 2>(a, st);
+      case 3: return launch_stream<2, 3, 4, 2>(a, st);
+      default: return launch_stream<2, 4, 3, 2>(a, st);
+    }
+  }
   switch (nt) {
-    case 1: return launch_stream<RT, 1>(a, st);
-    case 2: return launch_stream<RT, 2>(a, st);
-    case 3: return launch_stream<RT, 3>(a, st);
-    default: return launch_stream<RT, 4>(a, st);
+    case 1: return launch_stream<1, 1, 5, 4>(a, st);
+    case 2: return launch_stream<1, 2, 3, 4>(a, st);
+    case 3: return launch_stream<1, 3, 5, 2>(a, st);
+    default: return launch_stream<1, 4, 4, 2>(a, st);
   }
 }
 
@@ -611,7 +646,7 @@ I8Plan plan_linear_i8(int M, int K, int N) {
   if (M <= 64) {
     p.kind = I8Kernel::kStream;
     p.nt = static_cast<int>(ceil_div(M, 16));
-    p.rt = N >= 16384 ? 2 : 1;
+    p.rt = N >= 16384 && p.nt > 2 ? 2 : 1;
     p.name = "stream";
     return p;
   }
@@ -640,7 +675,7 @@ I8Plan plan_linear_i8(int M, int K, int N) {
 hipError_t launch_linear_i8(const I8Args& a, const I8Plan& p, hipStream_t st) {
   switch (p.kind) {
     case I8Kernel::kStream:
-      return p.rt == 2 ? launch_stream_tokens<2>(a, p.nt, st) : launch_stream_tokens<1>(a, p.nt, st);
+      return launch_stream_tokens(a, p.rt, p.nt, st);
     case I8Kernel::kTile256: return launch_tile<4, 4, 4, 1>(a, p, st);
     case I8Kernel::kTile128: return launch_tile<2, 2, 4, 2>(a, p, st);
     default: break;
