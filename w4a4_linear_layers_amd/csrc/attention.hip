@@ -522,38 +522,57 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, PrefillPlan 
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + uniform(threadIdx.x >> 6);
   const int t = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
   if (t >= (PREFILL ? a.T : a.B)) return;
-  const int count = parts_of_row<PREFILL>(a, p, t, psplits, chunk);
-  if (count < 0) return;
   const float2* ml = parts.ml + row * parts.splits;
   const float* po = parts.o + row * parts.splits * D + lane * W;
-  // The parts' maxima and sums by lanes, 64 at a time; then their sums of
-  // values, eight loads in flight.
-  float m = kNone;
-  for (int s = lane; s < count; s += 64) m = fmaxf(m, ml[s].x);
+  // Eight loads in flight, the next eight while these are added. The first start
+  // before it is known how many parts the row has: those of a prefix are always
+  // there, and a prompt's rows mostly have all of their few.
+  float v[2][8][W];
+  const auto load = [&](int s0, int n, float (&to)[8][W]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int i = 0; i < W; ++i) to[k][i] = s0 + k < n ? po[static_cast<int64_t>(s0 + k) * D + i] : 0.0f;
+  };
+  const int early = PREFILL ? (parts.splits < 4 ? parts.splits : 4) : psplits < 8 ? psplits : 8;
+  load(0, early, v[0]);
+  float2 first = lane < parts.splits ? ml[lane] : float2{kNone, 0.0f};
+  const int count = parts_of_row<PREFILL>(a, p, t, psplits, chunk);
+  if (count < 0) return;
+  if (lane >= count) first = float2{kNone, 0.0f};
+#pragma unroll
+  for (int k = 0; k < 8; ++k)                        // the rest of the first eight
+    if (k >= early && k < count) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[0][k][i] = po[static_cast<int64_t>(k) * D + i];
+    }
+  float m = first.x;
+  for (int s = lane + 64; s < count; s += 64) m = fmaxf(m, ml[s].x);
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
   const float r = ref(m);
-  float l = 0.0f, o[W] = {};
-  for (int s0 = 0; s0 < count; s0 += 64) {
-    const int n = count - s0 < 64 ? count - s0 : 64;
-    const float2 x = lane < n ? ml[s0 + lane] : float2{kNone, 0.0f};
-    const float f = exp2_(x.x - r);                // this lane's part's weight
-    l = __builtin_fmaf(f, x.y, l);
-    for (int s = 0; s < n; s += 8) {
-      float v[8][W];
+  float l = 0.0f, f = 0.0f, o[W] = {};               // f: this lane's part's weight, of 64 parts at a time
+  const auto add = [&](int s0, const float (&from)[8][W]) __attribute__((always_inline)) {
+    if ((s0 & 63) == 0) {
+      const float2 x = s0 == 0 ? first : s0 + lane < count ? ml[s0 + lane] : float2{kNone, 0.0f};
+      f = exp2_(x.x - r);
+      l = __builtin_fmaf(f, x.y, l);
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < 8; ++k) {
+      const float w = __shfl(f, (s0 + k) & 63, 64);
+      if (s0 + k < count) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[k][i] = s + k < n ? po[static_cast<int64_t>(s0 + s + k) * D + i] : 0.0f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float w = __shfl(f, (s + k) & 63, 64);
-        if (s + k < n) {
-#pragma unroll
-          for (int i = 0; i < W; ++i) o[i] = __builtin_fmaf(w, v[k][i], o[i]);
-        }
+        for (int i = 0; i < W; ++i) o[i] = __builtin_fmaf(w, from[k][i], o[i]);
       }
     }
+  };
+  for (int s0 = 0; s0 < count; s0 += 16) {
+    if (s0 + 8 < count) load(s0 + 8, count, v[1]);
+    add(s0, v[0]);
+    if (s0 + 8 >= count) break;
+    if (s0 + 16 < count) load(s0 + 16, count, v[0]);
+    add(s0 + 8, v[1]);
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) l += __shfl_xor(l, off, 64);
@@ -749,7 +768,14 @@ DecodePlan plan_decode(int kind, int B, int Hq, int Hkv, int D, int prefix_len, 
   // after a prefix: 50.6 us against 51.6; one of 4095 keys: 9.4 us against 8.4).
   const int64_t groups = static_cast<int64_t>(B) * Hkv * p.tiles;
   int64_t s = ceil_div(8192, groups);
-  p.chunk = cut(max_len, s, groups >= 512 ? 256 : 128);
+  // A cache of codes: a workgroup's four waves take 256 keys at a time, so parts
+  // are larger where there are many (256 sequences of 20 to 2000 keys, 8
+  // key/value heads of 128: parts of 1024 59.5 us, of 256 76.7; 120 of 5 to 900
+  // after a prefix 51.4 against 58.0; 128 of 500 to 1500 parts of 512 43.8, of 256
+  // 46.6, of 1024 52.6; 64 of 100 to 4096 parts of 256 36.9, of 1024 45.8).
+  int unit = groups >= 512 ? 256 : 128;
+  if ((kind & kCodes) && groups >= 768) unit = groups >= 1536 || max_len <= 1024 ? 1024 : 512;
+  p.chunk = cut(max_len, s, unit);
   p.splits = static_cast<int>(s);
   p.waves = 4;
   // Short caches whole: one launch and no join, eight waves a workgroup beyond
