@@ -51,7 +51,7 @@ def run(M, K, N, dtype, *, seed=1, low=-128, high=128):
     (1, 16, 1), (1, 4096, 320), (2, 272, 33), (16, 256, 16), (17, 2064, 50), (33, 4112, 100), (49, 1040, 65), (64, 2048, 64),
     (5, 1024, 16400), (64, 528, 16385),                             # two tiles of rows to a workgroup
     (65, 16, 1), (65, 64, 130), (128, 128, 128), (129, 80, 127), (200, 4096, 96), (66, 16384, 40), (130, 2064, 260),
-    (300, 320, 5000), (1000, 1040, 700),
+    (300, 320, 5000), (1000, 1040, 700), (1100, 528, 2050), (130, 12304, 260), (257, 80, 4500), (65, 64, 20000),
     (4096, 64, 4096), (3600, 272, 4000), (3585, 528, 4097), (2050, 1088, 7001),      # 256 x 256
     (1, 15, 3), (7, 131, 70), (70, 33, 300), (3, 20000 + 2, 5),      # no whole 16 bytes
 ])
@@ -105,7 +105,7 @@ def test_mlp_in_8_bits():
 
 
 def test_streams_graphs_and_refusals():
-    M, K, N = 100, 4096, 256                       # K in parts, through a workspace
+    M, K, N = 100, 16384, 256                      # K in parts, through a workspace
     g = torch.Generator()
     g.manual_seed(4)
     x = torch.randint(-127, 128, (M, K), generator=g, dtype=torch.int8).to(DEV)

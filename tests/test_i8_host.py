@@ -74,7 +74,7 @@ def lin(xq=A, sx=A, wq=A, sw=A, M=4, K=64, N=32, y=A, dt=BF16, acc=None, ws=None
     (dict(xq=None), EINVAL), (dict(sx=None), EINVAL), (dict(wq=None), EINVAL), (dict(sw=None), EINVAL), (dict(y=None), EINVAL),
     (dict(xq=A + 8), EALIGN), (dict(sx=A + 4), EALIGN), (dict(wq=A + 1), EALIGN), (dict(sw=A + 8), EALIGN), (dict(y=A + 2), EALIGN),
     (dict(acc=A + 4), EALIGN), (dict(ws=A + 4, size=1 << 40), EALIGN),
-    (dict(M=100, K=4096, N=256), EINVAL), (dict(M=100, K=4096, N=256, ws=A, size=100), EINVAL),      # a workspace is needed
+    (dict(M=100, K=16384, N=256), EINVAL), (dict(M=100, K=16384, N=256, ws=A, size=100), EINVAL),      # a workspace is needed
     (dict(M=0), OK), (dict(M=0, xq=None, sx=None, y=None), OK), (dict(M=0, wq=None), EINVAL),
 ])
 def test_refusals(kw, code):
@@ -85,6 +85,9 @@ def test_plans():
     w, name = _lib.lib.serq_linear_i8_workspace, S.i8_kernel_name
     assert w(-1, 64, 64) == -1 and w(1, 1 << 17, 64) == -1 and w(0, 64, 64) == 0 and name(1, 0, 1) is None
     assert name(4096, 8192, 8192) == "tile256x256" and name(1, 4096, 4096) == "stream" and name(1, 4090, 8) == "generic"
+    assert name(100, 4096, 4096) == "tile64x64" and name(400, 4096, 4096) == "tile64x128"
+    assert name(1000, 4096, 4096) == "tile128x128" and w(1000, 4096, 4096) == 0 and name(100, 14336, 4096) == "tile128x128"
+    assert w(100, 14336, 4096) > 0
     for M in (1, 16, 64, 65, 100, 128, 500, 2000, 5000, 1 << 20):
         for K, N in ((16, 1), (64, 64), (4096, 4096), (14336, 4096), (131056, 300), (4096, 128256)):
             assert 0 <= w(M, K, N) < 1 << 28, (M, K, N)

@@ -1,10 +1,10 @@
 // The linear in 8-bit integers for gfx950:
 //     Y[m, n] = sx[m] * (sw[n] * sum_k Xq[m, k] Wq[n, k]),
 // exact int32 sums on v_mfma_i32_*_i8, whose operands are the bytes as they are
-// stored. Three kernels: few tokens stream the weights from HBM straight into
-// registers; prompts take tiles of 256 x 256, or of 128 x 128 where those would
-// leave compute units idle, from LDS; rows that are no whole 16 bytes take one
-// lane an output.
+// stored. Three kernels, the operands of two of them by whole lines through LDS:
+// few tokens stream the weights from HBM, the workgroup's waves sharing its K;
+// more take tiles of 256 x 256, or smaller ones where those would leave compute
+// units idle; rows that are no whole 16 bytes take one lane an output.
 //
 // The matrix instructions take weights as their first operand, so a lane holds
 // four consecutive channels of one token at a time, which the epilogue scales
@@ -656,11 +656,22 @@ I8Plan plan_linear_i8(int M, int K, int N) {
     p.name = "tile256x256";
     return p;
   }
-  const int64_t tiles = ceil_div(N, 128) * ceil_div(M, 128);
+  // Tiles of 128 x 128 where there are enough of them; of half that size, or a
+  // quarter, where there are not (256 x 4096 x 4096: 11.5 us in tiles of 64 x 64,
+  // 17.7 of 128 x 128; 384 tokens 15.1 of 64 x 128, 18.5 of 64 x 64; 768 tokens 21.0 of
+  // 128 x 128, 26.6 of 64 x 128). Long rows are cut in parts instead (128 x 14336 x
+  // 4096: 25.7 us in eight parts, 29.3 in tiles of 64 x 64 and two; 128 x 8192 x
+  // 8192 27.2 in four and 27.5 in tiles of 64 x 64).
+  const int64_t tiles = ceil_div(N, 128) * ceil_div(M, 128), quarters = ceil_div(N, 64) * ceil_div(M, 64);
+  if (tiles < 150 && k_tiles <= 160) {
+    p.kind = quarters <= 256 ? I8Kernel::kTile64 : I8Kernel::kTile64x128;
+    p.name = quarters <= 256 ? "tile64x64" : "tile64x128";
+    return p;
+  }
   p.kind = I8Kernel::kTile128;
   p.name = "tile128x128";
-  if (tiles < 256) {
-    int64_t s = 512 / tiles;
+  if (tiles < 150) {
+    int64_t s = (256 + tiles / 2) / tiles;
     if (s > k_tiles / 8) s = k_tiles / 8;
     if (s > 16) s = 16;
     if (s > 1) {
@@ -678,6 +689,8 @@ hipError_t launch_linear_i8(const I8Args& a, const I8Plan& p, hipStream_t st) {
       return launch_stream_tokens(a, p.rt, p.nt, st);
     case I8Kernel::kTile256: return launch_tile<4, 4, 4, 1>(a, p, st);
     case I8Kernel::kTile128: return launch_tile<2, 2, 4, 2>(a, p, st);
+    case I8Kernel::kTile64x128: return launch_tile<1, 2, 6, 2>(a, p, st);
+    case I8Kernel::kTile64: return launch_tile<1, 1, 8, 2>(a, p, st);
     default: break;
   }
   const int64_t blocks = ceil_div(static_cast<int64_t>(a.M) * a.N, 256);
