@@ -4,7 +4,9 @@ The q/k/v and output projections are SERQ W4A4 linears; between them the
 queries and keys are normed, rotated and stored (rope_append), prompts attend
 in one packed call (attn_prefill), and every further token of all users in one
 call over a prefix that they share (attn_decode), captured once in a HIP graph
-and replayed.
+and replayed. With ``codes`` the cache holds FP8 codes (KvCacheF8), the output
+projection is one in 8-bit integers (linear_i8), and positions have three
+axes, alike here as for text (pair_axis).
 
     python examples/serve_attention.py
 
@@ -32,31 +34,44 @@ def rms(x):
 class AttentionBlock:
     """x -> x + o(attention(qkv(norm x))), its keys and values in a paged cache."""
 
-    def __init__(self, n_pages: int, seed: int = 0):
+    def __init__(self, n_pages: int, seed: int = 0, codes: bool = False):
         rng = np.random.default_rng(seed)
         width = (HQ + 2 * HKV) * D
         amax = np.full(HIDDEN, 4.0, np.float32)
         amax[rng.choice(HIDDEN, 10, replace=False)] = 60.0
         qkv = S.calibrate(rng.standard_normal((HIDDEN, width), dtype=np.float32) * 0.04, amax, r=64)
-        out = S.calibrate(rng.standard_normal((HQ * D, HIDDEN), dtype=np.float32) * 0.04,
-                          np.full(HQ * D, 3.0, np.float32), r=64)
-        self.qkv, self.out = qkv.to("cuda"), out.to("cuda")
-        # the linears take their inputs in saliency order
-        self.order_in, self.order_out = self.qkv.perm.long(), self.out.perm.long()
+        w_out, out_amax = rng.standard_normal((HQ * D, HIDDEN), dtype=np.float32) * 0.04, np.full(HQ * D, 3.0, np.float32)
+        out = S.calibrate_i8(w_out, out_amax) if codes else S.calibrate(w_out, out_amax, r=64)
+        self.qkv, self.out, self.codes = qkv.to("cuda"), out.to("cuda"), codes
+        # the W4A4 linears take their inputs in saliency order
+        self.order_in = self.qkv.perm.long()
+        self.order_out = None if codes else self.out.perm.long()
         self.q_norm = torch.from_numpy(1 + 0.1 * rng.standard_normal(D).astype(np.float32)).cuda()
         self.k_norm = torch.from_numpy(1 + 0.1 * rng.standard_normal(D).astype(np.float32)).cuda()
         # trained to 1024 positions, served to 4096
         self.table = torch.from_numpy(S.rope_table(D, MAX_POS, theta=500000.0, scaling="bands", factor=4.0,
                                                    orig_len=1024)).cuda()
-        self.cache = S.KvCache.empty(n_pages, HKV, PAGE, D)
+        self.cache = (S.KvCacheF8 if codes else S.KvCache).empty(n_pages, HKV, PAGE, D)
+        self.pair_axis = bytes(i % 3 for i in range(D // 2)) if codes else None
 
     def queries(self, x, pos, slot):
         """The rows' queries; their keys and values are stored."""
         qkv = S.linear(*S.quant_act(rms(x)[:, self.order_in].contiguous(), self.qkv), self.qkv)
-        return S.rope_append(qkv, HQ, self.cache, pos, slot, self.table, q_norm=self.q_norm, k_norm=self.k_norm)
+        if self.codes:
+            pos = pos.expand(3, -1).contiguous()
+        return S.rope_append(qkv, HQ, self.cache, pos, slot, self.table, q_norm=self.q_norm, k_norm=self.k_norm,
+                             pair_axis=self.pair_axis)
+
+    def tensors(self):
+        """The cache's tensors."""
+        c = self.cache
+        return (c.k, c.v, c.k_scale, c.v_scale) if self.codes else (c.k, c.v)
 
     def finish(self, x, o):
-        o = o.view(o.shape[0], HQ * D)[:, self.order_out].contiguous()
+        o = o.view(o.shape[0], HQ * D)
+        if self.codes:
+            return x + S.linear_i8(*S.quant_act(o, self.out.s_hat_inv, a_bits=8), self.out)
+        o = o[:, self.order_out].contiguous()
         return x + S.linear(*S.quant_act(o, self.out), self.out)
 
     def prefill(self, x, pos, slot, cu, pages, kv_len, max_len):
@@ -72,7 +87,8 @@ def slots(pages, seq, at):
     return (pages[seq, at // PAGE] * PAGE + at % PAGE).to(torch.int32)
 
 
-def serve(steps: int = 24, prefix_len: int = 5 * PAGE, prompts=(7, 33, 1, 20), seed: int = 0, graph: bool = True):
+def serve(steps: int = 24, prefix_len: int = 5 * PAGE, prompts=(7, 33, 1, 20), seed: int = 0, graph: bool = True,
+          codes: bool = False):
     """Prefills a shared prefix and one prompt per user, then decodes `steps`
     tokens for all of them. Returns every step's outputs (users x hidden) and
     what checks them: the block and its state."""
@@ -80,7 +96,7 @@ def serve(steps: int = 24, prefix_len: int = 5 * PAGE, prompts=(7, 33, 1, 20), s
     lead = prefix_len // PAGE                        # whole pages, so that a prompt can continue the prefix's row
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
-    block = AttentionBlock(lead + users * room + 1, seed)
+    block = AttentionBlock(lead + users * room + 1, seed, codes)
     order = torch.randperm(lead + users * room, generator=g, device="cuda").to(torch.int32)
     prefix, own = order[:lead].contiguous(), order[lead:].view(users, room).contiguous()
 
@@ -114,7 +130,8 @@ def serve(steps: int = 24, prefix_len: int = 5 * PAGE, prompts=(7, 33, 1, 20), s
 
     outs = []
     if graph:
-        keep = x.clone(), have.clone(), block.cache.k.clone(), block.cache.v.clone()
+        state = (x, have) + block.tensors()
+        keep = [t.clone() for t in state]
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):                              # once outside, as captures want it
@@ -123,7 +140,7 @@ def serve(steps: int = 24, prefix_len: int = 5 * PAGE, prompts=(7, 33, 1, 20), s
         captured = torch.cuda.CUDAGraph()
         with torch.cuda.graph(captured):
             q, o = step()
-        for dst, src in zip((x, have, block.cache.k, block.cache.v), keep):
+        for dst, src in zip(state, keep):
             dst.copy_(src)
         for _ in range(steps):
             captured.replay()
@@ -149,9 +166,10 @@ def check(state) -> float:
 
 
 if __name__ == "__main__":
-    outs, state = serve()
-    eager, _ = serve(graph=False)
-    same = all(torch.equal(a, b) for a, b in zip(outs, eager))
-    print(f"{len(outs)} steps of {outs[0].shape[0]} users over {state['prefix_len']} shared tokens; "
-          f"graph and eager {'agree bit for bit' if same else 'DIFFER'}; "
-          f"decode against prompt attention: {check(state):.4f} at most")
+    for codes in (False, True):
+        outs, state = serve(codes=codes)
+        eager, _ = serve(graph=False, codes=codes)
+        same = all(torch.equal(a, b) for a, b in zip(outs, eager))
+        print(f"{'8-bit' if codes else 'bf16'} cache: {len(outs)} steps of {outs[0].shape[0]} users over "
+              f"{state['prefix_len']} shared tokens; graph and eager {'agree bit for bit' if same else 'DIFFER'}; "
+              f"decode against prompt attention: {check(state):.4f} at most")
