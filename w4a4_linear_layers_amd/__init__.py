@@ -19,6 +19,7 @@ import numpy as np
 
 from . import _lib
 from ._lib import SERQ_BF16, SERQ_F32, SerqError, check
+from .attention import _current as _current_device, _stream as _raw_stream
 from .attention import (KvCache, KvCacheF8, attn_decode, attn_decode_workspace, attn_prefill, attn_prefill_workspace,
                         rope_append, rope_table)
 
@@ -592,40 +593,46 @@ def linear_i8(xq, sx, layer: I8Layer, *, out_dtype=None, out=None, workspace=Non
     import torch
     K, N, Wq, sw = layer.K, layer.N, layer.Wq, layer.sw
     dev = Wq.get_device()
-    if Wq.dtype != torch.int8 or Wq.shape != (N, K) or sw.dtype != torch.float32 or sw.shape != (N,):
+    if dev != _current_device() and dev >= 0:
+        with torch.cuda.device(dev):
+            return linear_i8(xq, sx, layer, out_dtype=out_dtype, out=out, workspace=workspace, debug=debug)
+    if Wq.dtype is not torch.int8 or Wq.shape != (N, K) or sw.dtype is not torch.float32 or sw.shape != (N,):
         raise ValueError("layer buffers do not match its sizes: Wq must be N x K int8 and sw N float32")
-    if xq.dim() != 2 or xq.shape[1] != K or xq.dtype != torch.int8:
+    shape = xq.shape
+    if len(shape) != 2 or shape[1] != K or xq.dtype is not torch.int8:
         raise ValueError(f"xq must be M x {K} int8")
-    M = xq.shape[0]
-    if sx.shape != (M,) or sx.dtype != torch.float32:
+    M = shape[0]
+    if sx.shape != (M,) or sx.dtype is not torch.float32:
         raise ValueError(f"sx must be ({M},) float32")
-    out_dtype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
-    if out_dtype == torch.bfloat16:
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    if out_dtype is torch.bfloat16:
         dt = SERQ_BF16
-    elif out_dtype == torch.float32:
+    elif out_dtype is torch.float32:
         dt = SERQ_F32
     else:
         raise ValueError("out_dtype must be float32 or bfloat16")
-    y = torch.empty((M, N), dtype=out_dtype, device=xq.device) if out is None else out
-    if y.shape != (M, N) or y.dtype != out_dtype:
+    y = sx.new_empty((M, N), dtype=out_dtype) if out is None else out
+    if y.shape != (M, N) or y.dtype is not out_dtype:
         raise ValueError(f"out must be a ({M}, {N}) {out_dtype} tensor")
     for t in (xq, sx, Wq, sw, y):
         if t.get_device() != dev or dev < 0 or not t.is_contiguous():
             raise ValueError("tensors must be contiguous and on one CUDA device")
-    need = lib.serq_linear_i8_workspace(M, K, N)
-    if need < 0:
+    size = lib.serq_linear_i8_workspace(M, K, N)
+    if size < 0:
         raise ValueError("sizes that the library does not take")
-    with torch.cuda.device(dev):
-        acc = torch.empty((M, N), dtype=torch.int32, device=xq.device) if debug else None
-        size = 0
-        if need:
-            if workspace is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=xq.device)
-            size = workspace.numel() * workspace.element_size()
-            if workspace.get_device() != dev or not workspace.is_contiguous() or size < need:
-                raise ValueError(f"workspace must be a contiguous CUDA tensor of {need} bytes or more on the layer's device")
-        status = lib.serq_linear_i8(xq.data_ptr(), sx.data_ptr(), Wq.data_ptr(), sw.data_ptr(), M, K, N, y.data_ptr(), dt,
-                                    acc.data_ptr() if debug else None, workspace.data_ptr() if need else None, size, _stream())
+    wp = None
+    if size:
+        need = size
+        if workspace is None:
+            workspace = xq.new_empty(need)
+        size = workspace.numel() * workspace.element_size()
+        if workspace.get_device() != dev or not workspace.is_contiguous() or size < need:
+            raise ValueError(f"workspace must be a contiguous CUDA tensor of {need} bytes or more on the layer's device")
+        wp = workspace.data_ptr()
+    acc = xq.new_empty((M, N), dtype=torch.int32) if debug else None
+    status = lib.serq_linear_i8(xq.data_ptr(), sx.data_ptr(), Wq.data_ptr(), sw.data_ptr(), M, K, N, y.data_ptr(), dt,
+                                acc.data_ptr() if debug else None, wp, size, _raw_stream(dev))
     if status:
         check("serq_linear_i8", status)
     return (y, acc) if debug else y

@@ -12,6 +12,7 @@
 
 #include "serq_i8.h"
 
+#include <atomic>
 #include <type_traits>
 #include <utility>
 
@@ -578,14 +579,28 @@ __global__ __launch_bounds__(256) void i8_generic_kernel(I8Args a) {
   }
 }
 
+// A kernel's dynamic LDS above 64 KB is allowed once per device (`done`: a bit each).
+hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  if (dev < 0 || dev >= 64) return hipErrorInvalidDevice;
+  const uint64_t bit = uint64_t{1} << dev;
+  if (done.load(std::memory_order_acquire) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
+
 template <int TN, int TM, int STAGES, int OCC>
 hipError_t launch_tile(const I8Args& a, const I8Plan& p, hipStream_t st) {
   constexpr int kLds = 64 * (TN + TM) * (STAGES * kKTile + 8);
   const int n_tiles = (a.N + 64 * TN - 1) / (64 * TN);
   const int tiles = n_tiles * ((a.M + 64 * TM - 1) / (64 * TM));
   auto* kernel = &i8_tile_kernel<TN, TM, STAGES, OCC>;
-  if (kLds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if constexpr (kLds > 64 * 1024) {
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), kLds, done);
     if (e != hipSuccess) return e;
   }
   const int groups = tiles < OCC * kCUs ? tiles : OCC * kCUs;
@@ -602,8 +617,9 @@ hipError_t launch_stream(const I8Args& a, hipStream_t st) {
   constexpr int kLds = STAGES * (RT + NT) * 16 * kWindow;
   static_assert(kLds * (OCC / 2) <= 160 * 1024, "LDS");
   auto* kernel = &i8_stream_kernel<RT, NT, STAGES, OCC>;
-  if (kLds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if constexpr (kLds > 64 * 1024) {
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), kLds, done);
     if (e != hipSuccess) return e;
   }
   kernel<<<dim3((a.N + 16 * RT - 1) / (16 * RT)), 64 * kStreamWaves, kLds, st>>>(a);
