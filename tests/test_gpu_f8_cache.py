@@ -435,6 +435,15 @@ def test_decode(dtype, lens, prefix, Hq, Hkv, D, page):
     run_decode(len(lens) + prefix, lens, prefix, Hq, Hkv, D, page, dtype)
 
 
+@pytest.mark.parametrize("lens,prefix,Hq,Hkv,D,page", [
+    ([9] * 70 + [0], 31800, 8, 2, 128, 16),
+    ([3] * 17, 22800, 48, 1, 64, 64),
+])
+def test_decode_after_a_long_prefix_of_codes(lens, prefix, Hq, Hkv, D, page):
+    """Enough work that the prefix goes to the tiles also where the cache holds codes."""
+    run_decode(7, lens, prefix, Hq, Hkv, D, page, torch.bfloat16)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_decode_strides_scale_and_loose_bound(dtype):
     run_decode(1, [20, 7], 40, 4, 2, 128, 16, dtype, scale=0.3, q_pad=64, o_pad=8)

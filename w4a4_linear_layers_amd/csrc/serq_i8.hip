@@ -108,7 +108,8 @@ __device__ __forceinline__ void static_for(F&& f) {
 // passes in windows of 512 bytes through STAGES places in LDS, by direct
 // global->LDS loads of two rows' 512 bytes each: whole lines, where an operand
 // loaded straight into registers takes 64 bytes of each of 16 rows and so half
-// of the rate into a compute unit (45 tokens, 14336 x 4096: 26 us). Wave w
+// of the rate into a compute unit (45 tokens, 14336 x 4096: 26 us against 19, 3.1
+// TB/s; one of 4096 x 28672 22 us, 5.3 TB/s, a large copy's rate). Wave w
 // multiplies bytes 64 w .. of each window, lane (row or token l = lane % 16, g =
 // lane / 16) with bytes 16 g of those, by v_mfma_i32_16x16x64_i8; the waves' sums
 // meet in LDS.
@@ -254,6 +255,15 @@ __device__ __forceinline__ void dma4(const void* sbase, uint32_t voff, uint32_t 
 // more, whose place the load of k-tile kt + STAGES takes. The loads stand
 // between products: issued at once, they would hold up the products until the
 // last is taken.
+//
+// 4000 tokens, 4096 x 28672: 540 us, 1.74 POPS (2.06 reached by the library's 8192^3
+// product on this card). Without the outputs' scaling and stores 378 us: the
+// products run at 2.5 POPS, near what the loads of 256 x 256 tiles allow (32 KB a
+// k-tile at some 32 bytes a clock into a compute unit, the products of a k-tile
+// 1024 clocks), and the rest is the epilogue, during which the matrix units
+// wait. Three places of k-tiles instead of four measure alike (564 us and 558),
+// with 128 x 128 up to 6 % more (512 tokens of 8192 x 8192 55 us and 52), with the
+// smaller four instead of eight 2 %.
 //
 // A tile's outputs are stored while the next tile's first k-tiles and its
 // scales are under way (the waits count loads, and stores after them make
@@ -662,12 +672,25 @@ I8Plan plan_linear_i8(int M, int K, int N) {
   if (M <= 64) {
     p.kind = I8Kernel::kStream;
     p.nt = static_cast<int>(ceil_div(M, 16));
-    p.rt = N >= 16384 && p.nt > 2 ? 2 : 1;
+    // Weights of two tiles a workgroup, which halves the reads of the tokens, where
+    // one tile each would make more workgroups than there are compute units: 45
+    // tokens of 4096 x 5120 in 6.9 us against 10.3, 64 of 4096 x 28672 in 36.5 against
+    // 47.9; with fewer, 45 of 14336 x 4096 take 22.8 us against 19.3. Few tokens are
+    // read quickly either way, and one tile leaves room for twice the workgroups:
+    // 16 of 4096 x 32768 in 25.3 us against 28.1, 8 in 25.1 against 25.6, one in 24.7
+    // against 24.1; 16 of 4096 x 10240 in 10.4 against 9.9.
+    p.rt = p.nt > 2 ? (N > 16 * kCUs ? 2 : 1) : (N >= 16384 && M > 8 ? 2 : 1);
     p.name = "stream";
     return p;
   }
-  const int64_t big = ceil_div(N, 256) * ceil_div(M, 256);
-  if (big >= 224) {
+  // Tiles of 256 x 256 take half the loads of 128 x 128 for a product, but go
+  // round the 256 compute units one each: two workgroups of the smaller take two
+  // thirds of a large tile's time. By rounds (8192 x 8192): 512 tokens 103 us in
+  // large tiles and 52 in small ones, 1024 106 and 97, 1280 121 and 134, 1536 123 and
+  // 139, 2048 141 and 185, 2304 224 and 202, 4352 348 and 370; 4096 x 28672: 256 tokens
+  // 67 and 55, 512 80 and 103, 1024 150 and 172.
+  const int64_t tiles = ceil_div(N, 128) * ceil_div(M, 128), big = ceil_div(N, 256) * ceil_div(M, 256);
+  if (3 * ceil_div(big, kCUs) < 2 * ceil_div(tiles, 2 * kCUs)) {
     p.kind = I8Kernel::kTile256;
     p.name = "tile256x256";
     return p;
@@ -678,7 +701,7 @@ I8Plan plan_linear_i8(int M, int K, int N) {
   // 128 x 128, 26.6 of 64 x 128). Long rows are cut in parts instead (128 x 14336 x
   // 4096: 25.7 us in eight parts, 29.3 in tiles of 64 x 64 and two; 128 x 8192 x
   // 8192 27.2 in four and 27.5 in tiles of 64 x 64).
-  const int64_t tiles = ceil_div(N, 128) * ceil_div(M, 128), quarters = ceil_div(N, 64) * ceil_div(M, 64);
+  const int64_t quarters = ceil_div(N, 64) * ceil_div(M, 64);
   if (tiles < 150 && k_tiles <= 160) {
     p.kind = quarters <= 256 ? I8Kernel::kTile64 : I8Kernel::kTile64x128;
     p.name = quarters <= 256 ? "tile64x64" : "tile64x128";
