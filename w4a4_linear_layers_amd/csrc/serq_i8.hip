@@ -243,8 +243,10 @@ __device__ __forceinline__ void dma4(const void* sbase, uint32_t voff, uint32_t 
 #pragma clang diagnostic pop
 
 // A tile of 64 TN channels by 64 TM tokens: 2 x 2 waves of TN x TM blocks of 32 x 32
-// (v_mfma_i32_32x32x32_i8), over one part of K. A workgroup takes tiles one
-// after another.
+// (v_mfma_i32_32x32x32_i8), over all of K or, with PARTS, one part of it. A
+// workgroup takes tiles one after another. (With both ways of storing, 256 x 256
+// kept addresses in scratch memory, whose loads wait for those of the next
+// tile: 4000 tokens of 4096 x 28672 in 532 us against 460.)
 //
 // K passes in k-tiles of 64 bytes through STAGES places in LDS, by direct
 // global->LDS loads. Lane half h of a block's operands holds bytes 32 h .. + 31
@@ -256,19 +258,19 @@ __device__ __forceinline__ void dma4(const void* sbase, uint32_t voff, uint32_t 
 // between products: issued at once, they would hold up the products until the
 // last is taken.
 //
-// 4000 tokens, 4096 x 28672: 540 us, 1.74 POPS (2.06 reached by the library's 8192^3
-// product on this card). Without the outputs' scaling and stores 378 us: the
-// products run at 2.5 POPS, near what the loads of 256 x 256 tiles allow (32 KB a
-// k-tile at some 32 bytes a clock into a compute unit, the products of a k-tile
-// 1024 clocks), and the rest is the epilogue, during which the matrix units
-// wait. Three places of k-tiles instead of four measure alike (564 us and 558),
+// 4000 tokens, 4096 x 28672: 460 us, 2.04 POPS (the library's 8192^3 product reaches
+// 2.06 on this card). Without the outputs' scaling and stores 378 us: the products
+// run at 2.5 POPS, near what the loads of 256 x 256 tiles allow (32 KB a k-tile at
+// some 32 bytes a clock into a compute unit, the products of a k-tile 1024
+// clocks), and the rest is the epilogue, during which the matrix units wait.
+// Three places of k-tiles instead of four measure alike (564 us and 558),
 // with 128 x 128 up to 6 % more (512 tokens of 8192 x 8192 55 us and 52), with the
 // smaller four instead of eight 2 %.
 //
 // A tile's outputs are stored while the next tile's first k-tiles and its
 // scales are under way (the waits count loads, and stores after them make
 // them wait for a little more, never for less).
-template <int TN, int TM, int STAGES, int OCC>
+template <int TN, int TM, int STAGES, int OCC, bool PARTS>
 __global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles, int tiles, int per) {
   constexpr int BN = 64 * TN, BM = 64 * TM;
   constexpr int kW = BN * kKTile, kStage = (BN + BM) * kKTile, CPW = TN + TM;
@@ -543,8 +545,12 @@ __global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles
       set ^= 1;
       begin(set);
     }
-    if (a.partial) store_parts(nn, mm);
-    else store_tile(nn, mm, now);
+    if constexpr (PARTS) {
+      if (a.partial) store_parts(nn, mm);
+      else store_tile(nn, mm, now);
+    } else {
+      store_tile(nn, mm, now);
+    }
     if (!more) break;
   }
 }
@@ -602,12 +608,12 @@ hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done)
   return e;
 }
 
-template <int TN, int TM, int STAGES, int OCC>
+template <int TN, int TM, int STAGES, int OCC, bool PARTS>
 hipError_t launch_tile(const I8Args& a, const I8Plan& p, hipStream_t st) {
   constexpr int kLds = 64 * (TN + TM) * (STAGES * kKTile + 8);
   const int n_tiles = (a.N + 64 * TN - 1) / (64 * TN);
   const int tiles = n_tiles * ((a.M + 64 * TM - 1) / (64 * TM));
-  auto* kernel = &i8_tile_kernel<TN, TM, STAGES, OCC>;
+  auto* kernel = &i8_tile_kernel<TN, TM, STAGES, OCC, PARTS>;
   if constexpr (kLds > 64 * 1024) {
     static std::atomic<uint64_t> done{0};
     const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), kLds, done);
@@ -726,10 +732,10 @@ hipError_t launch_linear_i8(const I8Args& a, const I8Plan& p, hipStream_t st) {
   switch (p.kind) {
     case I8Kernel::kStream:
       return launch_stream_tokens(a, p.rt, p.nt, st);
-    case I8Kernel::kTile256: return launch_tile<4, 4, 4, 1>(a, p, st);
-    case I8Kernel::kTile128: return launch_tile<2, 2, 4, 2>(a, p, st);
-    case I8Kernel::kTile64x128: return launch_tile<1, 2, 6, 2>(a, p, st);
-    case I8Kernel::kTile64: return launch_tile<1, 1, 8, 2>(a, p, st);
+    case I8Kernel::kTile256: return launch_tile<4, 4, 4, 1, false>(a, p, st);
+    case I8Kernel::kTile128: return launch_tile<2, 2, 4, 2, true>(a, p, st);
+    case I8Kernel::kTile64x128: return launch_tile<1, 2, 6, 2, false>(a, p, st);
+    case I8Kernel::kTile64: return launch_tile<1, 1, 8, 2, false>(a, p, st);
     default: break;
   }
   const int64_t blocks = ceil_div(static_cast<int64_t>(a.M) * a.N, 256);
