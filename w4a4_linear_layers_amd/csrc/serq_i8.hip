@@ -242,6 +242,15 @@ __device__ __forceinline__ void dma4(const void* sbase, uint32_t voff, uint32_t 
 }
 #pragma clang diagnostic pop
 
+// The lane's number, found again where it is used: what depends on it alone the
+// compiler would otherwise keep over the products, in scratch memory, whose
+// loads wait for the tiles' under way.
+__device__ __forceinline__ int lane_again() {
+  int n;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(n));
+  return n;
+}
+
 // A tile of 64 TN channels by 64 TM tokens: 2 x 2 waves of TN x TM blocks of 32 x 32
 // (v_mfma_i32_32x32x32_i8), over all of K or, with PARTS, one part of it. A
 // workgroup takes tiles one after another. (With both ways of storing, 256 x 256
@@ -258,7 +267,7 @@ __device__ __forceinline__ void dma4(const void* sbase, uint32_t voff, uint32_t 
 // between products: issued at once, they would hold up the products until the
 // last is taken.
 //
-// 4000 tokens, 4096 x 28672: 460 us, 2.04 POPS (the library's 8192^3 product reaches
+// 4000 tokens, 4096 x 28672: 439 us, 2.14 POPS (the library's 8192^3 product reaches
 // 2.06 on this card). Without the outputs' scaling and stores 378 us: the products
 // run at 2.5 POPS, near what the loads of 256 x 256 tiles allow (32 KB a k-tile at
 // some 32 bytes a clock into a compute unit, the products of a k-tile 1024
@@ -267,6 +276,11 @@ __device__ __forceinline__ void dma4(const void* sbase, uint32_t voff, uint32_t 
 // with 128 x 128 up to 6 % more (512 tokens of 8192 x 8192 55 us and 52), with the
 // smaller four instead of eight 2 %.
 //
+// bf16 outputs of 256 x 256 go by whole lines through LDS, 64 channels of a token
+// side by side, instead of 32 bytes of a row at a time: 439 us against 460. The
+// smaller tiles store as they are (1024 tokens of 8192 x 8192 in 128 x 128: 96 us, 101
+// through LDS).
+//
 // A tile's outputs are stored while the next tile's first k-tiles and its
 // scales are under way (the waits count loads, and stores after them make
 // them wait for a little more, never for less).
@@ -274,7 +288,9 @@ template <int TN, int TM, int STAGES, int OCC, bool PARTS>
 __global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles, int tiles, int per) {
   constexpr int BN = 64 * TN, BM = 64 * TM;
   constexpr int kW = BN * kKTile, kStage = (BN + BM) * kKTile, CPW = TN + TM;
-  constexpr int kScales = STAGES * kStage, kScaleBytes = 4 * (BN + BM);        // two sets of scales after the places
+  constexpr int kScales = STAGES * kStage, kScaleBytes = 4 * (BN + BM);        // two sets of scales after the places,
+  constexpr bool kThroughLds = TN == 4;
+  constexpr int kOut = kScales + 2 * kScaleBytes, kOutBytes = 4096;            // then a place of each wave for outputs
   static_assert(CPW * (STAGES - 1) < 64, "vmcnt range");
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
@@ -295,6 +311,8 @@ __global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles
   const int8_t* xsrc = nullptr;
   uint32_t woff[TN], xoff[TM];
   const auto take = [&](int tile) SERQ_INLINE {
+    const int ln = lane_again();
+    const int part = (ln & 3) ^ swz64(ln >> 2);
     int tn, tm;
     tile_coords(tile, tiles, n_tiles, tn, tm);
     n0 = __builtin_amdgcn_readfirstlane(tn * BN);
@@ -303,12 +321,12 @@ __global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles
     xsrc = a.Xq + static_cast<int64_t>(m0) * a.K + static_cast<int64_t>(kt0) * kKTile;
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
-      const int row = (wave * TN + i) * 16 + (lane >> 2), last = a.N - 1 - n0;
+      const int row = (wave * TN + i) * 16 + (ln >> 2), last = a.N - 1 - n0;
       woff[i] = static_cast<uint32_t>(row < last ? row : last) * a.K + part * 16;
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      const int row = (wave * TM + i) * 16 + (lane >> 2), last = a.M - 1 - m0;
+      const int row = (wave * TM + i) * 16 + (ln >> 2), last = a.M - 1 - m0;
       xoff[i] = static_cast<uint32_t>(row < last ? row : last) * a.K + part * 16;
     }
   };
@@ -337,6 +355,7 @@ __global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles
   // The scales of the tile (of channels and tokens that are there) into set
   // `set`, then its first k-tiles.
   const auto begin = [&](int set) SERQ_INLINE {
+    const int lane = lane_again();
     const uint32_t to = lds_base + kScales + set * kScaleBytes;
     if (wave == 0) {
 #pragma unroll
@@ -458,6 +477,8 @@ __global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles
     }
   };
   const auto store_tile = [&](int nn, int mm, int set) SERQ_INLINE {
+    const int ln = lane_again();
+    const int l32 = ln & 31, h = ln >> 5;
     const float* ssw = reinterpret_cast<const float*>(lds + kScales + set * kScaleBytes);
     const float* ssx = ssw + BN;
     float sx[TM];
@@ -469,13 +490,53 @@ __global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles
       m[j] = mm + row;
     }
     const bool pairs = a.y_bf16 && (a.N & 7) == 0 && !a.dbg;
+    if (kThroughLds && pairs) {
+      // 32 tokens by 64 channels at a time.
+      const int r8 = ln >> 3, c8 = ln & 7;
+      uint8_t* const mine = lds + kOut + wave * kOutBytes;
+      __bf16* const base = static_cast<__bf16*>(a.Y) + static_cast<int64_t>(mm) * a.N + nn;
+#pragma unroll
+      for (int i = 0; i < TN; i += 2) {
+        const int c = (wn * TN + i) * 32 + 8 * c8;
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+#pragma unroll
+          for (int b = 0; b < 8; b += 2) {                 // blocks of eight channels, two at a time
+            uint32_t w[2][2];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const int k = i + (b + v) / 4, q = (b + v) % 4;
+              const f32x4 sw = *reinterpret_cast<const f32x4*>(ssw + (wn * TN + k) * 32 + 8 * q + 4 * h);
+              float y[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e] = sx[j] * (sw[e] * static_cast<float>(acc[k][j][4 * q + e]));
+              w[v][0] = pack_bf16x2(y[0], y[1]);
+              w[v][1] = pack_bf16x2(y[2], y[3]);
+            }
+            const auto lo = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+            const auto hi = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+            *reinterpret_cast<u32x4*>(mine + l32 * 128 + (((b + h) ^ (l32 & 7)) << 4)) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+            asm volatile("" ::: "memory");
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = (wm * TM + j) * 32 + 8 * r + r8;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(mine + (8 * r + r8) * 128 + ((c8 ^ r8) << 4));
+            if (mm + row < a.M && nn + c < a.N) *reinterpret_cast<u32x4*>(base + static_cast<int64_t>(row) * a.N + c) = v;
+          }
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
       const int c0 = (wn * TN + i) * 32;
       f32x4 sw[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) sw[q] = *reinterpret_cast<const f32x4*>(ssw + c0 + 8 * q + 4 * h);
-      if (pairs) {
+      if (!kThroughLds && pairs) {
         // Lane half h holds channels 8 q + 4 h .. + 3: with the halves of two q
         // exchanged, each lane has eight channels side by side.
 #pragma unroll
@@ -610,7 +671,7 @@ hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done)
 
 template <int TN, int TM, int STAGES, int OCC, bool PARTS>
 hipError_t launch_tile(const I8Args& a, const I8Plan& p, hipStream_t st) {
-  constexpr int kLds = 64 * (TN + TM) * (STAGES * kKTile + 8);
+  constexpr int kLds = 64 * (TN + TM) * (STAGES * kKTile + 8) + (TN == 4 ? 4 * 4096 : 0);
   const int n_tiles = (a.N + 64 * TN - 1) / (64 * TN);
   const int tiles = n_tiles * ((a.M + 64 * TM - 1) / (64 * TM));
   auto* kernel = &i8_tile_kernel<TN, TM, STAGES, OCC, PARTS>;
@@ -690,13 +751,14 @@ I8Plan plan_linear_i8(int M, int K, int N) {
     return p;
   }
   // Tiles of 256 x 256 take half the loads of 128 x 128 for a product, but go
-  // round the 256 compute units one each: two workgroups of the smaller take two
-  // thirds of a large tile's time. By rounds (8192 x 8192): 512 tokens 103 us in
-  // large tiles and 52 in small ones, 1024 106 and 97, 1280 121 and 134, 1536 123 and
-  // 139, 2048 141 and 185, 2304 224 and 202, 4352 348 and 370; 4096 x 28672: 256 tokens
-  // 67 and 55, 512 80 and 103, 1024 150 and 172.
+  // round the 256 compute units one each: two of the smaller side by side take
+  // two thirds or more of a large tile's time. 8192 x 8192: 512 tokens 94 us in large
+  // tiles and 52 in small ones, 1024 97 and 96, 1280 101 and 122, 2048 126 and 178, 2304
+  // 196 and 197, 2900 208 and 244, 4352 309 and 355; 4096 x 28672: 256 tokens 59 and 53,
+  // 300 61 and 66, 512 67 and 96, 700 117 and 131; 4096 x 8192: 1024 tokens 49 and 45,
+  // 2304 106 and 98, 2900 110 and 123.
   const int64_t tiles = ceil_div(N, 128) * ceil_div(M, 128), big = ceil_div(N, 256) * ceil_div(M, 256);
-  if (3 * ceil_div(big, kCUs) < 2 * ceil_div(tiles, 2 * kCUs)) {
+  if (3 * ceil_div(big, kCUs) <= 2 * ceil_div(tiles, 2 * kCUs)) {
     p.kind = I8Kernel::kTile256;
     p.name = "tile256x256";
     return p;
