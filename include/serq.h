@@ -468,7 +468,7 @@ int serq_linear_mx(const uint8_t* Xq, const uint8_t* Xsc,
  * serq_quant_act and serq_silu_mul_quant_act with a_bits 8; Wq, N x K int8,
  * row n the codes of fl32(s_j W[j, n]) (qmax 127); sw, N floats.
  * Errors: SERQ_EINVAL (NULL W or output, K or N <= 0, alpha outside [0, 1],
- * bad w_dtype).
+ * bad w_dtype), SERQ_EUNSUPPORTED (no host memory for K floats).
  */
 int serq_calibrate_i8(const void* W, serq_dtype w_dtype, int K, int N, const float* act_absmax, float alpha,
                       float* s_hat_inv, int8_t* Wq, float* sw);

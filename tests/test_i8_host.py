@@ -48,6 +48,14 @@ def test_calibrate(K, N, alpha, smooth):
         assert not L.Wq[3].any() and L.sw[3] == 0
 
 
+@pytest.mark.parametrize("K,N", [(16, 255), (5, 256), (7, 257), (3, 4100), (2, 16 * 256 + 17), (40, 1000)])
+def test_calibrate_over_blocks_of_columns_and_threads(K, N):
+    W = np.random.default_rng(N).standard_normal((K, N)).astype(np.float32)
+    L = S.calibrate_i8(W, None)
+    shi, Wq, sw = plain(W, None, 0.5)
+    assert np.array_equal(L.s_hat_inv, shi) and np.array_equal(L.Wq, Wq) and np.array_equal(L.sw, sw)
+
+
 def test_calibrate_other_exponents_and_types():
     li = make_layer(64, 48, 1, n_out=2, factor=20.0, seed=5, tag=1)
     for alpha in (0.0, 0.25, 1.0):

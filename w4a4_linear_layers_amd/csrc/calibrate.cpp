@@ -21,6 +21,9 @@
 #include <cfloat>
 #include <cmath>
 #include <cstring>
+#include <exception>
+#include <memory>
+#include <new>
 #include <numeric>
 #include <thread>
 #include <vector>
@@ -52,6 +55,7 @@ struct Quantizer {
   float scale;
   float inv;
   bool zero;
+  Quantizer() : Quantizer(0.0f, 1.0f) {}
   Quantizer(float m, float qmax) {
     inv = qmax / m;
     zero = !(inv <= FLT_MAX);  // +inf: m == 0 or too small to invert
@@ -206,22 +210,25 @@ extern "C" int serq_calibrate(const void* W, serq_dtype w_dtype, int K, int N,
 
 namespace {
 
-// Output columns [n0, n1) of the layer in 8 bits, rows in their own order.
-void calibrate_i8_columns(const WeightView& W, int K, const float* s, int n0, int n1, int8_t* Wq, float* sw) {
-  const int nb = n1 - n0;
-  if (nb <= 0) return;
-  std::vector<float> cmax(nb, 0.0f);
-  for (int j = 0; j < K; ++j)
-    for (int c = 0; c < nb; ++c) cmax[c] = std::max(cmax[c], std::fabs(s[j] * W.at(j, n0 + c)));
-  std::vector<Quantizer> q;
-  q.reserve(nb);
-  for (int c = 0; c < nb; ++c) {
-    q.emplace_back(cmax[c], 127.0f);
-    sw[n0 + c] = q[c].scale;
+// Output columns [n0, n1) of the layer in 8 bits, rows in their own order, 256
+// columns at a time; sw holds their maxima first. (Nothing here is allocated.)
+void calibrate_i8_columns(const WeightView& W, int K, const float* s, int n0, int n1, int8_t* Wq, float* sw) noexcept {
+  constexpr int kColumns = 256;
+  Quantizer q[kColumns];
+  for (; n0 < n1; n0 += kColumns) {
+    const int nb = std::min(n1 - n0, kColumns);
+    std::fill(sw + n0, sw + n0 + nb, 0.0f);
+    for (int j = 0; j < K; ++j)
+      for (int c = 0; c < nb; ++c) sw[n0 + c] = std::max(sw[n0 + c], std::fabs(s[j] * W.at(j, n0 + c)));
+    for (int c = 0; c < nb; ++c) {
+      q[c] = Quantizer(sw[n0 + c], 127.0f);
+      sw[n0 + c] = q[c].scale;
+    }
+    for (int j = 0; j < K; ++j)
+      for (int c = 0; c < nb; ++c)
+        Wq[static_cast<size_t>(n0 + c) * K + j] = static_cast<int8_t>(q[c].code(s[j] * W.at(j, n0 + c), -127, 127));
+    if (n1 - n0 <= kColumns) break;
   }
-  for (int j = 0; j < K; ++j)
-    for (int c = 0; c < nb; ++c)
-      Wq[static_cast<size_t>(n0 + c) * K + j] = static_cast<int8_t>(q[c].code(s[j] * W.at(j, n0 + c), -127, 127));
 }
 
 }  // namespace
@@ -232,19 +239,26 @@ extern "C" int serq_calibrate_i8(const void* W, serq_dtype w_dtype, int K, int N
   if (w_dtype != SERQ_F32 && w_dtype != SERQ_BF16) return SERQ_EINVAL;
   if (K <= 0 || N <= 0 || !(alpha >= 0.0f && alpha <= 1.0f)) return SERQ_EINVAL;
   const WeightView wv{W, w_dtype, N};
-  std::vector<float> s(K, 1.0f);
+  const std::unique_ptr<float[]> s(new (std::nothrow) float[K]);
+  if (!s) return SERQ_EUNSUPPORTED;
+  std::fill(s.get(), s.get() + K, 1.0f);
   std::fill(s_hat_inv, s_hat_inv + K, 1.0f);
-  if (act_absmax) smoothing_factors(wv, K, N, act_absmax, alpha, s.data(), s_hat_inv);
+  if (act_absmax) smoothing_factors(wv, K, N, act_absmax, alpha, s.get(), s_hat_inv);
   const int T = worker_count(N);
-  const int per = (N + T - 1) / T;
-  std::vector<std::thread> pool;
-  for (int t = 1; t < T; ++t) {
-    const int n0 = t * per, n1 = std::min(N, n0 + per);
-    if (n0 >= n1) break;
-    pool.emplace_back(calibrate_i8_columns, std::cref(wv), K, s.data(), n0, n1, Wq, sw);
+  const int per = N / T + (N % T != 0);
+  std::thread pool[16];
+  int done = N;                                   // columns [done, N) have a thread
+  try {
+    for (int t = T - 1; t > 0; --t) {
+      const int n0 = static_cast<int>(std::min<int64_t>(N, static_cast<int64_t>(t) * per));
+      if (n0 < done) pool[t] = std::thread(calibrate_i8_columns, std::cref(wv), K, s.get(), n0, done, Wq, sw);
+      done = n0;
+    }
+  } catch (const std::exception&) {               // no more threads: the rest here
   }
-  calibrate_i8_columns(wv, K, s.data(), 0, std::min(N, per), Wq, sw);
-  for (auto& th : pool) th.join();
+  calibrate_i8_columns(wv, K, s.get(), 0, done, Wq, sw);
+  for (auto& th : pool)
+    if (th.joinable()) th.join();
   return SERQ_OK;
 }
 
