@@ -656,6 +656,8 @@ __global__ __launch_bounds__(256) void i8_generic_kernel(I8Args a) {
   }
 }
 
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 // A kernel's dynamic LDS above 64 KB is allowed once per device (`done`: a bit each).
 hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
   int dev = 0;
@@ -672,8 +674,8 @@ hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done)
 template <int TN, int TM, int STAGES, int OCC, bool PARTS>
 hipError_t launch_tile(const I8Args& a, const I8Plan& p, hipStream_t st) {
   constexpr int kLds = 64 * (TN + TM) * (STAGES * kKTile + 8) + (TN == 4 ? 4 * 4096 : 0);
-  const int n_tiles = (a.N + 64 * TN - 1) / (64 * TN);
-  const int tiles = n_tiles * ((a.M + 64 * TM - 1) / (64 * TM));
+  const int n_tiles = static_cast<int>(ceil_div(a.N, 64 * TN));
+  const int tiles = n_tiles * static_cast<int>(ceil_div(a.M, 64 * TM));
   auto* kernel = &i8_tile_kernel<TN, TM, STAGES, OCC, PARTS>;
   if constexpr (kLds > 64 * 1024) {
     static std::atomic<uint64_t> done{0};
@@ -721,8 +723,6 @@ hipError_t launch_stream_tokens(const I8Args& a, int rt, int nt, hipStream_t st)
     default: return launch_stream<1, 4, 4, 2>(a, st);
   }
 }
-
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
