@@ -27,8 +27,8 @@
 // another 12000.
 //
 // A cache of FP8 codes (F8): 12000 tokens of 32 query and 8 key/value heads 1.06
-// ms, 1.11 PFLOP/s, where a bf16 cache takes 1.00: making bf16 of the codes is
-// the vector unit's, beside the softmax.
+// ms, 1.11 PFLOP/s, where a bf16 cache takes 1.00: the codes go through registers
+// into LDS, beside the softmax and the products, instead of straight there.
 
 #include <type_traits>
 

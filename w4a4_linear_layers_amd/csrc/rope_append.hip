@@ -352,8 +352,8 @@ __global__ __launch_bounds__(64) void rope_append_scalar_kernel(RopeArgs a) {
 // in 64 bits and rounded to fp32 once, so that a cache does not depend on the
 // order of a sum: next to the border of two codes, or of two scales, the last
 // bit of a key would decide. What that costs shows beside the values, which are
-// coded as they are: 8192 tokens of 8 normed heads of 128 on three axes take 18 us
-// for the keys, 10 for the values (and 28 for 32 heads of queries, at 4.8 TB/s).
+// coded as they are: 8192 tokens of 8 normed heads of 128 take 19 us for the keys,
+// 10 for the values (and 28 for 32 heads of queries, at 4.8 TB/s).
 
 // Least exponent >= kLeast with |y| <= 448 * 2^e for the finite fp32 number of bits `top`.
 constexpr int kLeast = -117, kMost = 120;

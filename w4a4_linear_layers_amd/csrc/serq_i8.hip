@@ -108,8 +108,8 @@ __device__ __forceinline__ void static_for(F&& f) {
 // passes in windows of 512 bytes through STAGES places in LDS, by direct
 // global->LDS loads of two rows' 512 bytes each: whole lines, where an operand
 // loaded straight into registers takes 64 bytes of each of 16 rows and so half
-// of the rate into a compute unit (45 tokens, 14336 x 4096: 26 us against 19, 3.1
-// TB/s; one of 4096 x 28672 22 us, 5.3 TB/s, a large copy's rate). Wave w
+// of the rate into a compute unit (45 tokens, 14336 x 4096, weights from HBM: 26 us
+// against 19, 3.1 TB/s; one of 4096 x 28672 22 us, 5.3 TB/s, a large copy's rate). Wave w
 // multiplies bytes 64 w .. of each window, lane (row or token l = lane % 16, g =
 // lane / 16) with bytes 16 g of those, by v_mfma_i32_16x16x64_i8; the waves' sums
 // meet in LDS.
