@@ -33,7 +33,8 @@ def rotate_all(x, w, eps, table, pos):
 
 @TYPES
 @pytest.mark.parametrize("M,Hkv,D,rot,norm,lead", [(4096, 2, 128, 128, True, 0), (4211, 3, 64, 64, True, 5), (5003, 5, 128, 64, False, 9),
-                                                   (4100, 1, 64, 0, True, 15), (2500, 2, 128, 128, True, 11)])
+                                                   (4100, 1, 64, 0, True, 15), (2500, 2, 128, 128, True, 11),
+                                                   (2047, 3, 128, 64, True, 6), (2048, 3, 64, 64, False, 2)])
 def test_append_of_many_tokens(dtype, M, Hkv, D, rot, norm, lead):
     """Prompts one after another, each in pages of its own, that begin `lead` tokens inside a block they share with
     earlier ones, so that runs cross windows in every way; some end with a row of padding."""

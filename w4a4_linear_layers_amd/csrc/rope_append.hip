@@ -353,7 +353,8 @@ __global__ __launch_bounds__(64) void rope_append_scalar_kernel(RopeArgs a) {
 // order of a sum: next to the border of two codes, or of two scales, the last
 // bit of a key would decide. What that costs shows beside the values, which are
 // coded as they are: 8192 tokens of 8 normed heads of 128 take 19 us for the keys,
-// 10 for the values (and 28 for 32 heads of queries, at 4.8 TB/s).
+// 10 for the values, each alone (24 in one launch; 28 for 32 heads of queries, at 4.8
+// TB/s).
 
 // Least exponent >= kLeast with |y| <= 448 * 2^e for the finite fp32 number of bits `top`.
 constexpr int kLeast = -117, kMost = 120;
@@ -738,12 +739,19 @@ __global__ __launch_bounds__(kThreads) void rope_append_f8_kernel(RopeArgs a, in
   }
 }
 
-// Keys alone, or values alone: each with the registers that it needs.
-template <typename T, int D, bool INTER, bool NORM, int HB, bool VALUE>
-__global__ __launch_bounds__(kThreads) void store_f8_kernel(RopeArgs a, int first) {
-  constexpr int EACH = HB * heads_side_by_side<T, D>();
-  const int parts = (a.Hkv + EACH - 1) / EACH;
-  store_codes<T, D, INTER, NORM, true, HB, VALUE>(a, first / 16 + blockIdx.x / parts, blockIdx.x % parts * EACH);
+// Keys and values without the queries: `keys` workgroups of KB heads' keys, then
+// those of VB heads' values.
+template <typename T, int D, bool INTER, bool NORM, int KB, int VB>
+__global__ __launch_bounds__(kThreads) void store_f8_kernel(RopeArgs a, int first, int keys) {
+  constexpr int EACH = heads_side_by_side<T, D>();
+  const int b = blockIdx.x;
+  if (b < keys) {
+    const int parts = (a.Hkv + KB * EACH - 1) / (KB * EACH);
+    store_codes<T, D, INTER, NORM, true, KB, false>(a, first / 16 + b / parts, b % parts * (KB * EACH));
+  } else {
+    const int parts = (a.Hkv + VB * EACH - 1) / (VB * EACH), x = b - keys;
+    store_codes<T, D, false, false, true, VB, true>(a, first / 16 + x / parts, x % parts * (VB * EACH));
+  }
 }
 
 // A workgroup per set of heads, or per three sets where many tokens are normed:
@@ -793,14 +801,18 @@ hipError_t launch_by_dim(const RopeArgs& a, hipStream_t st) {
   return a.D == 64 ? launch_typed<T, 64, AXES>(a, st) : launch_typed<T, 128, AXES>(a, st);
 }
 
-// Tokens [first, first + tokens) of a call onto a cache of codes: keys, values
-// and queries in one launch, or in one each where many tokens make that cost
-// little and each its own registers and sets of heads gain more (32 and 8 normed
-// heads of 128, bf16: 256 tokens 4.8 us in one launch, 13.1 in three; 2048 21.4 and
-// 21.6; 4096 39.4 and 31.9; 8192 75 and 53; fp32 2048 31.1 and 31.0, 8192 138 and 104).
-// Heads of a workgroup then, which load what depends on the token once: two of
-// keys (8192 tokens 18.4 us, one 22.3, four 21.1) and four of values (9.7, two
-// alike, one 11.2).
+// From so many tokens on, keys and values of a call onto a cache of codes take a
+// launch and the queries another, each with its own registers and heads of a
+// workgroup: 32 and 8 normed heads of 128, bf16, 1024 tokens 11.5 us in one
+// launch; 2048 21.3 in one and 17.4 in two; 4096 39.4 and 27.8; 8192 75 and 48;
+// fp32 2048 31.1 and 25.8, 8192 138 and 96. (Keys and values in a launch each: 8192
+// 52; all in one with these heads 51, without norms 57 against 44.)
+constexpr int kManyStored = 2048;
+
+// Tokens [first, first + tokens) of a call onto a cache of codes. Where they are
+// many, a workgroup takes two heads of keys (alone 8192 tokens 18.4 us, one head
+// 22.3, four 21.1) or four of values (9.7, two alike, one 11.2), which load what
+// depends on the token once.
 template <typename T, int D, bool INTER, bool NORM>
 hipError_t launch_f8(const RopeArgs& a, int first, int tokens, hipStream_t st) {
   constexpr int GROUPS = kThreads / (D / Elem<T>::kVec), KB = 2, VB = 4;
@@ -819,15 +831,16 @@ hipError_t launch_f8(const RopeArgs& a, int first, int tokens, hipStream_t st) {
     x.Hkv = 0;
     return x;
   };
-  const bool vector = vector_path<T>(a), many = tokens >= kManyTokens;
+  const bool vector = vector_path<T>(a), many = tokens >= kManyStored;
   if (vector && !many) {
     rope_append_f8_kernel<T, D, INTER, NORM, true>
         <<<dim3(static_cast<unsigned>(2 * stores(1) + static_cast<int64_t>(tokens) * sets)), kThreads, 0, st>>>(a, first, tokens, sets);
     return hipGetLastError();
   }
   if (vector) {
-    store_f8_kernel<T, D, INTER, NORM, KB, false><<<dim3(static_cast<unsigned>(stores(KB))), kThreads, 0, st>>>(a, first);
-    store_f8_kernel<T, D, false, false, VB, true><<<dim3(static_cast<unsigned>(stores(VB))), kThreads, 0, st>>>(a, first);
+    const int keys = static_cast<int>(stores(KB));
+    store_f8_kernel<T, D, INTER, NORM, KB, VB>
+        <<<dim3(static_cast<unsigned>(keys + stores(VB))), kThreads, 0, st>>>(a, first, keys);
   } else {
     rope_append_f8_kernel<T, D, INTER, NORM, false><<<dim3(static_cast<unsigned>(2 * stores(1))), kThreads, 0, st>>>(a, first, tokens, 0);
   }
