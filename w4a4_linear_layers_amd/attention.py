@@ -181,6 +181,9 @@ _stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
 _current = getattr(getattr(torch, "_C", None), "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
 
 
+_AXES = bytes(range(4))
+
+
 # The checks below run on every call of a decoding step, where a handful of
 # microseconds is what the kernels take: each attribute is read once.
 
@@ -277,7 +280,7 @@ def rope_append(qkv, n_heads: int, cache, pos, slot, table, *, layout: str = "ha
                 tp, pp = table.data_ptr(), _ints(pos, (M,), dev, "pos")
             else:
                 axes, n_axes = bytes(pair_axis), pos.shape[0] if pos.dim() == 2 else 0
-                if len(axes) != rot // 2 or not 1 <= n_axes <= 4 or max(axes) >= n_axes:
+                if len(axes) != rot // 2 or not 1 <= n_axes <= 4 or axes.translate(None, _AXES[:n_axes]):
                     raise ValueError(f"pair_axis must hold {rot // 2} axes and pos a row of {M} for each (four at most)")
                 tp, pp = table.data_ptr(), _ints(pos, (n_axes, M), dev, "pos")
     qw = None if q_norm is None else _norm(q_norm, D, dev)
