@@ -500,8 +500,8 @@ int serq_linear_i8(const int8_t* Xq, const float* sx, const int8_t* Wq, const fl
 int64_t serq_linear_i8_workspace(int M, int K, int N);
 
 /* Which kernel serq_linear_i8 launches for these sizes (static string:
- * "stream", "tile64x64", "tile64x128", "tile128x128", "tile256x256" or
- * "generic"), or NULL for invalid sizes. Host only. */
+ * "stream", "tile64x64", "tile64x128", "tile128x128", "tile256x128",
+ * "tile256x256" or "generic"), or NULL for invalid sizes. Host only. */
 const char* serq_linear_i8_kernel_name(int M, int K, int N);
 
 /*

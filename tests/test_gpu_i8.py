@@ -64,6 +64,7 @@ def test_linear(dtype, M, K, N):
     (8, 1040, 16401), (9, 1040, 16401), (16, 2576, 16384), (17, 528, 16390), (32, 16, 20001),      # tokens in one part or two
     (33, 2064, 4096), (33, 2064, 4097), (48, 528, 4111), (49, 4624, 5000), (64, 16, 4112), (64, 3088, 7003),
     (300, 64, 28600), (513, 80, 16385), (2305, 16, 8192),                     # rounds of the larger tiles or of the smaller
+    (520, 80, 8200), (129, 336, 20001), (1100, 528, 4100), (1025, 64, 4096), (1030, 2000, 4098),     # 256 x 128
 ])
 def test_linear_where_the_tiles_change(dtype, M, K, N):
     run(M, K, N, dtype)

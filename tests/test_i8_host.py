@@ -93,6 +93,7 @@ def test_plans():
     w, name = _lib.lib.serq_linear_i8_workspace, S.i8_kernel_name
     assert w(-1, 64, 64) == -1 and w(1, 1 << 17, 64) == -1 and w(0, 64, 64) == 0 and name(1, 0, 1) is None
     assert name(4096, 8192, 8192) == "tile256x256" and name(1, 4096, 4096) == "stream" and name(1, 4090, 8) == "generic"
+    assert name(1024, 8192, 8192) == "tile256x128" and name(1100, 528, 4100) == "tile256x128"
     assert name(100, 4096, 4096) == "tile64x64" and name(400, 4096, 4096) == "tile64x128"
     assert name(1000, 4096, 4096) == "tile128x128" and w(1000, 4096, 4096) == 0 and name(100, 14336, 4096) == "tile128x128"
     assert w(100, 14336, 4096) > 0

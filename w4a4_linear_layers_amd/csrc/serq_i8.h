@@ -18,7 +18,7 @@ struct I8Args {
   int y_bf16;
 };
 
-enum class I8Kernel { kStream, kTile64, kTile64x128, kTile128, kTile256, kGeneric };
+enum class I8Kernel { kStream, kTile64, kTile64x128, kTile128, kTile256, kTile256x128, kGeneric };
 
 struct I8Plan {
   I8Kernel kind;

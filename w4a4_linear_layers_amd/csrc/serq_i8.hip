@@ -289,7 +289,7 @@ __global__ __launch_bounds__(256, OCC) void i8_tile_kernel(I8Args a, int n_tiles
   constexpr int BN = 64 * TN, BM = 64 * TM;
   constexpr int kW = BN * kKTile, kStage = (BN + BM) * kKTile, CPW = TN + TM;
   constexpr int kScales = STAGES * kStage, kScaleBytes = 4 * (BN + BM);        // two sets of scales after the places,
-  constexpr bool kThroughLds = TN == 4;
+  constexpr bool kThroughLds = TN == 4 && TM == 4;
   constexpr int kOut = kScales + 2 * kScaleBytes, kOutBytes = 4096;            // then a place of each wave for outputs
   static_assert(CPW * (STAGES - 1) < 64, "vmcnt range");
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
@@ -673,7 +673,7 @@ hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done)
 
 template <int TN, int TM, int STAGES, int OCC, bool PARTS>
 hipError_t launch_tile(const I8Args& a, const I8Plan& p, hipStream_t st) {
-  constexpr int kLds = 64 * (TN + TM) * (STAGES * kKTile + 8) + (TN == 4 ? 4 * 4096 : 0);
+  constexpr int kLds = 64 * (TN + TM) * (STAGES * kKTile + 8) + (TN == 4 && TM == 4 ? 4 * 4096 : 0);
   const int n_tiles = static_cast<int>(ceil_div(a.N, 64 * TN));
   const int tiles = n_tiles * static_cast<int>(ceil_div(a.M, 64 * TM));
   auto* kernel = &i8_tile_kernel<TN, TM, STAGES, OCC, PARTS>;
@@ -763,6 +763,15 @@ I8Plan plan_linear_i8(int M, int K, int N) {
     p.name = "tile256x256";
     return p;
   }
+  // 256 channels by 128 tokens where a unit would have two tiles of 128 x 128 side
+  // by side: 1024 tokens of 8192 x 8192 in 87 us against 96, 256 of 4096 x 28672 in 48
+  // against 54, 2048 of 14336 x 4096 in 142 against 158, 1000 of 4096 x 6144 in 34
+  // against 37; with fewer tiles, 512 of 8192 x 8192 take 75 against 57.
+  if (tiles > kCUs) {
+    p.kind = I8Kernel::kTile256x128;
+    p.name = "tile256x128";
+    return p;
+  }
   // Tiles of 128 x 128 where there are enough of them; of half that size, or a
   // quarter, where there are not (256 x 4096 x 4096: 11.5 us in tiles of 64 x 64,
   // 17.7 of 128 x 128; 384 tokens 15.1 of 64 x 128, 18.5 of 64 x 64; 768 tokens 21.0 of
@@ -795,6 +804,7 @@ hipError_t launch_linear_i8(const I8Args& a, const I8Plan& p, hipStream_t st) {
     case I8Kernel::kStream:
       return launch_stream_tokens(a, p.rt, p.nt, st);
     case I8Kernel::kTile256: return launch_tile<4, 4, 4, 1, false>(a, p, st);
+    case I8Kernel::kTile256x128: return launch_tile<4, 2, 3, 2, false>(a, p, st);
     case I8Kernel::kTile128: return launch_tile<2, 2, 4, 2, true>(a, p, st);
     case I8Kernel::kTile64x128: return launch_tile<1, 2, 6, 2, false>(a, p, st);
     case I8Kernel::kTile64: return launch_tile<1, 1, 8, 2, false>(a, p, st);
