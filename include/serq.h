@@ -623,9 +623,11 @@ int serq_rope_append_axes(const void* QKV, serq_dtype dtype, int64_t ld, int M, 
  * has a power of two:
  *     k_scale[page][kv head][page_size / 16],  v_scale likewise,
  * bytes e + 127 (OCP E8M0) with -117 <= e <= 120; both arrays 4-byte aligned.
- * A cache value is code * 2^e. Half the bytes of a bf16 cache and 1 in 16 D
- * more; a value has 4 significant bits, so it is off by at most 2^-4 of itself
- * (2^-10 * 2^e near 0).
+ * A cache value is code * 2^e, which is a bf16 number; at e = 120 the codes from
+ * 256 on, 2^128 and more, are infinities. Half the bytes of a bf16 cache and 1 in
+ * 16 D more; a value has 4 significant bits, so it is off by at most 2^-4 of itself
+ * (2^-10 * 2^e near 0), and one of 248 * 2^120 (3.297e38) or more in magnitude
+ * becomes an infinity, as it would rounded to 4 bits.
  *
  * Storing a block's token 0 begins it anew: its scale then comes from what that
  * call stores in it, and the codes of its other tokens stay as they are, to be
@@ -751,10 +753,11 @@ int64_t serq_attn_decode_workspace(serq_dtype dtype, int B, int Hq, int Hkv, int
 
 /*
  * serq_attn_prefill_f8, serq_attn_decode_f8 -- the same attentions over a cache
- * in 8 bits: keys and values are code * 2^e, exactly (they are bf16 numbers),
- * and everything else is as for serq_attn_prefill and serq_attn_decode with
- * `dtype` that of Q and O. A code NaN behaves as a NaN does there. Scales of
- * blocks that no token of a sequence lies in are never used.
+ * in 8 bits: keys and values are code * 2^e, exactly (bf16 numbers, or at e = 120
+ * infinities), and everything else is as for serq_attn_prefill and
+ * serq_attn_decode with `dtype` that of Q and O. A code NaN behaves as a NaN does
+ * there, and those infinities as infinities. Scales of blocks that no token of a
+ * sequence lies in are never used.
  * Errors as there; SERQ_EINVAL (NULL) and SERQ_EALIGN (not 4-byte aligned) for
  * the scales too. Their workspaces are sized by their own functions.
  */

@@ -286,7 +286,7 @@ struct Rows8<float, D> {
 #pragma unroll
     for (int j = 0; j < 4; ++j) p[j] = exp2_(z[j] - r);
     l += (p[0] + p[1]) + (p[2] + p[3]);
-    bool odd = false;
+    bool odd = sv >= kInfinities;
     float x[4][B][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -300,7 +300,7 @@ struct Rows8<float, D> {
         x[j][b][0] = lo[0], x[j][b][1] = lo[1], x[j][b][2] = hi[0], x[j][b][3] = hi[1];
       }
     }
-    if (cut && __any(odd)) {          // a NaN on a key that some of these queries do not see: 0 * NaN is not 0
+    if (cut && __any(odd)) {          // NaN or infinities on a key that some of these queries do not see: 0 * NaN is not 0
 #pragma unroll
       for (int c = 0; c < B * 4; ++c)
 #pragma unroll 1

@@ -214,6 +214,10 @@ __device__ __forceinline__ int page_entry(const int32_t* table, int i) {
   return ((const __attribute__((address_space(4))) int32_t*)table)[i];
 }
 
+// Scale of a block of FP8 codes from which on some stand for 2^128 and more, which
+// neither bf16 nor fp32 holds: 256 * 2^120.
+constexpr float kInfinities = 0x1p120f;
+
 // A page inside the cache, whatever the entry says.
 __device__ __forceinline__ int in_cache(int page, int n_pages) {
   return page < 0 ? 0 : page >= n_pages ? n_pages - 1 : page;

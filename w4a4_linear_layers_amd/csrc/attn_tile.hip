@@ -278,7 +278,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
   const auto put_v = [&](int at) { put(smem + (kRing + at) * kTile, swizzle_v<D>(cr), vc, vs); };
   // The scales of the codes that go to their places next: K tile t + 1, V tile t.
   // As for look_over, V's rows past the end are cleared, and it is noted whether
-  // the others are finite.
+  // the others are finite: a code NaN is not, and in blocks of 2^120 the codes from
+  // 256 on are infinities (such a block is taken to hold one).
   const auto make_ready = [&](int t, int at) {
     ks = to_scale(ks_word, ks_bit);
     vs = to_scale(vs_word, vs_bit);
@@ -291,7 +292,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
         odd |= (((vc[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
       }
       if (from + t * kKeys + kPer * wave >= len) vs = 1.0f;       // (a scale that is no number)
-      const int any = __any(odd);
+      const int any = __any(odd || vs >= kInfinities);
       if (lane == 0) odd_rows[at][wave] = any;
     }
   };
