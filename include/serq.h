@@ -622,7 +622,10 @@ int serq_rope_append_axes(const void* QKV, serq_dtype dtype, int64_t ld, int M, 
  * value) in the layout above, and each block of 16 tokens of a page and head
  * has a power of two:
  *     k_scale[page][kv head][page_size / 16],  v_scale likewise,
- * bytes e + 127 (OCP E8M0) with -117 <= e <= 120; both arrays 4-byte aligned.
+ * bytes e + 127 (OCP E8M0) with -117 <= e <= 120. Both arrays are 4-byte aligned
+ * and are read by words of 4 bytes: where their size is no multiple of 4, the
+ * memory has to reach to the next one. (What lies there is not used, and never
+ * written.)
  * A cache value is code * 2^e, which is a bf16 number; at e = 120 the codes from
  * 256 on, 2^128 and more, are infinities. Half the bytes of a bf16 cache and 1 in
  * 16 D more; a value has 4 significant bits, so it is off by at most 2^-4 of itself
@@ -649,8 +652,9 @@ int serq_rope_append_axes(const void* QKV, serq_dtype dtype, int64_t ld, int M, 
  * as for serq_rope_append.
  *   dtype      of QKV and Q.
  *   Kc, Vc     n_pages * Hkv * page_size * D bytes each, 16-byte aligned.
- *   k_scale, v_scale  n_pages * Hkv * page_size / 16 bytes each. Bytes outside
- *              10..247 of a block that is not begun anew are taken as the
+ *   k_scale, v_scale  n_pages * Hkv * page_size / 16 bytes each, in memory that
+ *              the attention calls can read to the next multiple of 4. Bytes
+ *              outside 10..247 of a block that is not begun anew are taken as the
  *              nearest inside.
  * Errors as for serq_rope_append_axes, SERQ_EINVAL and SERQ_EALIGN (4 bytes)
  * for the scales too. Uses no scratch memory.

@@ -103,7 +103,8 @@ class KvCacheF8:
     is its code times its block's power. Queries are bfloat16 or float32,
     whichever a call is given. A block begins with its first token and is
     filled in order (serq_rope_append_f8 says how its scale follows). Tensors
-    may be replaced, as for KvCache."""
+    may be replaced, as for KvCache. (Scales are read by words of 4 bytes:
+    tensors over memory that is not torch's own have to end with a whole one.)"""
 
     k: "object"
     v: "object"
@@ -142,7 +143,8 @@ class KvCacheF8:
         """A cache of uninitialised pages."""
         shape, blocks = (n_pages, n_kv_heads, page_size, head_dim), (n_pages, n_kv_heads, page_size // 16)
         k, v = (torch.empty(shape, dtype=_F8, device=device) for _ in range(2))
-        ks, vs = (torch.empty(blocks, dtype=_U8, device=device) for _ in range(2))
+        n = blocks[0] * blocks[1] * blocks[2]
+        ks, vs = (torch.empty((n + 3) // 4 * 4, dtype=_U8, device=device)[:n].view(blocks) for _ in range(2))
         return cls(k, v, ks, vs)
 
 

@@ -41,7 +41,8 @@ struct Pages8 {
 };
 
 // A block's scale, 2^(byte - 127). Kernels that read scales write none, so this
-// is a scalar load, of the dword that holds the byte (the arrays are 4-byte aligned).
+// is a scalar load, of the dword that holds the byte (the arrays are 4-byte aligned,
+// and their memory ends with a whole dword).
 __device__ __forceinline__ float scale_of(const uint8_t* scales, int64_t block) {
   const uint32_t w = ((const __attribute__((address_space(4))) uint32_t*)scales)[block >> 2];
   return __uint_as_float((w >> (8 * (static_cast<int>(block) & 3)) & 0xFFu) << 23);

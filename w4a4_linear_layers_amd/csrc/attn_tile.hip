@@ -255,6 +255,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, P
       codes[0] = x[0], codes[1] = x[1];
     }
   };
+  // (the dword that holds it: the arrays' memory ends with a whole one)
   const auto fetch_scale = [&](const uint8_t* scales, uint64_t at, uint32_t& word, int& bit) {
     const uint64_t block = at / (16 * D);        // (rows of a wave lie in one block)
     word = ((const __attribute__((address_space(4))) uint32_t*)scales)[block >> 2];
