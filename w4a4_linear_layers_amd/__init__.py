@@ -588,8 +588,10 @@ def i8_kernel_name(M: int, K: int, N: int) -> str | None:
 def linear_i8(xq, sx, layer: I8Layer, *, out_dtype=None, out=None, workspace=None, debug: bool = False):
     """The linear in 8-bit integers (serq_linear_i8) on the current stream of
     the layer's device: ``xq`` M x K int8 and ``sx`` M float32 (quant_act with
-    a_bits=8). A workspace is taken from torch's allocator unless given. Returns
-    Y (M x N) or, with ``debug=True``, (Y, the int32 sums)."""
+    a_bits=8). A workspace is taken from torch's allocator unless given. There is
+    no backward pass: where torch records gradients, scales or an ``out`` that
+    require one are refused. Returns Y (M x N) or, with ``debug=True``, (Y, the
+    int32 sums)."""
     import torch
     K, N, Wq, sw = layer.K, layer.N, layer.Wq, layer.sw
     dev = Wq.get_device()
@@ -615,6 +617,8 @@ def linear_i8(xq, sx, layer: I8Layer, *, out_dtype=None, out=None, workspace=Non
     y = sx.new_empty((M, N), dtype=out_dtype) if out is None else out
     if y.shape != (M, N) or y.dtype is not out_dtype:
         raise ValueError(f"out must be a ({M}, {N}) {out_dtype} tensor")
+    if (sx.requires_grad or sw.requires_grad or y.requires_grad) and torch.is_grad_enabled():
+        raise ValueError("sx, the layer's scales or out require a gradient, and linear_i8 has none: use torch.no_grad()")
     for t in (xq, sx, Wq, sw, y):
         if t.get_device() != dev or dev < 0 or not t.is_contiguous():
             raise ValueError("tensors must be contiguous and on one CUDA device")
