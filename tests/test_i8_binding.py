@@ -45,3 +45,20 @@ def test_a_gradient_is_not_lost_silently(lib, name, tensor):
     with torch.no_grad():
         call(**{name: t})
     assert t.address in lib.args
+
+
+@pytest.mark.parametrize("sizes", [dict(M=(1 << 32) + 5, K=1, N=1), dict(M=1 << 31, K=16, N=8), dict(K=(1 << 32) + 16, N=1), dict(N=(1 << 32) + 8, K=16)])
+def test_sizes_that_no_int_holds_are_refused(lib, monkeypatch, sizes):
+    """(ctypes would hand on their low 32 bits)"""
+    with pytest.raises(ValueError):
+        call(**sizes)
+    assert lib.name is None
+    monkeypatch.undo()
+    M, K, N = ({**dict(M=3, K=64, N=32), **sizes}[k] for k in "MKN")
+    assert S.linear_i8_workspace(M, K, N) == -1 and S.i8_kernel_name(M, K, N) is None
+
+
+def test_sizes_are_told_from_those_of_other_bits():
+    for sizes in ((-(1 << 32) + 3, 64, 32), (3, -(1 << 32) + 64, 32), (3, 64, -(1 << 32) + 32), (-1, 64, 32), (3, 0, 32), (3, 64, 0)):
+        assert S.linear_i8_workspace(*sizes) == -1 and S.i8_kernel_name(*sizes) is None
+    assert S.linear_i8_workspace(3, 64, 32) == 0 and S.i8_kernel_name(3, 64, 32) == "stream"

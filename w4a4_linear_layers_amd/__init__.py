@@ -573,14 +573,22 @@ def calibrate_i8(W, act_absmax=None, *, alpha: float = 0.5, w_dtype: str | None 
     return I8Layer(K=K, N=N, s_hat_inv=shi, Wq=Wq, sw=sw)
 
 
+_MOST_INT = (1 << 31) - 1     # (a larger one would reach the library by its low 32 bits)
+
+
 def linear_i8_workspace(M: int, K: int, N: int) -> int:
     """Bytes of workspace linear_i8 needs (serq_linear_i8_workspace); -1 for
     sizes that it does not take."""
+    if not (0 <= M <= _MOST_INT and 0 < K <= _MOST_INT and 0 < N <= _MOST_INT):
+        return -1
     return lib.serq_linear_i8_workspace(M, K, N)
 
 
 def i8_kernel_name(M: int, K: int, N: int) -> str | None:
-    """The kernel serq_linear_i8 launches for these sizes."""
+    """The kernel serq_linear_i8 launches for these sizes, None for those that
+    it does not take."""
+    if linear_i8_workspace(M, K, N) < 0:
+        return None
     s = lib.serq_linear_i8_kernel_name(M, K, N)
     return s.decode() if s else None
 
@@ -622,7 +630,7 @@ def linear_i8(xq, sx, layer: I8Layer, *, out_dtype=None, out=None, workspace=Non
     for t in (xq, sx, Wq, sw, y):
         if t.get_device() != dev or dev < 0 or not t.is_contiguous():
             raise ValueError("tensors must be contiguous and on one CUDA device")
-    size = lib.serq_linear_i8_workspace(M, K, N)
+    size = linear_i8_workspace(M, K, N)
     if size < 0:
         raise ValueError("sizes that the library does not take")
     wp = None
