@@ -302,7 +302,7 @@ def rope_append(qkv, n_heads: int, cache, pos, slot, table, *, layout: str = "ha
             qkv.data_ptr(), dt, ld, M, n_heads, Hkv, D, qw, kw, eps, tp, rot, max_pos, order, pp,
             sp, q.data_ptr(), ldq, kc, vc, n_pages, page, _stream(dev))
     if status:
-        check("serq_rope_append" + ("_f8" if len(now) > 9 else ""), status)
+        check("serq_rope_append" + ("_f8" if len(now) > 9 else "_axes" if axes is not None else ""), status)
     return q
 
 
