@@ -186,6 +186,15 @@ _current = getattr(getattr(torch, "_C", None), "_cuda_getDevice", None) or (lamb
 _AXES = bytes(range(4))
 
 
+def _axes_of(pair_axis):
+    """The numbers of a sequence as bytes. (bytes() of an int would be so many
+    zeros, and of an array its memory.)"""
+    try:
+        return bytes(list(pair_axis))
+    except TypeError as e:
+        raise ValueError("pair_axis must be bytes or a sequence of whole numbers") from e
+
+
 # The checks below run on every call of a decoding step, where a handful of
 # microseconds is what the kernels take: each attribute is read once.
 
@@ -281,7 +290,8 @@ def rope_append(qkv, n_heads: int, cache, pos, slot, table, *, layout: str = "ha
             if pair_axis is None:
                 tp, pp = table.data_ptr(), _ints(pos, (M,), dev, "pos")
             else:
-                axes, n_axes = bytes(pair_axis), pos.shape[0] if pos.dim() == 2 else 0
+                axes = pair_axis if type(pair_axis) is bytes else _axes_of(pair_axis)
+                n_axes = pos.shape[0] if pos.dim() == 2 else 0
                 if len(axes) != rot // 2 or not 1 <= n_axes <= 4 or axes.translate(None, _AXES[:n_axes]):
                     raise ValueError(f"pair_axis must hold {rot // 2} axes and pos a row of {M} for each (four at most)")
                 tp, pp = table.data_ptr(), _ints(pos, (n_axes, M), dev, "pos")
