@@ -221,6 +221,8 @@ def _out(out, shape, dtype, dev):
     """(output, its row stride)"""
     if out.shape != shape:
         raise ValueError(f"out must be of shape {tuple(shape)}")
+    if out.requires_grad:
+        _no_gradient("out")
     return out, _rows(out, shape, shape[2], dtype, dev, "out")
 
 
@@ -285,6 +287,8 @@ def rope_append(qkv, n_heads: int, cache, pos, slot, table, *, layout: str = "ha
         size = table.shape
         if len(size) != 2 or table.dtype is not _F32 or table.get_device() != dev or not table.is_contiguous():
             raise ValueError("table must be a contiguous CUDA (max_pos, rot_dim) float32 tensor on the cache's device")
+        if table.requires_grad:
+            _no_gradient("table")
         max_pos, rot = size
         if rot:
             if pair_axis is None:
