@@ -1,4 +1,5 @@
-"""Prompts of 2048 tokens and more onto a cache in 8 bits, in every form of the
+"""Prompts of many tokens or heads onto a cache in 8 bits (from 2^16 tokens times
+heads on keys and values take a launch of their own), in every form of the
 rotation: both layouts, several axes, part of the head, rows that suit no vector
 loads. Codes and scales bit for bit, queries those of a cache of the model's type."""
 
@@ -44,17 +45,20 @@ def test_the_plain_form_is_the_tests_other_one():
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("M,Hkv,D,rot,norm,layout,axes,kind,pad,shift", [
-    (2048, 3, 128, 128, True, "interleaved", 1, "blocks", 0, 0),
-    (2051, 5, 64, 64, False, "interleaved", 1, "blocks", 0, 0),
-    (2300, 2, 128, 64, True, "interleaved", 3, "turns", 0, 0),
-    (2200, 3, 128, 128, True, "half", 3, "blocks", 0, 0),
-    (4100, 2, 128, 128, True, "half", 3, "turns", 0, 0),       # (queries of three heads a lane)
-    (4099, 3, 64, 64, True, "interleaved", 4, "blocks", 0, 0),
-    (2100, 1, 64, 32, False, "half", 2, "turns", 0, 0),
-    (2049, 2, 128, 128, True, "half", 3, "turns", 1, 0),       # rows that lie unaligned
-    (2500, 3, 64, 64, False, "interleaved", 2, "blocks", 0, 1),
-    (2064, 2, 64, 20, True, "half", 3, "blocks", 0, 0),        # a part that no whole 16 bytes hold
-    (2065, 2, 128, 6, True, "interleaved", 3, "turns", 8, 8),
+    (2048, 8, 128, 128, True, "interleaved", 1, "blocks", 0, 0),
+    (2051, 8, 64, 64, False, "interleaved", 1, "blocks", 0, 0),
+    (2300, 8, 128, 64, True, "interleaved", 3, "turns", 0, 0),
+    (2200, 8, 128, 128, True, "half", 3, "blocks", 0, 0),
+    (2047, 8, 128, 128, True, "half", 3, "turns", 0, 0),       # (one launch)
+    (4100, 9, 128, 128, True, "half", 3, "turns", 0, 0),       # (queries of three heads a lane)
+    (4099, 5, 64, 64, True, "interleaved", 4, "blocks", 0, 0),
+    (16500, 1, 64, 32, False, "half", 2, "turns", 0, 0),
+    (2100, 1, 64, 32, False, "half", 2, "turns", 0, 0),        # (one launch)
+    (120, 137, 128, 128, True, "half", 1, "blocks", 0, 0),     # few tokens of many heads
+    (2049, 8, 128, 128, True, "half", 3, "turns", 1, 0),       # rows that lie unaligned
+    (2500, 7, 64, 64, False, "interleaved", 2, "blocks", 0, 1),
+    (2064, 8, 64, 20, True, "half", 3, "blocks", 0, 0),        # a part that no whole 16 bytes hold
+    (2065, 8, 128, 6, True, "interleaved", 3, "turns", 8, 8),
 ])
 def test_append(dtype, M, Hkv, D, rot, norm, layout, axes, kind, pad, shift):
     g = gen(M + rot)

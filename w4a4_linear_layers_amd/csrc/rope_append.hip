@@ -801,13 +801,18 @@ hipError_t launch_by_dim(const RopeArgs& a, hipStream_t st) {
   return a.D == 64 ? launch_typed<T, 64, AXES>(a, st) : launch_typed<T, 128, AXES>(a, st);
 }
 
-// From so many tokens on, keys and values of a call onto a cache of codes take a
-// launch and the queries another, each with its own registers and heads of a
-// workgroup: 32 and 8 normed heads of 128, bf16, 1024 tokens 11.5 us in one
-// launch; 2048 21.3 in one and 17.4 in two; 4096 39.4 and 27.8; 8192 75 and 48;
-// fp32 2048 31.1 and 25.8, 8192 138 and 96. (Keys and values in a launch each: 8192
-// 52; all in one with these heads 51, without norms 57 against 44.)
-constexpr int kManyStored = 2048;
+// From so many tokens times heads (of all three kinds) on, keys and values of a call
+// onto a cache of codes take a launch and the queries another, each with its own
+// registers and heads of a workgroup. One launch against two, 2048 normed tokens
+// unless said otherwise: 32 and 8 heads of 128, bf16, 1024 tokens 11.5 us and 11.3, 1536
+// 16.5 and 14.7, 2048 21.3 and 17.4, 8192 75 and 48 (fp32, 1536 24.2 and 22.1); 64 and 8 30.4
+// and 23.3, 512 tokens 9.2 and 11.1; 32 and 32 39.0 and 30.8; 8 and 1 7.4 and 9.7, 8192
+// tokens 24.6 and 19.8 (fp32 7.2 and 11.5, 25.1 and 24.2); heads of 64, 32 and 8, 1024
+// tokens 7.3 and 9.1, 1536 10.0 and 10.1, 16 and 16 15.8 and 11.2, 8 and 8 without norms
+// 8.9 and 8.4, 3000 tokens 12.1 and 9.9. They change over between 43 and 82 thousand. (Keys and
+// values in a launch each: 8192 tokens of 32 and 8 heads 52; all in one with these
+// heads of a workgroup 51.)
+constexpr int64_t kManyStored = 1 << 16;
 
 // Tokens [first, first + tokens) of a call onto a cache of codes. Where they are
 // many, a workgroup takes two heads of keys (alone 8192 tokens 18.4 us, one head
@@ -831,7 +836,7 @@ hipError_t launch_f8(const RopeArgs& a, int first, int tokens, hipStream_t st) {
     x.Hkv = 0;
     return x;
   };
-  const bool vector = vector_path<T>(a), many = tokens >= kManyStored;
+  const bool vector = vector_path<T>(a), many = static_cast<int64_t>(tokens) * (a.Hq + 2 * a.Hkv) >= kManyStored;
   if (vector && !many) {
     rope_append_f8_kernel<T, D, INTER, NORM, true>
         <<<dim3(static_cast<unsigned>(2 * stores(1) + static_cast<int64_t>(tokens) * sets)), kThreads, 0, st>>>(a, first, tokens, sets);
