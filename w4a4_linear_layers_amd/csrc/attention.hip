@@ -717,12 +717,20 @@ constexpr int kTileRows = 256;       // rows of a workgroup of the tile kernel
 // 18.6 against 12.8.
 constexpr int64_t kPrefixTileWork = 6000000;
 // Of codes the rows' kernel reads half as much, while the tiles' products stay
-// what they are. With 5 to 700 keys of each sequence after it, the whole call: 32
-// sequences of 32 heads, 6000 keys 31.9 us against 24.7, 16000 41.3 against 38.9,
-// 30000 57.3 against 56.4; 96 sequences, 2000 keys 34.3 against 28.8, 6000 42.3
-// against 43.1, 9000 47.8 against 54.3; 256 sequences, 1500 keys 50.3 against 45.6,
-// 3000 56.2 against 60.5; heads of 64, 128 sequences, 4000 keys 27.5 against 23.1.
-constexpr int64_t kPrefixTileWorkCodes = 18000000;
+// what they are; here the work counts the heads' width too, and 64 rows a head or
+// fewer, which fill a quarter of a tile, stay with the rows' kernel. With 5 to 700
+// keys of each sequence after the prefix, the whole call, tiles against rows: 32
+// and 8 heads of 128, 32 sequences, 16000 keys 42.2 us and 39.3, 30000 54.8 and
+// 55.4, 60000 84 and 99; 96 sequences, 2000 keys 34.2 and 28.7, 6000 41.7 and 42.9,
+// 9000 47.3 and 54.3; 256, 2000 keys 52.6 and 50.9, 3000 55.7 and 60.2; 64 and 8
+// heads, 64 sequences, 3000 keys 37.4 and 32.5, 6000 41.6 and 47.2; 8 heads and 1,
+// 128 sequences, 9000 keys 31.6 and 27.5, 18000 35.9 and 37.7; 16 and 16 heads, 200
+// sequences, 8000 keys 64.2 and 69.6; heads of 64, 128 sequences, 8000 keys 32.9
+// and 30.9, 16000 43.1 and 47.0 (but 32 of them, 60000 keys, 53 and 45). 64 rows a
+// head: 16 sequences of 32 and 8 heads, 60000 keys 76 and 73, 64 of 16 and 16, 24000
+// keys 74 and 64.
+constexpr int64_t kPrefixTileWorkCodes = int64_t{18000000} * 128;
+constexpr int64_t kPrefixRowsCodes = 64;
 
 PrefillPlan plan_prefill(int kind, int B, int T, int Hq, int Hkv, int D, int max_len) {
   PrefillPlan p{};
@@ -799,7 +807,8 @@ DecodePlan plan_decode(int kind, int B, int Hq, int Hkv, int D, int prefix_len, 
     p.waves = max_len > 256 ? 8 : 4;
   }
   if (prefix_len > 0) {
-    p.ptiled = (kind & kBf16) && static_cast<int64_t>(B) * Hq * prefix_len >= (kind & kCodes ? kPrefixTileWorkCodes : kPrefixTileWork);
+    const int64_t work = static_cast<int64_t>(B) * Hq * prefix_len;      // (below 2^60)
+    p.ptiled = (kind & kBf16) && (kind & kCodes ? work >= kPrefixTileWorkCodes / D && rows > kPrefixRowsCodes : work >= kPrefixTileWork);
     p.ptiles = ceil_div(rows, p.ptiled ? kTileRows : 16);
     s = ceil_div(p.ptiled ? 256 : 1024, static_cast<int64_t>(Hkv) * p.ptiles);
     p.pchunk = cut(prefix_len, s, p.ptiled ? 64 : 128);

@@ -801,17 +801,17 @@ hipError_t launch_by_dim(const RopeArgs& a, hipStream_t st) {
   return a.D == 64 ? launch_typed<T, 64, AXES>(a, st) : launch_typed<T, 128, AXES>(a, st);
 }
 
-// From so many tokens times heads (of all three kinds) on, keys and values of a call
-// onto a cache of codes take a launch and the queries another, each with its own
-// registers and heads of a workgroup. One launch against two, 2048 normed tokens
-// unless said otherwise: 32 and 8 heads of 128, bf16, 1024 tokens 11.5 us and 11.3, 1536
-// 16.5 and 14.7, 2048 21.3 and 17.4, 8192 75 and 48 (fp32, 1536 24.2 and 22.1); 64 and 8 30.4
-// and 23.3, 512 tokens 9.2 and 11.1; 32 and 32 39.0 and 30.8; 8 and 1 7.4 and 9.7, 8192
-// tokens 24.6 and 19.8 (fp32 7.2 and 11.5, 25.1 and 24.2); heads of 64, 32 and 8, 1024
-// tokens 7.3 and 9.1, 1536 10.0 and 10.1, 16 and 16 15.8 and 11.2, 8 and 8 without norms
-// 8.9 and 8.4, 3000 tokens 12.1 and 9.9. They change over between 43 and 82 thousand. (Keys and
-// values in a launch each: 8192 tokens of 32 and 8 heads 52; all in one with these
-// heads of a workgroup 51.)
+// From so many tokens times heads (of all three kinds) on, keys and values of a
+// call onto a cache of codes take a launch and the queries another, each with its
+// own registers and heads of a workgroup. One launch against two, bf16, 2048 normed
+// tokens unless said otherwise: 32 and 8 heads of 128, 1024 tokens 11.5 us and 11.3,
+// 1536 16.5 and 14.7, 2048 21.3 and 17.4, 8192 75 and 48 (fp32, 1536 24.2 and 22.1);
+// 64 and 8 heads 30.4 and 23.3, 512 tokens 9.2 and 11.1; 32 and 32 39.0 and 30.8; 8
+// and 1 7.4 and 9.7, 8192 tokens 24.6 and 19.8 (fp32 7.2 and 11.5, 25.1 and 24.2);
+// heads of 64, 32 and 8, 1024 tokens 7.3 and 9.1, 1536 10.0 and 10.1; 16 and 16 15.8
+// and 11.2; 8 and 8 without norms 8.9 and 8.4, 3000 tokens 12.1 and 9.9. The two
+// change places between 43 and 82 thousand. (Keys and values in a launch each: 8192
+// tokens of 32 and 8 heads 52; all in one with these heads of a workgroup 51.)
 constexpr int64_t kManyStored = 1 << 16;
 
 // Tokens [first, first + tokens) of a call onto a cache of codes. Where they are
