@@ -784,14 +784,24 @@ DecodePlan plan_decode(int kind, int B, int Hq, int Hkv, int D, int prefix_len, 
   const int64_t groups = static_cast<int64_t>(B) * Hkv * p.tiles;
   int64_t s = ceil_div(8192, groups);
   // A cache of codes: a workgroup's four waves take 256 keys at a time, so parts
-  // are larger where there are many (256 sequences of 20 to 2000 keys, 8
-  // key/value heads of 128: parts of 1024 59.5 us, of 256 76.7; 120 of 5 to 900
-  // after a prefix 51.4 against 58.0; 128 of 500 to 1500 parts of 512 43.8, of 256
-  // 46.6, of 1024 52.6; 64 of 100 to 4096 parts of 256 36.9, of 1024 45.8). fp32
-  // queries gain alike (the 256 sequences 158 us against 195, the 128 96 against 104).
-  int unit = groups >= 512 ? 256 : 128;
-  if ((kind & kCodes) && groups >= 768) unit = groups >= 1536 || max_len <= 1024 ? 1024 : 512;
+  // are larger where there are many, 512 keys or, up to 1024, one part (of 512
+  // against 256: 128 sequences of 500 to 1500 keys 43.6 us and 47.1, 200 of 100 to
+  // 4096 102 and 107; one part, 120 of 5 to 900 after a prefix 51 and 58). And no
+  // power of two of them but one and two: a sequence's parts lie side by side, and
+  // where short ones leave every fourth workgroup with keys, say, those go round
+  // to the same compute units. All figures over 8 heads of 128, the nearest number
+  // of parts below against the power of two: 256 of 20 to 2000 47 and 60 to 77 (of
+  // 64: 30 and 36 to 46), 128 of 100 to 4096 59 and 69 (fp32 queries 151 and 175),
+  // 200 of them 102 and 135 (64: 45 and 63; fp32 200 and 345), 256 of 100 to 8000
+  // 200 and 269, 500 of 20 to 4000 174 and 212; even or up to 3 % behind where
+  // lengths are alike (200 of 4096 313 and 311, 64 of 32 heads 115 and 112).
+  const bool larger = (kind & kCodes) && groups >= 768;
+  const int unit = larger ? (max_len <= 1024 ? 1024 : 512) : groups >= 512 ? 256 : 128;
   p.chunk = cut(max_len, s, unit);
+  while (larger && s > 2 && (s & (s - 1)) == 0) {
+    --s;
+    p.chunk = cut(max_len, s, 256);
+  }
   p.splits = static_cast<int>(s);
   p.waves = 4;
   // Short caches whole: one launch and no join, eight waves a workgroup beyond
