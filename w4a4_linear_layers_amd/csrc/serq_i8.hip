@@ -279,7 +279,8 @@ __device__ __forceinline__ int lane_again() {
 // bf16 outputs of 256 x 256 go by whole lines through LDS, 64 channels of a token
 // side by side, instead of 32 bytes of a row at a time: 439 us against 460. The
 // smaller tiles store as they are (1024 tokens of 8192 x 8192 in 128 x 128: 96 us, 101
-// through LDS).
+// through LDS). fp32 outputs, 16 bytes of a token a lane: 463 us of 4000 tokens against
+// 430, 151 of 2048 x 8192 x 8192 against 123; in the smaller tiles within 10 %.
 //
 // A tile's outputs are stored while the next tile's first k-tiles and its
 // scales are under way (the waits count loads, and stores after them make
