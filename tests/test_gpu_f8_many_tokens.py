@@ -21,6 +21,8 @@ def turned(x, w, eps, table, pos, listed, layout):
     x = x.double()
     if w is not None:
         x = x / torch.sqrt((x * x).mean(-1, keepdim=True) + eps) * w.double()
+    if table is None:
+        return x
     half = table.shape[1] // 2
     at = pos.long()[torch.tensor(listed)].t()                  # M x pairs: each pair's position
     i = torch.arange(half)
@@ -55,6 +57,10 @@ def test_the_plain_form_is_the_tests_other_one():
     (16500, 1, 64, 32, False, "half", 2, "turns", 0, 0),
     (2100, 1, 64, 32, False, "half", 2, "turns", 0, 0),        # (one launch)
     (120, 137, 128, 128, True, "half", 1, "blocks", 0, 0),     # few tokens of many heads
+    (2600, 9, 128, 128, True, "half", 1, "blocks", 0, 0),
+    (2050, 8, 64, 64, True, "half", 1, "blocks", 0, 0),
+    (2070, 8, 64, 0, True, "half", 1, "blocks", 0, 0),
+    (2071, 8, 128, 0, False, "half", 1, "blocks", 0, 0),
     (2049, 8, 128, 128, True, "half", 3, "turns", 1, 0),       # rows that lie unaligned
     (2500, 7, 64, 64, False, "interleaved", 2, "blocks", 0, 1),
     (2064, 8, 64, 20, True, "half", 3, "blocks", 0, 0),        # a part that no whole 16 bytes hold
@@ -75,7 +81,7 @@ def test_append(dtype, M, Hkv, D, rot, norm, layout, axes, kind, pad, shift):
     flat = torch.randn(M * (width + pad) + shift, generator=g).to(dtype)
     qkv = torch.as_strided(flat, (M, width), (width + pad, 1), shift)
     dq = torch.as_strided(flat.to(DEV), (M, width), (width + pad, 1), shift)
-    table = torch.from_numpy(S.rope_table(rot, 300, theta=900.0))
+    table = torch.from_numpy(S.rope_table(rot, 300, theta=900.0)) if rot else None
     pos = torch.randint(0, 300, (axes, M), generator=g).to(torch.int32)
     pair_axis, listed = axes_of(rot, axes, kind)
     w = 1 + 0.3 * torch.randn(D, generator=g) if norm else None
@@ -84,7 +90,7 @@ def test_append(dtype, M, Hkv, D, rot, norm, layout, axes, kind, pad, shift):
     kw = dict(layout=layout, eps=eps, q_norm=w.to(DEV) if norm else None, k_norm=w.to(DEV) if norm else None)
     if axes > 1:
         kw["pair_axis"] = pair_axis
-    args = (pos if axes > 1 else pos[0]).to(DEV), ints(slot).to(DEV), table.to(DEV)
+    args = (pos if axes > 1 else pos[0]).to(DEV), ints(slot).to(DEV), table.to(DEV) if rot else None
     cache = S.KvCacheF8(*[c.to(DEV) for c in (k, k, s, s.clone())])
     q = S.rope_append(dq, Hq, cache, *args, **kw)
     x = qkv.reshape(M, -1, D)
